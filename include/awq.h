@@ -417,14 +417,105 @@ awq_status awq_w4a16_matmul(const void* X, int64_t M, int64_t ld_x, const int32_
                             int64_t ld_y, int32_t y_dtype, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Microscaled (MX) formats: a row is cut into blocks of 32 consecutive values
+ * that share one power of two.
+ *   AWQ_MX_FP8: e4m3 elements, one byte each (largest 448);
+ *   AWQ_MX_FP4: e2m1 elements (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives),
+ *               two to a byte, the even column in the low half.
+ *   codes:  contiguous [rows, cols] bytes (FP8) or [rows, cols / 2] bytes (FP4),
+ *           16-byte aligned;
+ *   scales: contiguous [rows, cols / 32] bytes b, each standing for 2^(b - 127)
+ *           (e8m0); 255 stands for NaN.  Any alignment.
+ * A block of values v, computed in fp32, is quantized as
+ *   e = floor(log2 max|v|) - emax, emax = 8 (FP8) or 2 (FP4), at least -127
+ *   element = v / 2^e rounded to nearest even, saturated at +-448 or +-6
+ * (an all-zero block has e = -127).  A block that holds a NaN or an infinity
+ * gets the scale 255 and zero elements.
+ * cols % 32 == 0 and rows * cols < 2^33 (AWQ_ESHAPE otherwise); rows = 0 or
+ * cols = 0 returns AWQ_OK at once.  16-bit inputs and outputs need the
+ * alignment of their elements only, and row strides (ld_*, in elements) >= cols
+ * of any parity.  No workspace; one launch each.
+ * ------------------------------------------------------------------------- */
+#define AWQ_MX_FP8 0
+#define AWQ_MX_FP4 1
+
+/* ---------------------------------------------------------------------------
+ * awq_mx_quantize -- v = x, or RN_fp32(x * s[col]) when s != NULL (the AWQ scale
+ * of the input channels, as awq_quantize_pack takes it), to codes and scales.
+ * X: fp16 or bf16 [rows, ld_x].  s: fp32 [cols] or NULL.
+ * ------------------------------------------------------------------------- */
+awq_status awq_mx_quantize(const void* X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld_x, const float* s,
+                           int32_t fmt, void* codes, uint8_t* scales, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * awq_mx_dequant -- the values a code stands for: element * 2^(b - 127), divided
+ * by s[col] (IEEE fp32) when s != NULL, rounded to out_dtype (fp16, bf16, fp32).
+ * NaN for a block whose scale is 255.  out: [rows, ld_out].
+ * ------------------------------------------------------------------------- */
+awq_status awq_mx_dequant(const void* codes, const uint8_t* scales, int32_t fmt, int64_t rows, int64_t cols,
+                          const float* s, void* out, int32_t out_dtype, int64_t ld_out, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * awq_rms_norm_mx -- root-mean-square norm, with the residual's addition when
+ * residual != NULL, and a quantized result.  norm is the norm's weight, for
+ * instance as folded by awq_norm_group_fold.
+ *   h = x + residual                          fp32, unrounded below
+ *   residual_out = RN(h)                      in x_dtype
+ *   v = h / sqrt(mean_col h^2 + eps) * norm   fp32 -> codes, scales
+ * X, residual, residual_out: fp16 or bf16 (x_dtype) [rows, ld_*]; residual and
+ * residual_out are both given or both NULL; residual_out may be residual or X
+ * itself (same row stride), else the buffers do not overlap.  norm: [cols] of
+ * norm_dtype (fp16, bf16 or fp32).  eps >= 0.  cols <= 65536 (AWQ_ESHAPE).
+ * A row's result depends on that row alone, not on how many there are.
+ * ------------------------------------------------------------------------- */
+awq_status awq_rms_norm_mx(const void* X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                           const void* residual, int64_t ld_r, const void* norm, int32_t norm_dtype, float eps,
+                           void* residual_out, int64_t ld_ro, int32_t fmt, void* codes, uint8_t* scales,
+                           hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * awq_silu_mul_mx -- the gated activation between the gate/up and the down
+ * linear, quantized: v = gate / (1 + exp(-gate)) * up, in fp32.
+ * gate, up: fp16 or bf16 (x_dtype) [rows, ld_g] and [rows, ld_u]; they may be
+ * the two halves of one gate/up result.
+ * ------------------------------------------------------------------------- */
+awq_status awq_silu_mul_mx(const void* gate, int64_t ld_g, const void* up, int64_t ld_u, int32_t x_dtype, int64_t rows,
+                           int64_t cols, int32_t fmt, void* codes, uint8_t* scales, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * awq_mx_matmul -- product of quantized activations with 4-bit weights:
+ *
+ *   Y[m, n] = sum_b 2^(a_scales[m, b] + w_scales[n, b] - 254)
+ *                   sum_{k in block b} a[m, k] * w[n, k]
+ *
+ * a_codes [M, K] of a_fmt (AWQ_MX_FP8 or AWQ_MX_FP4) and w_codes [N, K] of
+ * AWQ_MX_FP4, laid out as above.  Y: [M, ld_y] of y_dtype, ld_y >= N, aligned to
+ * its elements; AWQ_F16 or AWQ_BF16 (rounded to nearest even once), or AWQ_F32
+ * for a_fmt = AWQ_MX_FP4.  Products are exact and summed in fp32 by the matrix
+ * cores.  For 8-bit codes these align each 8 consecutive products to the
+ * largest of them and drop what lies more than 13 bits below it (measured: the
+ * result is within 1e-5 of its norm), which a 16-bit result does not show; an
+ * fp32 result with AWQ_MX_FP8 activations is therefore refused (AWQ_EDTYPE).
+ * A NaN scale makes every result of its row (a) or column (w) NaN; finite
+ * results past the range of y_dtype become infinite.
+ * M, N <= 2^26, K <= 2^22, K % 32 == 0 (AWQ_ESHAPE).  M = 0 or N = 0 returns
+ * AWQ_OK at once.  ws: awq_mx_matmul_workspace bytes (possibly 0; ws may then
+ * be NULL), 256-byte aligned.  Deterministic.
+ * ------------------------------------------------------------------------- */
+awq_status awq_mx_matmul_workspace(int32_t a_fmt, int64_t M, int64_t N, int64_t K, size_t* bytes /* [host] */);
+awq_status awq_mx_matmul(const void* a_codes, const uint8_t* a_scales, int32_t a_fmt, int64_t M, const void* w_codes,
+                         const uint8_t* w_scales, int64_t N, int64_t K, void* Y, int64_t ld_y, int32_t y_dtype,
+                         void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * awq_set_timing_events -- benchmark hook.  While set, every later call on
  * this host thread records `before` and `after` (hipEvent_t handles passed as
  * void*, created by the caller) on the call's stream immediately around its
  * main kernel launches: the partial-sum kernel of awq_act_stats; the search
  * kernel (weight score) or the chunked dW-build + GEMM launches (output score)
  * of awq_search_scales; the pack kernel of awq_quantize_pack; every launch of
- * awq_w4a16_matmul (GEMV or GEMM and, where used, the reduction).  Pass NULL,
- * NULL to clear.  The library records the events and nothing else.
+ * awq_w4a16_matmul (GEMV or GEMM and, where used, the reduction); every launch
+ * of the microscaled operators.  Pass NULL, NULL to clear.  The library records the events and nothing else.
  * ------------------------------------------------------------------------- */
 awq_status awq_set_timing_events(void* before, void* after);
 

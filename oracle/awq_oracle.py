@@ -566,3 +566,85 @@ def export_norm_group(W_members: Sequence[np.ndarray], s_members: Sequence[np.nd
 def export_rtn(W: np.ndarray, group_size: int):
     """Step 3: o_proj / down_proj at plain round-to-nearest (s = 1)."""
     return quantize_pack(W, None, group_size)
+
+
+# ---------------------------------------------------------------------------
+# Microscaled (MX) formats: blocks of 32 values sharing a power of two, elements
+# e4m3 ("fp8", largest 448) or e2m1 ("fp4", largest 6, two codes a byte, the even
+# column low).  Quantization is decided on fp32 values; sums are fp64.
+# ---------------------------------------------------------------------------
+MX_BLOCK = 32
+_MX = {"fp8": (3, -6, 8, 448.0), "fp4": (1, 0, 2, 6.0)}   # mantissa bits, smallest exponent, emax, largest
+
+
+def mx_element_table(fmt: str) -> np.ndarray:
+    """fp64 value of every code (256 or 16 of them); NaN for the e4m3 NaN codes."""
+    mbits, emin, _, _ = _MX[fmt]
+    half = 128 if fmt == "fp8" else 8
+    out = np.zeros(2 * half)
+    for c in range(half):
+        e, m = c >> mbits, c & ((1 << mbits) - 1)
+        out[c] = 2.0 ** (emin - mbits) * m if e == 0 else 2.0 ** (emin + e - 1) * (1 + m / (1 << mbits))
+    if fmt == "fp8":
+        out[127] = np.nan
+    out[half:] = -out[:half]
+    return out
+
+
+def _mx_encode(v: np.ndarray, fmt: str) -> np.ndarray:
+    """Codes of fp64 values: nearest element, ties to the even code, saturated."""
+    t = mx_element_table(fmt)
+    half = t.size // 2
+    mags = t[:half - 1] if fmt == "fp8" else t[:half]
+    a = np.minimum(np.abs(v), mags[-1])
+    hi = np.clip(np.searchsorted(mags, a, side="left"), 0, mags.size - 1)   # first element >= a
+    lo = np.maximum(hi - 1, 0)
+    dl, dh = a - mags[lo], mags[hi] - a                                      # exact in fp64
+    code = np.where((dh < dl) | ((dh == dl) & (hi % 2 == 0)), hi, lo)
+    return (code + half * np.signbit(v)).astype(np.uint8)
+
+
+def mx_quantize(v: np.ndarray, fmt: str):
+    """v [rows, cols] (fp32 or fp64 values): (codes uint8, scales uint8)."""
+    rows, cols = v.shape
+    _, _, emax, _ = _MX[fmt]
+    b = v.astype(np.float64).reshape(rows, cols // MX_BLOCK, MX_BLOCK)
+    with np.errstate(invalid="ignore"):
+        top = np.abs(b).max(axis=2)
+    bad = ~np.isfinite(top)
+    e = np.frexp(np.where(bad, 1.0, top))[1] - 1 - emax
+    e = np.where(top == 0, -127, np.maximum(e, -127))
+    x = np.where(bad[..., None], 0.0, b) / np.exp2(e.astype(np.float64))[..., None]
+    codes = _mx_encode(x, fmt).reshape(rows, cols)
+    if fmt == "fp4":
+        codes = codes[:, 0::2] | (codes[:, 1::2] << 4)
+    return codes, np.where(bad, 255, e + 127).astype(np.uint8)
+
+
+def mx_values(codes: np.ndarray, scales: np.ndarray, fmt: str) -> np.ndarray:
+    """fp64 values of codes and scales."""
+    if fmt == "fp4":
+        c = np.empty((codes.shape[0], 2 * codes.shape[1]), np.uint8)
+        c[:, 0::2], c[:, 1::2] = codes & 15, codes >> 4
+    else:
+        c = codes
+    unit = np.where(scales == 255, np.nan, np.exp2(scales.astype(np.float64) - 127))
+    return mx_element_table(fmt)[c] * np.repeat(unit, MX_BLOCK, axis=1)
+
+
+def mx_matmul(a_codes, a_scales, a_fmt, w_codes, w_scales) -> np.ndarray:
+    """fp64 A W^T, W in "fp4"."""
+    return mx_values(a_codes, a_scales, a_fmt) @ mx_values(w_codes, w_scales, "fp4").T
+
+
+def rms_norm(x: np.ndarray, weight: np.ndarray, eps: float, residual=None):
+    """(h, y) in fp64: h = x + residual, y = h / sqrt(mean h^2 + eps) * weight."""
+    h = x.astype(np.float64) + (0.0 if residual is None else residual.astype(np.float64))
+    return h, h / np.sqrt((h * h).mean(axis=1, keepdims=True) + eps) * weight.astype(np.float64)
+
+
+def silu_mul(gate: np.ndarray, up: np.ndarray) -> np.ndarray:
+    """fp64 gate / (1 + exp(-gate)) * up."""
+    g = gate.astype(np.float64)
+    with np.errstate(over="ignore"):
+        return g / (1.0 + np.exp(-g)) * up.astype(np.float64)

@@ -15,6 +15,11 @@ Entry points (same names as the C ABI):
 * ``search_scales``       alpha grid search, weight or output score, optional clip search
 * ``quantize_pack``       INT4 codes + fp16 scales in the AutoAWQ GEMM layout
 * ``unpack_dequant``      inverse of quantize_pack
+* ``mx_quantize``         microscaled 8-bit or 4-bit codes (blocks of 32, power-of-two scales)
+* ``mx_dequant``          inverse of mx_quantize
+* ``rms_norm_mx``         RMS norm with the residual's addition, microscaled result
+* ``silu_mul_mx``         SiLU gating, microscaled result
+* ``mx_matmul``           product of microscaled activations with 4-bit microscaled weights
 """
 from __future__ import annotations
 
@@ -31,6 +36,7 @@ LIB_PATH = os.path.join(_HERE, "libawq.so")
 AWQ_OK, AWQ_EINVAL, AWQ_ESHAPE, AWQ_EDTYPE, AWQ_EWORKSPACE, AWQ_EALIGN, AWQ_EHIP = range(7)
 AWQ_F16, AWQ_BF16, AWQ_F32 = 0, 1, 2
 AWQ_SCORE_WEIGHT, AWQ_SCORE_OUTPUT = 0, 1
+AWQ_MX_FP8, AWQ_MX_FP4 = 0, 1
 AWQ_FLAG_DUO = 1
 AWQ_FLAG_ASYM = 2
 AWQ_FLAG_OUT_DIRECT = 4
@@ -44,6 +50,8 @@ EXPORTED = ("awq_act_stats_workspace", "awq_act_stats", "awq_candidate_scales_wo
             "awq_unpack_dequant", "awq_norm_group_fold", "awq_weight_channel_mean_workspace",
             "awq_weight_channel_mean", "awq_candidate_scales_duo_workspace", "awq_candidate_scales_duo",
             "awq_w4a16_workspace", "awq_w4a16_matmul", "awq_search_scales_noalloc",
+            "awq_mx_quantize", "awq_mx_dequant", "awq_rms_norm_mx", "awq_silu_mul_mx", "awq_mx_matmul_workspace",
+            "awq_mx_matmul",
             "awq_last_error", "awq_abi_version", "awq_set_timing_events")
 
 
@@ -91,6 +99,12 @@ def _load() -> ctypes.CDLL:
         "awq_candidate_scales_duo": [P, P, I64, I32, F64, P, P, SZ, P],
         "awq_w4a16_workspace": [I64, I64, I64, PSZ],
         "awq_w4a16_matmul": [P, I64, I64, P, P, P, I64, I64, I32, P, I64, I32, P, SZ, P],
+        "awq_mx_quantize": [P, I32, I64, I64, I64, P, I32, P, P, P],
+        "awq_mx_dequant": [P, P, I32, I64, I64, P, P, I32, I64, P],
+        "awq_rms_norm_mx": [P, I32, I64, I64, I64, P, I64, P, I32, F32, P, I64, I32, P, P, P],
+        "awq_silu_mul_mx": [P, I64, P, I64, I32, I64, I64, I32, P, P, P],
+        "awq_mx_matmul_workspace": [I32, I64, I64, I64, PSZ],
+        "awq_mx_matmul": [P, P, I32, I64, P, P, I64, I64, P, I64, I32, P, SZ, P],
         "awq_set_timing_events": [P, P],
         "awq_search_scales_noalloc": [ctypes.POINTER(SearchCfg), ctypes.POINTER(WGroup), I64, P, P, P, P, P],
     }
@@ -587,6 +601,245 @@ def norm_group_fold(s_members: Sequence[torch.Tensor], norm: Optional[torch.Tens
     return FoldPlan(s_members, norm, out, s_shared, stream).run()
 
 
+# ---------------------------------------------------------------------------
+# Microscaled (MX) operators.  codes: float8_e4m3fn [rows, cols] ("fp8") or uint8
+# [rows, cols / 2] with two 4-bit codes a byte ("fp4"); scales: float8_e8m0fnu
+# [rows, cols / 32].  The plans run on the device that holds their tensors.
+# ---------------------------------------------------------------------------
+_MX_FMT = {"fp8": AWQ_MX_FP8, "fp4": AWQ_MX_FP4}
+_X16 = (torch.float16, torch.bfloat16)
+_FLOATS = {torch.float16: AWQ_F16, torch.bfloat16: AWQ_BF16, torch.float32: AWQ_F32}
+
+
+class _MxPrepared(_Prepared):
+    """A prepared call on the device of `like`: its current stream unless one is given, and that
+    device made current around the launch when it is not."""
+
+    def _place(self, like: torch.Tensor, stream) -> int:
+        self._device = like.device
+        return torch.cuda.current_stream(like.device).cuda_stream if stream is None else stream.cuda_stream
+
+    def launch(self) -> None:
+        if torch.cuda.current_device() == self._device.index:
+            _check(self._f(*self._args))
+        else:
+            with torch.cuda.device(self._device):
+                _check(self._f(*self._args))
+
+
+def _mx_fmt(fmt: str) -> int:
+    if fmt not in _MX_FMT:
+        raise ValueError(f"fmt {fmt!r} not in {sorted(_MX_FMT)}")
+    return _MX_FMT[fmt]
+
+
+def _mx_rows(t: torch.Tensor, name: str, dtype=_X16, shape=(None, None), like=None, optional=False) -> int:
+    """Checks a 2-D operand with unit column stride; returns its row stride (at least a row)."""
+    _tensor(t, name, dtype, shape, unit_col_stride=True, like=like, optional=optional)
+    if t is None:
+        return 0
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _mx_out(out, rows: int, cols: int, fmt: str, like: torch.Tensor):
+    """Checks the shape of a quantized result, and `out` if given."""
+    _mx_fmt(fmt)
+    if cols % 32:
+        raise ValueError(f"need columns in whole blocks of 32, got {cols}")
+    if out is not None:
+        codes, scales = out
+        if fmt == "fp8":
+            _tensor(codes, "codes", torch.float8_e4m3fn, (rows, cols), like=like)
+        else:
+            _tensor(codes, "codes", torch.uint8, (rows, cols // 2), like=like)
+        _tensor(scales, "scales", torch.float8_e8m0fnu, (rows, cols // 32), like=like)
+
+
+def _mx_empty(out, rows: int, cols: int, fmt: str, device):
+    if out is not None:
+        return tuple(out)
+    codes = (torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device) if fmt == "fp8" else
+             torch.empty((rows, cols // 2), dtype=torch.uint8, device=device))
+    return codes, torch.empty((rows, cols // 32), dtype=torch.float8_e8m0fnu, device=device)
+
+
+def _mx_operand(codes: torch.Tensor, scales: torch.Tensor, name: str, like=None):
+    """(fmt, rows, cols) of a quantized operand."""
+    _tensor(codes, f"{name}codes", (torch.float8_e4m3fn, torch.uint8), (None, None), like=like)
+    fmt = "fp8" if codes.dtype == torch.float8_e4m3fn else "fp4"
+    rows, cols = codes.shape[0], codes.shape[1] * (1 if fmt == "fp8" else 2)
+    if cols % 32:
+        raise ValueError(f"{name}codes: need columns in whole blocks of 32, got {cols}")
+    _tensor(scales, f"{name}scales", torch.float8_e8m0fnu, (rows, cols // 32), like=codes)
+    return fmt, rows, cols
+
+
+class MxQuantPlan(_MxPrepared):
+    """codes, scales of X [rows, cols] (fp16 or bf16, rows any stride apart), or of X * s."""
+    _fn = "awq_mx_quantize"
+
+    def __init__(self, X: torch.Tensor, fmt: str = "fp8", s: Optional[torch.Tensor] = None, out=None, stream=None):
+        ld = _mx_rows(X, "X")
+        rows, cols = X.shape
+        _tensor(s, "s", torch.float32, (cols,), like=X, optional=True)
+        _mx_out(out, rows, cols, fmt, X)
+        _dev(X, "X")
+        self.out = _mx_empty(out, rows, cols, fmt, X.device)
+        self._keep = (X, s)
+        self._bind(_ptr(X), _FLOATS[X.dtype], rows, cols, ld, _ptr(s), _mx_fmt(fmt), _ptr(self.out[0]),
+                   _ptr(self.out[1]), self._place(X, stream))
+
+    def run(self):
+        self.launch()
+        return self.out
+
+
+def mx_quantize(X: torch.Tensor, fmt: str = "fp8", s: Optional[torch.Tensor] = None, out=None, stream=None):
+    """Returns (codes, scales) of X, or of X * s (s fp32 [cols], the AWQ scale of the input channels):
+    blocks of 32 values sharing a power of two, elements e4m3 ("fp8") or e2m1 ("fp4")."""
+    return MxQuantPlan(X, fmt, s, out, stream).run()
+
+
+class MxDequantPlan(_MxPrepared):
+    """The values of codes and scales [rows, cols], divided by s if given."""
+    _fn = "awq_mx_dequant"
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, s: Optional[torch.Tensor] = None,
+                 out_dtype=torch.float32, out: Optional[torch.Tensor] = None, stream=None):
+        fmt, rows, cols = _mx_operand(codes, scales, "")
+        _tensor(s, "s", torch.float32, (cols,), like=codes, optional=True)
+        if out_dtype not in _FLOATS:
+            raise ValueError(f"out_dtype must be one of {list(_FLOATS)}, got {out_dtype}")
+        if out is not None:
+            _mx_rows(out, "out", tuple(_FLOATS), (rows, cols), like=codes)
+        _dev(codes, "codes")
+        self.out = torch.empty((rows, cols), dtype=out_dtype, device=codes.device) if out is None else out
+        ld = self.out.stride(0) if rows > 1 else max(self.out.stride(0), cols)
+        self._keep = (codes, scales, s)
+        self._bind(_ptr(codes), _ptr(scales), _MX_FMT[fmt], rows, cols, _ptr(s), _ptr(self.out),
+                   _FLOATS[self.out.dtype], ld, self._place(codes, stream))
+
+    def run(self) -> torch.Tensor:
+        self.launch()
+        return self.out
+
+
+def mx_dequant(codes: torch.Tensor, scales: torch.Tensor, s: Optional[torch.Tensor] = None, out_dtype=torch.float32,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values that codes and scales stand for (divided by s if given): inverse of mx_quantize."""
+    return MxDequantPlan(codes, scales, s, out_dtype, out, stream).run()
+
+
+class RmsNormMxPlan(_MxPrepared):
+    """h = X + residual; codes, scales of h / sqrt(mean h^2 + eps) * weight; residual_out = h in X's dtype.
+    residual_out may be residual or X itself."""
+    _fn = "awq_rms_norm_mx"
+
+    def __init__(self, X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                 residual: Optional[torch.Tensor] = None, fmt: str = "fp8",
+                 residual_out: Optional[torch.Tensor] = None, out=None, stream=None):
+        ld_x = _mx_rows(X, "X")
+        rows, cols = X.shape
+        _tensor(weight, "weight", tuple(_FLOATS), (cols,), like=X)
+        ld_r = _mx_rows(residual, "residual", X.dtype, (rows, cols), like=X, optional=True)
+        if residual is None and residual_out is not None:
+            raise ValueError("residual_out without residual")
+        ld_ro = _mx_rows(residual_out, "residual_out", X.dtype, (rows, cols), like=X, optional=True)
+        _mx_out(out, rows, cols, fmt, X)
+        _dev(X, "X")
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty((rows, cols), dtype=X.dtype, device=X.device)
+            ld_ro = cols
+        self.out = (*_mx_empty(out, rows, cols, fmt, X.device), residual_out)
+        self._keep = (X, weight, residual)
+        self._bind(_ptr(X), _FLOATS[X.dtype], rows, cols, ld_x, _ptr(residual), ld_r, _ptr(weight),
+                   _FLOATS[weight.dtype], eps, _ptr(residual_out), ld_ro, _mx_fmt(fmt), _ptr(self.out[0]),
+                   _ptr(self.out[1]), self._place(X, stream))
+
+    def run(self):
+        self.launch()
+        return self.out
+
+
+def rms_norm_mx(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+                fmt: str = "fp8", residual_out: Optional[torch.Tensor] = None, out=None, stream=None):
+    """Returns (codes, scales, residual_out): the RMS norm of h = X + residual, quantized, and h in X's
+    dtype (None without a residual)."""
+    return RmsNormMxPlan(X, weight, eps, residual, fmt, residual_out, out, stream).run()
+
+
+class SiluMulMxPlan(_MxPrepared):
+    """codes, scales of silu(gate) * up (fp16 or bf16 [rows, cols] each, rows any stride apart)."""
+    _fn = "awq_silu_mul_mx"
+
+    def __init__(self, gate: torch.Tensor, up: torch.Tensor, fmt: str = "fp8", out=None, stream=None):
+        ld_g = _mx_rows(gate, "gate")
+        rows, cols = gate.shape
+        ld_u = _mx_rows(up, "up", gate.dtype, (rows, cols), like=gate)
+        _mx_out(out, rows, cols, fmt, gate)
+        _dev(gate, "gate")
+        self.out = _mx_empty(out, rows, cols, fmt, gate.device)
+        self._keep = (gate, up)
+        self._bind(_ptr(gate), ld_g, _ptr(up), ld_u, _FLOATS[gate.dtype], rows, cols, _mx_fmt(fmt),
+                   _ptr(self.out[0]), _ptr(self.out[1]), self._place(gate, stream))
+
+    def run(self):
+        self.launch()
+        return self.out
+
+
+def silu_mul_mx(gate: torch.Tensor, up: torch.Tensor, fmt: str = "fp8", out=None, stream=None):
+    """Returns (codes, scales) of silu(gate) * up; gate and up may be the halves of one tensor's columns."""
+    return SiluMulMxPlan(gate, up, fmt, out, stream).run()
+
+
+def mx_matmul_workspace_bytes(fmt: str, M: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().awq_mx_matmul_workspace(_mx_fmt(fmt), M, N, K, ctypes.byref(n)))
+    return n.value
+
+
+class MxMatmulPlan(_MxPrepared):
+    """Y [M, N] = A [M, K] W [N, K]^T from quantized operands: A "fp8" or "fp4", W "fp4"."""
+    _fn = "awq_mx_matmul"
+
+    def __init__(self, a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                 out_dtype=torch.float16, out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                 stream=None):
+        fmt, M, K = _mx_operand(a_codes, a_scales, "a_")
+        w_fmt, N, Kw = _mx_operand(w_codes, w_scales, "w_", like=a_codes)
+        if w_fmt != "fp4":
+            raise ValueError("w_codes must hold 4-bit codes (uint8)")
+        if Kw != K:
+            raise ValueError(f"a_codes have {K} columns, w_codes {Kw}")
+        if out is not None:
+            _mx_rows(out, "out", tuple(_FLOATS), (M, N), like=a_codes)
+            out_dtype = out.dtype
+        if out_dtype not in _FLOATS:
+            raise ValueError(f"out_dtype must be one of {list(_FLOATS)}, got {out_dtype}")
+        _tensor(ws, "ws", torch.uint8, (None,), like=a_codes, optional=True)
+        _dev(a_codes, "a_codes")
+        need = mx_matmul_workspace_bytes(fmt, M, N, K)
+        self.ws = workspace(need, a_codes.device) if (ws is None or ws.numel() < need) else ws
+        self.out = torch.empty((M, N), dtype=out_dtype, device=a_codes.device) if out is None else out
+        ld = self.out.stride(0) if M > 1 else max(self.out.stride(0), N)
+        self._keep = (a_codes, a_scales, w_codes, w_scales)
+        self._bind(_ptr(a_codes), _ptr(a_scales), _MX_FMT[fmt], M, _ptr(w_codes), _ptr(w_scales), N, K,
+                   _ptr(self.out), ld, _FLOATS[self.out.dtype], _ptr(self.ws), self.ws.numel(),
+                   self._place(a_codes, stream))
+
+    def run(self) -> torch.Tensor:
+        self.launch()
+        return self.out
+
+
+def mx_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+              out_dtype=torch.float16, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y = A W^T of quantized A ("fp8" or "fp4" codes) and W ("fp4" codes), rounded once to out_dtype
+    (float16, bfloat16, or float32 for 4-bit A)."""
+    return MxMatmulPlan(a_codes, a_scales, w_codes, w_scales, out_dtype, out, stream=stream).run()
+
+
 def set_timing_events(before: Optional[int], after: Optional[int]) -> None:
     """Record raw hipEvent_t handles around the main kernel of every later call (None clears)."""
     _check(lib().awq_set_timing_events(before, after))
@@ -594,4 +847,6 @@ def set_timing_events(before: Optional[int], after: Optional[int]) -> None:
 
 __all__ = ["set_timing_events", "ActStatsPlan", "SearchPlan", "search_scales_noalloc", "PackPlan", "FoldPlan", "norm_group_fold",
            "weight_channel_mean", "candidate_scales_duo", "W4A16Plan", "w4a16_matmul", "AwqError", "act_stats", "candidate_scales", "search_scales", "quantize_pack", "unpack_dequant",
-           "search_workspace_bytes", "act_stats_workspace_bytes", "SearchResult", "lib", "LIB_PATH"]
+           "search_workspace_bytes", "act_stats_workspace_bytes", "SearchResult", "lib", "LIB_PATH",
+           "MxQuantPlan", "mx_quantize", "MxDequantPlan", "mx_dequant", "RmsNormMxPlan", "rms_norm_mx",
+           "SiluMulMxPlan", "silu_mul_mx", "MxMatmulPlan", "mx_matmul", "mx_matmul_workspace_bytes"]

@@ -750,4 +750,139 @@ awq_status awq_unpack_dequant(const int32_t* qweight, const uint16_t* scales, co
                     "awq_unpack_dequant");
 }
 
+// Shapes shared by the microscaled operators: whole blocks of 32, and fewer than
+// 2^33 values (the launches hold a lane index for 8 or more of them in 32 bits).
+static awq_status mx_shape(int32_t fmt, int64_t rows, int64_t cols) {
+  if (fmt != AWQ_MX_FP8 && fmt != AWQ_MX_FP4) return fail(AWQ_EDTYPE, "format %d: need AWQ_MX_FP8 or AWQ_MX_FP4", fmt);
+  if (rows < 0 || cols < 0) return fail(AWQ_EINVAL, "negative size");
+  if (cols % 32) return fail(AWQ_ESHAPE, "cols %lld not a multiple of 32", (long long)cols);
+  if (cols > 0 && rows >= ((int64_t)1 << 33) / cols)
+    return fail(AWQ_ESHAPE, "%lld x %lld: 2^33 values or more", (long long)rows, (long long)cols);
+  return ok();
+}
+static bool x16(int32_t dtype) { return dtype == AWQ_F16 || dtype == AWQ_BF16; }
+static bool any_float(int32_t dtype) { return x16(dtype) || dtype == AWQ_F32; }
+static bool misaligned(const void* p, int32_t dtype) { return ((uintptr_t)p & (dtype == AWQ_F32 ? 3u : 1u)) != 0; }
+
+awq_status awq_mx_quantize(const void* X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld_x, const float* s,
+                           int32_t fmt, void* codes, uint8_t* scales, hipStream_t stream) {
+  if (!x16(x_dtype)) return fail(AWQ_EDTYPE, "x_dtype %d: need AWQ_F16 or AWQ_BF16", x_dtype);
+  if (awq_status st = mx_shape(fmt, rows, cols)) return st;
+  if (rows == 0 || cols == 0) return ok();
+  if (ld_x < cols) return fail(AWQ_ESHAPE, "ld_x %lld < cols %lld", (long long)ld_x, (long long)cols);
+  if (!X || !codes || !scales) return fail(AWQ_EINVAL, "X / codes / scales is NULL");
+  if (misaligned(X, x_dtype) || misaligned(s, AWQ_F32)) return fail(AWQ_EALIGN, "X / s misaligned");
+  if (!aligned16(codes)) return fail(AWQ_EALIGN, "codes not 16-byte aligned");
+  mark(true, stream);
+  hipError_t e = launch_mx_quantize(X, x_dtype, rows, cols, ld_x, s, fmt, codes, scales, stream);
+  mark(false, stream);
+  return hip_status(e, "awq_mx_quantize");
+}
+
+awq_status awq_mx_dequant(const void* codes, const uint8_t* scales, int32_t fmt, int64_t rows, int64_t cols,
+                          const float* s, void* out, int32_t out_dtype, int64_t ld_out, hipStream_t stream) {
+  if (!any_float(out_dtype)) return fail(AWQ_EDTYPE, "out_dtype %d: need AWQ_F16, AWQ_BF16 or AWQ_F32", out_dtype);
+  if (awq_status st = mx_shape(fmt, rows, cols)) return st;
+  if (rows == 0 || cols == 0) return ok();
+  if (ld_out < cols) return fail(AWQ_ESHAPE, "ld_out %lld < cols %lld", (long long)ld_out, (long long)cols);
+  if (!codes || !scales || !out) return fail(AWQ_EINVAL, "codes / scales / out is NULL");
+  if (misaligned(out, out_dtype) || misaligned(s, AWQ_F32)) return fail(AWQ_EALIGN, "out / s misaligned");
+  if (!aligned16(codes)) return fail(AWQ_EALIGN, "codes not 16-byte aligned");
+  mark(true, stream);
+  hipError_t e = launch_mx_dequant(codes, scales, fmt, rows, cols, s, out, out_dtype, ld_out, stream);
+  mark(false, stream);
+  return hip_status(e, "awq_mx_dequant");
+}
+
+awq_status awq_rms_norm_mx(const void* X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                           const void* residual, int64_t ld_r, const void* norm, int32_t norm_dtype, float eps,
+                           void* residual_out, int64_t ld_ro, int32_t fmt, void* codes, uint8_t* scales,
+                           hipStream_t stream) {
+  if (!x16(x_dtype)) return fail(AWQ_EDTYPE, "x_dtype %d: need AWQ_F16 or AWQ_BF16", x_dtype);
+  if (!any_float(norm_dtype)) return fail(AWQ_EDTYPE, "norm_dtype %d: need AWQ_F16, AWQ_BF16 or AWQ_F32", norm_dtype);
+  if (awq_status st = mx_shape(fmt, rows, cols)) return st;
+  if (!(eps >= 0.0f)) return fail(AWQ_EINVAL, "eps %g is negative or NaN", (double)eps);
+  if ((residual == nullptr) != (residual_out == nullptr))
+    return fail(AWQ_EINVAL, "residual and residual_out go together");
+  if (rows == 0 || cols == 0) return ok();
+  if (cols > rms_norm_mx_max_cols())
+    return fail(AWQ_ESHAPE, "cols %lld > %lld", (long long)cols, (long long)rms_norm_mx_max_cols());
+  if (ld_x < cols) return fail(AWQ_ESHAPE, "ld_x %lld < cols %lld", (long long)ld_x, (long long)cols);
+  if (residual && (ld_r < cols || ld_ro < cols))
+    return fail(AWQ_ESHAPE, "ld_r %lld or ld_ro %lld < cols %lld", (long long)ld_r, (long long)ld_ro, (long long)cols);
+  if (!X || !norm || !codes || !scales) return fail(AWQ_EINVAL, "X / norm / codes / scales is NULL");
+  if (misaligned(X, x_dtype) || misaligned(residual, x_dtype) || misaligned(residual_out, x_dtype) ||
+      misaligned(norm, norm_dtype))
+    return fail(AWQ_EALIGN, "X / residual / residual_out / norm misaligned");
+  if (!aligned16(codes)) return fail(AWQ_EALIGN, "codes not 16-byte aligned");
+  mark(true, stream);
+  hipError_t e = launch_rms_norm_mx(X, x_dtype, rows, cols, ld_x, residual, ld_r, norm, norm_dtype, eps, residual_out,
+                                    ld_ro, fmt, codes, scales, stream);
+  mark(false, stream);
+  return hip_status(e, "awq_rms_norm_mx");
+}
+
+awq_status awq_silu_mul_mx(const void* gate, int64_t ld_g, const void* up, int64_t ld_u, int32_t x_dtype, int64_t rows,
+                           int64_t cols, int32_t fmt, void* codes, uint8_t* scales, hipStream_t stream) {
+  if (!x16(x_dtype)) return fail(AWQ_EDTYPE, "x_dtype %d: need AWQ_F16 or AWQ_BF16", x_dtype);
+  if (awq_status st = mx_shape(fmt, rows, cols)) return st;
+  if (rows == 0 || cols == 0) return ok();
+  if (ld_g < cols || ld_u < cols)
+    return fail(AWQ_ESHAPE, "ld_g %lld or ld_u %lld < cols %lld", (long long)ld_g, (long long)ld_u, (long long)cols);
+  if (!gate || !up || !codes || !scales) return fail(AWQ_EINVAL, "gate / up / codes / scales is NULL");
+  if (misaligned(gate, x_dtype) || misaligned(up, x_dtype)) return fail(AWQ_EALIGN, "gate / up misaligned");
+  if (!aligned16(codes)) return fail(AWQ_EALIGN, "codes not 16-byte aligned");
+  mark(true, stream);
+  hipError_t e = launch_silu_mul_mx(gate, ld_g, up, ld_u, x_dtype, rows, cols, fmt, codes, scales, stream);
+  mark(false, stream);
+  return hip_status(e, "awq_silu_mul_mx");
+}
+
+// Sizes of the product: rows fit the launches' 32-bit indices, and 256 rows of
+// codes a 32-bit offset.
+constexpr int64_t kMxMaxRows = (int64_t)1 << 26, kMxMaxK = (int64_t)1 << 22;
+
+static awq_status mx_matmul_shape(int32_t a_fmt, int64_t M, int64_t N, int64_t K) {
+  if (a_fmt != AWQ_MX_FP8 && a_fmt != AWQ_MX_FP4)
+    return fail(AWQ_EDTYPE, "a_fmt %d: need AWQ_MX_FP8 or AWQ_MX_FP4", a_fmt);
+  if (M < 0 || N < 0 || K < 0) return fail(AWQ_EINVAL, "negative size");
+  if (K % 32) return fail(AWQ_ESHAPE, "K %lld not a multiple of 32", (long long)K);
+  if (M > kMxMaxRows || N > kMxMaxRows || K > kMxMaxK)
+    return fail(AWQ_ESHAPE, "M %lld, N %lld or K %lld: need M, N <= 2^26 and K <= 2^22", (long long)M, (long long)N,
+                (long long)K);
+  return ok();
+}
+
+awq_status awq_mx_matmul_workspace(int32_t a_fmt, int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  if (!bytes) return fail(AWQ_EINVAL, "bytes is NULL");
+  if (awq_status st = mx_matmul_shape(a_fmt, M, N, K)) return st;
+  *bytes = (M == 0 || N == 0 || K == 0) ? 0 : align256(mx_matmul_workspace(a_fmt, M, N, K));
+  return ok();
+}
+
+awq_status awq_mx_matmul(const void* a_codes, const uint8_t* a_scales, int32_t a_fmt, int64_t M, const void* w_codes,
+                         const uint8_t* w_scales, int64_t N, int64_t K, void* Y, int64_t ld_y, int32_t y_dtype,
+                         void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (awq_status st = mx_matmul_shape(a_fmt, M, N, K)) return st;
+  if (!any_float(y_dtype)) return fail(AWQ_EDTYPE, "y_dtype %d: need AWQ_F16, AWQ_BF16 or AWQ_F32", y_dtype);
+  if (y_dtype == AWQ_F32 && a_fmt == AWQ_MX_FP8)
+    return fail(AWQ_EDTYPE, "an fp32 result needs AWQ_MX_FP4 activations: sums of 8-bit products are not fp32-exact");
+  if (M == 0 || N == 0) return ok();
+  if (K == 0) return fail(AWQ_ESHAPE, "K is 0 with M, N > 0");
+  if (ld_y < N) return fail(AWQ_ESHAPE, "ld_y %lld < N %lld", (long long)ld_y, (long long)N);
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !Y)
+    return fail(AWQ_EINVAL, "a_codes / a_scales / w_codes / w_scales / Y is NULL");
+  if (!aligned16(a_codes) || !aligned16(w_codes)) return fail(AWQ_EALIGN, "codes not 16-byte aligned");
+  if (misaligned(Y, y_dtype)) return fail(AWQ_EALIGN, "Y misaligned");
+  const size_t need = align256(mx_matmul_workspace(a_fmt, M, N, K));
+  if (need > 0) {
+    if (!ws || ws_bytes < need) return fail(AWQ_EWORKSPACE, "workspace %zu bytes < %zu", ws_bytes, need);
+    if ((uintptr_t)ws & 255u) return fail(AWQ_EALIGN, "ws not 256-byte aligned");
+  }
+  mark(true, stream);
+  hipError_t e = launch_mx_matmul(a_codes, a_scales, a_fmt, M, w_codes, w_scales, N, K, Y, ld_y, y_dtype, ws, stream);
+  mark(false, stream);
+  return hip_status(e, "awq_mx_matmul");
+}
+
 }  // extern "C"

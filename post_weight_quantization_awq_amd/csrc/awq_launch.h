@@ -145,4 +145,23 @@ int64_t duo_cand_blocks(int64_t d_in);
 hipError_t launch_candidates_duo(const float* x_mean, const float* w_mean, int64_t d_in, int n_grid, double s_min,
                                  double* T, double* ext, float* S, float* C2, hipStream_t stream);
 
+// Microscaled formats (mx_device.h); fmt kMxFp8 / kMxFp4, dtypes AWQ_F16 / AWQ_BF16 (/ AWQ_F32 where named).
+// codes and scales are contiguous: [rows, cols] or [rows, cols / 2] bytes, [rows, cols / 32] bytes
+hipError_t launch_mx_quantize(const void* X, int dt, int64_t rows, int64_t cols, int64_t ld, const float* s, int fmt,
+                              void* codes, uint8_t* scales, hipStream_t stream);
+// out: fp16, bf16 or fp32, row stride ld; s optional (the values are divided by it)
+hipError_t launch_mx_dequant(const void* codes, const uint8_t* scales, int fmt, int64_t rows, int64_t cols,
+                             const float* s, void* out, int out_dtype, int64_t ld, hipStream_t stream);
+hipError_t launch_silu_mul_mx(const void* gate, int64_t ld_g, const void* up, int64_t ld_u, int dt, int64_t rows,
+                              int64_t cols, int fmt, void* codes, uint8_t* scales, hipStream_t stream);
+// residual and residual_out may both be null; norm: fp16, bf16 or fp32 [cols]
+int64_t rms_norm_mx_max_cols();
+hipError_t launch_rms_norm_mx(const void* X, int dt, int64_t rows, int64_t cols, int64_t ld_x, const void* residual,
+                              int64_t ld_r, const void* norm, int norm_dtype, float eps, void* residual_out,
+                              int64_t ld_ro, int fmt, void* codes, uint8_t* scales, hipStream_t stream);
+// Y [M, N] (fp16, bf16 or fp32, row stride ld_y) = A [M, K] W [N, K]^T, W of kMxFp4
+size_t mx_matmul_workspace(int a_fmt, int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx_matmul(const void* A, const uint8_t* as, int a_fmt, int64_t M, const void* W, const uint8_t* ws,
+                            int64_t N, int64_t K, void* Y, int64_t ld_y, int y_dtype, void* work, hipStream_t stream);
+
 }  // namespace awq

@@ -1,0 +1,356 @@
+// Microscaled (MX) quantization, its inverse, and the two operators whose
+// result is quantized as it is formed: RMS norm with the residual's addition,
+// and SiLU gating.  All are bound by memory: each reads its inputs once and
+// writes codes and scales once, in one launch.
+//
+// A lane holds 8 consecutive values (16 bytes of input), so a block of 32 is
+// 4 neighbouring lanes and its maximum two lane permutations away.
+#include "awq_launch.h"
+#include "mx_device.h"
+
+namespace awq {
+
+// ---------------------------------------------------------------------------
+// quantize: v = x (or RN(x s[col])) -> codes, scales
+// silu-mul: v = g / (1 + e^-g) u    -> codes, scales
+// A block of 256 lanes takes 1024 consecutive chunks of 8 values, four a lane,
+// all loads ahead of the arithmetic.
+// ---------------------------------------------------------------------------
+constexpr int kEwThreads = 256, kEwUnroll = 4;
+
+// row and column chunk of chunk `base + off`, with base = r0 * cpr + c0
+struct ChunkPos {
+  int64_t row;
+  uint32_t col;
+};
+__device__ __forceinline__ ChunkPos chunk_pos(int64_t r0, uint32_t c0, uint32_t off, uint32_t cpr) {
+  const uint32_t c = c0 + off;
+  const uint32_t q = c / cpr;
+  return {r0 + q, c - q * cpr};
+}
+
+template <int DT, int FMT, bool SCALED>
+__global__ __launch_bounds__(kEwThreads) void mx_quantize_kernel(const uint16_t* __restrict__ X, int64_t n_chunks,
+                                                                 uint32_t cpr, int64_t ld, const float* __restrict__ s,
+                                                                 uint8_t* __restrict__ out,
+                                                                 uint8_t* __restrict__ scales) {
+  const int64_t base = (int64_t)blockIdx.x * (kEwThreads * kEwUnroll);
+  const int64_t r0 = base / cpr;
+  const uint32_t c0 = (uint32_t)(base - r0 * cpr);
+  uint4 x[kEwUnroll];
+  float sv[kEwUnroll][8];
+#pragma unroll
+  for (int u = 0; u < kEwUnroll; ++u) {
+    const uint32_t off = threadIdx.x + kEwThreads * u;
+    if (base + off < n_chunks) {
+      const ChunkPos p = chunk_pos(r0, c0, off, cpr);
+      x[u] = ld_any<uint4>(X + p.row * ld + 8 * (int64_t)p.col);
+      if constexpr (SCALED) {
+        *(float4*)&sv[u][0] = ld_any<float4>(s + 8 * (int64_t)p.col);
+        *(float4*)&sv[u][4] = ld_any<float4>(s + 8 * (int64_t)p.col + 4);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kEwUnroll; ++u) {
+    const int64_t chunk = base + threadIdx.x + kEwThreads * u;
+    if (chunk < n_chunks) {
+      float v[8];
+      unpack8<DT>(x[u], v);
+      if constexpr (SCALED) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= sv[u][j];
+      }
+      uint32_t codes[2];
+      const uint32_t byte = mx_quantize8<FMT>(v, codes);
+      mx_store8<FMT>(codes, byte, out, scales, chunk);
+    }
+  }
+}
+
+template <int DT, int FMT>
+__global__ __launch_bounds__(kEwThreads) void silu_mul_mx_kernel(const uint16_t* __restrict__ gate, int64_t ld_g,
+                                                                 const uint16_t* __restrict__ up, int64_t ld_u,
+                                                                 int64_t n_chunks, uint32_t cpr,
+                                                                 uint8_t* __restrict__ out,
+                                                                 uint8_t* __restrict__ scales) {
+  const int64_t base = (int64_t)blockIdx.x * (kEwThreads * kEwUnroll);
+  const int64_t r0 = base / cpr;
+  const uint32_t c0 = (uint32_t)(base - r0 * cpr);
+  uint4 g[kEwUnroll], w[kEwUnroll];
+#pragma unroll
+  for (int u = 0; u < kEwUnroll; ++u) {
+    const uint32_t off = threadIdx.x + kEwThreads * u;
+    if (base + off < n_chunks) {
+      const ChunkPos p = chunk_pos(r0, c0, off, cpr);
+      g[u] = ld_any<uint4>(gate + p.row * ld_g + 8 * (int64_t)p.col);
+      w[u] = ld_any<uint4>(up + p.row * ld_u + 8 * (int64_t)p.col);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kEwUnroll; ++u) {
+    const int64_t chunk = base + threadIdx.x + kEwThreads * u;
+    if (chunk < n_chunks) {
+      float v[8], b[8];
+      unpack8<DT>(g[u], v);
+      unpack8<DT>(w[u], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = v[j] / (1.0f + expf(-v[j])) * b[j];
+      uint32_t codes[2];
+      const uint32_t byte = mx_quantize8<FMT>(v, codes);
+      mx_store8<FMT>(codes, byte, out, scales, chunk);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dequant: out = RN(RN32(code 2^e / s[col])), s optional.  code 2^e is exact in
+// fp32 (unless it overflows); the quotient is rounded to fp32 and then to a
+// 16-bit output, as unpack_dequant does.
+// ---------------------------------------------------------------------------
+template <int FMT, int OT, bool SCALED>
+__global__ __launch_bounds__(kEwThreads) void mx_dequant_kernel(const uint8_t* __restrict__ codes,
+                                                                const uint8_t* __restrict__ scales, int64_t n_chunks,
+                                                                uint32_t cpr, const float* __restrict__ s,
+                                                                void* __restrict__ out, int64_t ld) {
+  const int64_t base = (int64_t)blockIdx.x * (kEwThreads * kEwUnroll);
+  const int64_t r0 = base / cpr;
+  const uint32_t c0 = (uint32_t)(base - r0 * cpr);
+  uint2 c[kEwUnroll];
+  uint32_t e[kEwUnroll];
+#pragma unroll
+  for (int u = 0; u < kEwUnroll; ++u) {
+    const int64_t chunk = base + threadIdx.x + kEwThreads * u;
+    if (chunk < n_chunks) {
+      if constexpr (FMT == kMxFp8) c[u] = *(const uint2*)(codes + 8 * chunk);
+      else c[u].x = *(const uint32_t*)(codes + 4 * chunk);
+      e[u] = scales[chunk >> 2];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kEwUnroll; ++u) {
+    const uint32_t off = threadIdx.x + kEwThreads * u;
+    if (base + off < n_chunks) {
+      const ChunkPos p = chunk_pos(r0, c0, off, cpr);
+      const float unit = mx_unit(e[u]);
+      float v[8];
+      f32x2v t;
+      if constexpr (FMT == kMxFp8) {
+        t = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[u].x, false), v[0] = t[0], v[1] = t[1];
+        t = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[u].x, true), v[2] = t[0], v[3] = t[1];
+        t = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[u].y, false), v[4] = t[0], v[5] = t[1];
+        t = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[u].y, true), v[6] = t[0], v[7] = t[1];
+      } else {
+        t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u].x, 1.0f, 0), v[0] = t[0], v[1] = t[1];
+        t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u].x, 1.0f, 1), v[2] = t[0], v[3] = t[1];
+        t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u].x, 1.0f, 2), v[4] = t[0], v[5] = t[1];
+        t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u].x, 1.0f, 3), v[6] = t[0], v[7] = t[1];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= unit;
+      if constexpr (SCALED) {
+        float sv[8];
+        *(float4*)&sv[0] = ld_any<float4>(s + 8 * (int64_t)p.col);
+        *(float4*)&sv[4] = ld_any<float4>(s + 8 * (int64_t)p.col + 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = v[j] / sv[j];
+      }
+      const int64_t at = p.row * ld + 8 * (int64_t)p.col;
+      if constexpr (OT == 2) {
+        st_any((float*)out + at, make_float4(v[0], v[1], v[2], v[3]));
+        st_any((float*)out + at + 4, make_float4(v[4], v[5], v[6], v[7]));
+      } else {
+        st_any((uint16_t*)out + at, pack8<OT>(v));
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// RMS norm: h = x + residual (fp32), residual_out = RN16(h),
+// y = h / sqrt(mean h^2 + eps) * weight -> codes, scales.  The mean is taken
+// over the unrounded fp32 h.  A row stays in registers between its sum of
+// squares and its scaling, so the inputs are read once.  Lanes of a row: GL
+// lanes of a wave (several rows a wave) up to 1024 columns, else a whole block
+// with one exchange of wave sums through LDS.  The split depends on the row
+// length alone: a row's result is the same in every batch.
+// ---------------------------------------------------------------------------
+struct NormArgs {
+  const uint16_t* X;
+  int64_t ld_x;
+  const uint16_t* R;  // may be null
+  int64_t ld_r;
+  uint16_t* RO;       // null with R
+  int64_t ld_ro;
+  const void* w;
+  int w_dtype;        // 0 fp16, 1 bf16, 2 fp32
+  float eps;
+  int64_t rows;
+  int64_t cols;
+  uint8_t* codes;
+  uint8_t* scales;
+};
+
+__device__ __forceinline__ void load_weight8(const void* w, int dt, int64_t col, float (&f)[8]) {
+  if (dt == 2) {
+    *(float4*)&f[0] = ld_any<float4>((const float*)w + col);
+    *(float4*)&f[4] = ld_any<float4>((const float*)w + col + 4);
+  } else {
+    const uint4 u = ld_any<uint4>((const uint16_t*)w + col);
+    if (dt == 0) unpack8<0>(u, f);
+    else unpack8<1>(u, f);
+  }
+}
+
+// GL = 0: the block holds one row (blockDim.x lanes); else GL lanes of a wave do
+template <int DT, int FMT, int GL, int CH>
+__global__ __launch_bounds__(GL ? 256 : 1024) void rms_norm_mx_kernel(const NormArgs a) {
+  const int lanes = GL ? GL : (int)blockDim.x;
+  const int lane = GL ? (int)threadIdx.x % (GL ? GL : 1) : (int)threadIdx.x;
+  const int64_t row = GL ? (int64_t)blockIdx.x * (256 / (GL ? GL : 1)) + (int)threadIdx.x / (GL ? GL : 1)
+                         : (int64_t)blockIdx.x;
+  const int cpr = (int)(a.cols / 8);
+  const bool live = row < a.rows;
+  float h[CH][8];
+  float sum = 0.0f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int k = lane + c * lanes;
+    if (live && k < cpr) {
+      unpack8<DT>(ld_any<uint4>(a.X + row * a.ld_x + 8 * k), h[c]);
+      if (a.R != nullptr) {
+        float r[8];
+        unpack8<DT>(ld_any<uint4>(a.R + row * a.ld_r + 8 * k), r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[c][j] += r[j];
+        st_any(a.RO + row * a.ld_ro + 8 * k, pack8<DT>(h[c]));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(h[c][j], h[c][j], sum);
+    }
+  }
+  if constexpr (GL != 0) {
+#pragma unroll
+    for (int m = GL / 2; m >= 1; m >>= 1) sum += __shfl_xor(sum, m, kWave);
+  } else {
+    __shared__ float part[16];
+    sum = wave_sum(sum);
+    const int wave = (int)threadIdx.x >> 6, nw = (int)blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) part[wave] = sum;
+    __syncthreads();
+    sum = 0.0f;
+    for (int i = 0; i < nw; ++i) sum += part[i];
+  }
+  const float r = 1.0f / sqrtf(sum / (float)a.cols + a.eps);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int k = lane + c * lanes;
+    if (live && k < cpr) {
+      float w[8];
+      load_weight8(a.w, a.w_dtype, 8 * (int64_t)k, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[c][j] = h[c][j] * r * w[j];
+      uint32_t codes[2];
+      const uint32_t byte = mx_quantize8<FMT>(h[c], codes);
+      mx_store8<FMT>(codes, byte, a.codes, a.scales, row * cpr + k);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+static unsigned ew_blocks(int64_t n_chunks) {
+  return (unsigned)((n_chunks + kEwThreads * kEwUnroll - 1) / (kEwThreads * kEwUnroll));
+}
+
+hipError_t launch_mx_quantize(const void* X, int dt, int64_t rows, int64_t cols, int64_t ld, const float* s, int fmt,
+                              void* codes, uint8_t* scales, hipStream_t stream) {
+  const int64_t n = rows * (cols / 8);
+  const unsigned g = ew_blocks(n);
+#define AWQ_MXQ(D, F, S)                                                                                          \
+  mx_quantize_kernel<D, F, S><<<g, kEwThreads, 0, stream>>>((const uint16_t*)X, n, (uint32_t)(cols / 8), ld, s, \
+                                                            (uint8_t*)codes, scales)
+#define AWQ_MXQ_S(D, F) \
+  if (s) AWQ_MXQ(D, F, true); else AWQ_MXQ(D, F, false)
+  if (dt == 0) {
+    if (fmt == kMxFp8) { AWQ_MXQ_S(0, kMxFp8); } else { AWQ_MXQ_S(0, kMxFp4); }
+  } else {
+    if (fmt == kMxFp8) { AWQ_MXQ_S(1, kMxFp8); } else { AWQ_MXQ_S(1, kMxFp4); }
+  }
+#undef AWQ_MXQ_S
+#undef AWQ_MXQ
+  return hipGetLastError();
+}
+
+hipError_t launch_silu_mul_mx(const void* gate, int64_t ld_g, const void* up, int64_t ld_u, int dt, int64_t rows,
+                              int64_t cols, int fmt, void* codes, uint8_t* scales, hipStream_t stream) {
+  const int64_t n = rows * (cols / 8);
+  const unsigned g = ew_blocks(n);
+#define AWQ_SILU(D, F)                                                                                         \
+  silu_mul_mx_kernel<D, F><<<g, kEwThreads, 0, stream>>>((const uint16_t*)gate, ld_g, (const uint16_t*)up, ld_u, n, \
+                                                         (uint32_t)(cols / 8), (uint8_t*)codes, scales)
+  if (dt == 0) {
+    if (fmt == kMxFp8) AWQ_SILU(0, kMxFp8); else AWQ_SILU(0, kMxFp4);
+  } else {
+    if (fmt == kMxFp8) AWQ_SILU(1, kMxFp8); else AWQ_SILU(1, kMxFp4);
+  }
+#undef AWQ_SILU
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_dequant(const void* codes, const uint8_t* scales, int fmt, int64_t rows, int64_t cols,
+                             const float* s, void* out, int out_dtype, int64_t ld, hipStream_t stream) {
+  const int64_t n = rows * (cols / 8);
+  const unsigned g = ew_blocks(n);
+#define AWQ_MXD(F, O, S)                                                                                            \
+  mx_dequant_kernel<F, O, S><<<g, kEwThreads, 0, stream>>>((const uint8_t*)codes, scales, n, (uint32_t)(cols / 8), s, \
+                                                           out, ld)
+#define AWQ_MXD_S(F, O) \
+  if (s) AWQ_MXD(F, O, true); else AWQ_MXD(F, O, false)
+#define AWQ_MXD_O(F)                       \
+  if (out_dtype == 0) { AWQ_MXD_S(F, 0); } \
+  else if (out_dtype == 1) { AWQ_MXD_S(F, 1); } \
+  else { AWQ_MXD_S(F, 2); }
+  if (fmt == kMxFp8) { AWQ_MXD_O(kMxFp8) } else { AWQ_MXD_O(kMxFp4) }
+#undef AWQ_MXD_O
+#undef AWQ_MXD_S
+#undef AWQ_MXD
+  return hipGetLastError();
+}
+
+int64_t rms_norm_mx_max_cols() { return 1024 * 8 * 8; }
+
+template <int DT, int FMT>
+static void rms_norm_launch(const NormArgs& a, hipStream_t stream) {
+  const int64_t cpr = a.cols / 8;
+#define AWQ_NORM_W(GL, CH) \
+  rms_norm_mx_kernel<DT, FMT, GL, CH><<<(unsigned)((a.rows + 256 / GL - 1) / (256 / GL)), 256, 0, stream>>>(a)
+#define AWQ_NORM_B(CH)                                                                                             \
+  rms_norm_mx_kernel<DT, FMT, 0, CH><<<(unsigned)a.rows, (unsigned)(((cpr + CH - 1) / CH + 63) / 64 * 64), 0, stream>>>( \
+      a)
+  if (cpr <= 16) AWQ_NORM_W(16, 1);
+  else if (cpr <= 32) AWQ_NORM_W(32, 1);
+  else if (cpr <= 64) AWQ_NORM_W(64, 1);
+  else if (cpr <= 128) AWQ_NORM_W(64, 2);
+  else if (cpr <= 1024) AWQ_NORM_B(2);
+  else if (cpr <= 4096) AWQ_NORM_B(4);
+  else AWQ_NORM_B(8);
+#undef AWQ_NORM_W
+#undef AWQ_NORM_B
+}
+
+hipError_t launch_rms_norm_mx(const void* X, int dt, int64_t rows, int64_t cols, int64_t ld_x, const void* residual,
+                              int64_t ld_r, const void* norm, int norm_dtype, float eps, void* residual_out,
+                              int64_t ld_ro, int fmt, void* codes, uint8_t* scales, hipStream_t stream) {
+  const NormArgs a = {(const uint16_t*)X, ld_x, (const uint16_t*)residual, ld_r, (uint16_t*)residual_out, ld_ro,
+                      norm, norm_dtype, eps, rows, cols, (uint8_t*)codes, scales};
+  if (dt == 0) {
+    if (fmt == kMxFp8) rms_norm_launch<0, kMxFp8>(a, stream); else rms_norm_launch<0, kMxFp4>(a, stream);
+  } else {
+    if (fmt == kMxFp8) rms_norm_launch<1, kMxFp8>(a, stream); else rms_norm_launch<1, kMxFp4>(a, stream);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace awq

@@ -1,0 +1,496 @@
+"""Microscaled operators against the fp64 oracle, on the GPU.
+
+Tolerances, from the arithmetic (u = 2^-24):
+* mx_quantize, mx_dequant, residual_out: every step is a single fp32 rounding or
+  exact, so results equal the oracle's bit for bit.
+* rms_norm_mx, silu_mul_mx: the fp32 value v is within d |v| of the exact one.
+  Norm: a lane adds at most 64 squares by fma, 6 lane exchanges and 16 waves
+  follow: 86 roundings of a sum of squares, halved by the root, then mean, eps,
+  root, quotient, two products and the residual's addition (whose rounding is
+  relative to h): d = 64 u.  SiLU: exp (2 ulp), sum, quotient, product: d = 8 u.
+  The element is then at most half a step of its format from v, or v saturates.
+* mx_matmul: B[m, n] = sum |a w|.  fp32 sums: K / 128 + 16 additions of at most
+  2 u B each.  8-bit activations: the matrix cores align each 8 consecutive
+  products to the largest of them and may drop what lies 13 bits below it, so
+  each of the 8 is off by at most 2^-13 of the largest: 2^-10 max|a| max|w| per 8.
+  The result's rounding adds half a step of its type.
+"""
+import numpy as np
+import pytest
+
+from oracle import awq_oracle as O
+from tests._util import say
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+STEP = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+@pytest.fixture(scope="module")
+def A():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import post_weight_quantization_awq_amd as A
+    A.lib()
+    return A
+
+
+def tdt(name):
+    import torch
+    return {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}[name]
+
+
+def values(rng, rows, cols, spread=1.0):
+    m = np.exp(spread * rng.standard_normal(cols))
+    return (rng.standard_normal((rows, cols)) * m).astype(np.float32)
+
+
+def to_dev(a, dtype, ld=None, offset=0):
+    """(device tensor [rows, cols] with row stride ld, `offset` elements into its buffer, and its fp32 values)."""
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(tdt(dtype))
+    rows, cols = t.shape
+    ld = ld or cols
+    buf = torch.full((offset + rows * ld + 16,), 3.0, dtype=t.dtype, device="cuda")
+    v = buf[offset:offset + rows * ld].view(rows, ld)[:, :cols]
+    v.copy_(t)
+    return v, t.float().numpy()
+
+
+def codes_np(c):
+    import torch
+    return c.view(torch.uint8).cpu().numpy()
+
+
+def quantized(out):
+    import torch
+    torch.cuda.synchronize()
+    return codes_np(out[0]), codes_np(out[1])
+
+
+def fmt_of(c):
+    import torch
+    return "fp8" if c.dtype == torch.float8_e4m3fn else "fp4"
+
+
+def random_mx(rng, rows, cols, fmt, A=None):
+    """Random operand: (codes, scales) arrays; values of a normal distribution, quantized by the oracle."""
+    return O.mx_quantize(values(rng, rows, cols, 0.5), fmt)
+
+
+def dev_mx(codes, scales, fmt):
+    import torch
+    c = torch.from_numpy(np.ascontiguousarray(codes)).cuda()
+    s = torch.from_numpy(np.ascontiguousarray(scales)).cuda().view(torch.float8_e8m0fnu)
+    return (c.view(torch.float8_e4m3fn) if fmt == "fp8" else c), s
+
+
+def check_near(out, fmt, y, d):
+    """Quantized `out` against exact values y, each known to the kernel within d |y|."""
+    codes, scales = quantized(out)
+    rows, cols = y.shape
+    emax, most, mbits, emin = {"fp8": (8, 448.0, 3, -6), "fp4": (2, 6.0, 1, 0)}[fmt]
+    top = np.abs(y).reshape(rows, -1, 32).max(axis=2)
+    es = [np.maximum(np.frexp(top * f)[1] - 1 - emax, -127) + 127 for f in (1 - d, 1 + d)]
+    es = [np.where(top == 0, 0, e) for e in es]
+    sc = scales.astype(np.int64)
+    assert np.all((sc == es[0]) | (sc == es[1])), "scale"
+    unit = np.repeat(np.exp2(sc - 127.0), 32, axis=1)
+    got = O.mx_values(codes, scales, fmt)
+    x = np.abs(y) / unit
+    step = np.exp2(np.maximum(np.floor(np.log2(np.maximum(np.minimum(x * (1 + d), most), 1e-30))), emin) - mbits)
+    want = np.sign(y) * np.minimum(x, most) * unit
+    assert np.all(np.abs(got - want) <= unit * step / 2 + d * np.abs(y)), "element"
+
+
+# ---- quantization and its inverse: bit for bit --------------------------------
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,cols,ld,offset,scaled", [
+    (1, 32, None, 0, False), (1, 4096, None, 0, True), (3, 96, 97, 1, False), (257, 160, 163, 3, True),
+    (130, 2080, None, 0, True), (1000, 1056, 1064, 8, False), (7, 12288, 24576, 0, False),
+])
+def test_quantize_bit_exact(A, fmt, dtype, rows, cols, ld, offset, scaled):
+    import torch
+    say(f"mx_quantize {fmt} {dtype} {rows}x{cols} ld {ld} offset {offset} scaled {scaled}")
+    rng = np.random.default_rng(rows * 7 + cols)
+    X, x = to_dev(values(rng, rows, cols), dtype, ld, offset)
+    s = np.exp(0.5 * rng.standard_normal(cols)).astype(np.float32) if scaled else None
+    out = A.mx_quantize(X, fmt, s=None if s is None else torch.from_numpy(s).cuda())
+    codes, scales = quantized(out)
+    ref = O.mx_quantize(x if s is None else x * s, fmt)     # fp32 product, rounded once
+    assert np.array_equal(scales, ref[1]) and np.array_equal(codes, ref[0])
+    for odt in ("f16", "bf16", "f32"):
+        back = A.mx_dequant(*out, s=None if s is None else torch.from_numpy(s).cuda(), out_dtype=tdt(odt))
+        v = O.mx_values(*ref, fmt).astype(np.float32)
+        v = v if s is None else v / s
+        want = torch.from_numpy(v).to(tdt(odt))
+        assert torch.equal(back.cpu(), want), odt
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_quantize_every_bf16(A, fmt):
+    """Every bf16 bit pattern as the largest value of a block, with its neighbours: NaN, infinities, subnormals,
+    ties, saturation; zero blocks."""
+    import torch
+    say(f"mx_quantize every bf16 {fmt}")
+    bits = torch.arange(65536, dtype=torch.int32)
+    x = torch.zeros((65536, 32), dtype=torch.int16)
+    for j in range(32):
+        x[:, j] = (bits - 61 * j).clamp(min=0).where(bits < 32768, (bits - 61 * j).clamp(min=32768)).to(torch.int16)
+    X = x.view(torch.bfloat16).cuda()
+    out = A.mx_quantize(X, fmt)
+    codes, scales = quantized(out)
+    with np.errstate(invalid="ignore"):
+        ref = O.mx_quantize(X.float().cpu().numpy(), fmt)
+    assert np.array_equal(scales, ref[1]) and np.array_equal(codes, ref[0])
+    back = A.mx_dequant(*out).cpu().numpy()
+    assert np.array_equal(back, O.mx_values(*ref, fmt).astype(np.float32), equal_nan=True)
+
+
+def test_quantize_zero_infinite_and_nan_blocks(A):
+    import torch
+    say("mx_quantize special blocks")
+    X = torch.zeros((5, 128), dtype=torch.float16, device="cuda")
+    X[1, 5], X[2, 40], X[3, 127] = float("nan"), float("inf"), float("-inf")
+    X[4] = 65504
+    for fmt in ("fp8", "fp4"):
+        codes, scales = quantized(A.mx_quantize(X, fmt))
+        ref = O.mx_quantize(X.float().cpu().numpy(), fmt)
+        assert np.array_equal(scales, ref[1]) and np.array_equal(codes, ref[0])
+
+
+def test_dequant_into_strided_rows(A):
+    import torch
+    say("mx_dequant strided")
+    rng = np.random.default_rng(5)
+    c, s = random_mx(rng, 9, 96, "fp4")
+    for odt in ("f16", "f32"):
+        buf = torch.full((9 * 101 + 3,), 5.0, dtype=tdt(odt), device="cuda")
+        out = buf[3:].view(9, 101)[:, 1:97]
+        A.mx_dequant(*dev_mx(c, s, "fp4"), out=out)
+        want = O.mx_values(c, s, "fp4").astype(np.float32)
+        assert np.array_equal(out.float().cpu().numpy(), want.astype(np.float16 if odt == "f16" else np.float32))
+        rest = buf.cpu()
+        assert rest[:3].eq(5).all() and rest[3:].view(9, 101)[:, 97:].eq(5).all() and \
+            rest[3:].view(9, 101)[:, :1].eq(5).all()
+
+
+def test_quantize_offsets_past_32_bits(A):
+    """A matrix of more than 4 GiB: its last rows."""
+    import torch
+    say("mx_quantize past 4 GiB")
+    rows, cols = 1 << 20, 2080
+    X = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(1)
+    tail, x = to_dev(values(rng, 5, cols), "bf16")
+    X[-5:] = tail
+    codes, scales = A.mx_quantize(X, "fp8")
+    assert not codes[:-5].view(torch.uint8).any() and not scales[:-5].view(torch.uint8).any()
+    ref = O.mx_quantize(x, "fp8")
+    assert np.array_equal(codes_np(codes[-5:]), ref[0]) and np.array_equal(codes_np(scales[-5:]), ref[1])
+    back = A.mx_dequant(codes, scales, out_dtype=torch.bfloat16)
+    assert np.array_equal(back[-5:].float().cpu().numpy(), O.mx_values(*ref, "fp8").astype(np.float32))
+    assert not back[:-5].any()
+
+
+# ---- RMS norm -------------------------------------------------------------------
+@pytest.mark.parametrize("rows,cols,dtype,wdtype,residual,fmt,ld,offset", [
+    (1, 32, "f16", "f16", True, "fp8", None, 0), (5, 96, "bf16", "f32", False, "fp8", 99, 1),
+    (67, 128, "bf16", "bf16", True, "fp4", None, 0), (33, 160, "f16", "f32", True, "fp8", None, 0),
+    (19, 512, "f16", "bf16", True, "fp8", 517, 5), (9, 1024, "bf16", "bf16", True, "fp8", None, 0),
+    (1, 4096, "bf16", "bf16", True, "fp8", None, 0), (130, 4096, "f16", "f16", False, "fp4", 4104, 0),
+    (21, 2080, "bf16", "f32", True, "fp8", 2081, 3), (3, 8192, "f16", "f16", True, "fp8", None, 0),
+    (3, 8224, "bf16", "bf16", True, "fp8", None, 0), (2, 32768, "bf16", "f32", True, "fp8", None, 0),
+    (2, 65536, "f16", "f16", False, "fp4", None, 0),
+])
+def test_rms_norm(A, rows, cols, dtype, wdtype, residual, fmt, ld, offset):
+    import torch
+    say(f"rms_norm_mx {rows}x{cols} {dtype} w {wdtype} residual {residual} {fmt} ld {ld}")
+    rng = np.random.default_rng(rows + cols)
+    X, x = to_dev(values(rng, rows, cols), dtype, ld, offset)
+    W, w = to_dev(1 + 0.2 * rng.standard_normal((1, cols)), wdtype)
+    R, r = to_dev(2 * values(rng, rows, cols), dtype, ld, offset) if residual else (None, None)
+    before = X.clone()
+    out = A.rms_norm_mx(X, W[0].contiguous(), 1e-5, residual=R, fmt=fmt)
+    _, y = O.rms_norm(x, w[0], 1e-5, r)
+    check_near(out, fmt, y, 64 * U)
+    assert torch.equal(X, before)
+    if residual:
+        assert torch.equal(out[2].cpu(), torch.from_numpy(x + r).to(tdt(dtype)))
+    else:
+        assert out[2] is None
+
+
+def test_rms_norm_in_place_and_batch_independent(A):
+    import torch
+    say("rms_norm_mx in place, per-row results")
+    rng = np.random.default_rng(3)
+    X, _ = to_dev(values(rng, 37, 4096), "bf16")
+    R, _ = to_dev(values(rng, 37, 4096), "bf16")
+    w = torch.ones(4096, device="cuda")
+    ref = A.rms_norm_mx(X, w, residual=R)
+    one = [A.rms_norm_mx(X[i:i + 1], w, residual=R[i:i + 1]) for i in (0, 17, 36)]
+    for i, o in zip((0, 17, 36), one):
+        for a, b in zip(o, ref):
+            assert torch.equal(a.view(torch.uint8), b[i:i + 1].view(torch.uint8))
+    for which in ("residual", "x"):
+        X2, R2 = X.clone(), R.clone()
+        got = A.rms_norm_mx(X2, w, residual=R2, residual_out=R2 if which == "residual" else X2)
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, ref))
+
+
+def test_rms_norm_bad_rows_stay_alone(A):
+    """A row with a NaN or an infinity is NaN; a row of zeros is zero; the others are as without them."""
+    import torch
+    say("rms_norm_mx bad rows")
+    rng = np.random.default_rng(4)
+    X, _ = to_dev(values(rng, 6, 160), "f16")
+    w = torch.ones(160, device="cuda")
+    ref = A.mx_dequant(*A.rms_norm_mx(X, w)[:2])
+    X[1, 7], X[3, 0] = float("nan"), float("inf")
+    X[4] = 0
+    got = A.mx_dequant(*A.rms_norm_mx(X, w)[:2])
+    assert got[1].isnan().all()
+    assert got[3, :32].isnan().all() and not got[3, 32:].any()   # x / inf is 0, inf / inf NaN
+    assert not got[4].any()
+    assert torch.equal(got[[0, 2, 5]], ref[[0, 2, 5]])
+
+
+# ---- SiLU gating ----------------------------------------------------------------
+@pytest.mark.parametrize("rows,cols,dtype,fmt,fused", [
+    (1, 32, "f16", "fp8", False), (4, 12288, "bf16", "fp8", True), (57, 96, "f16", "fp4", True),
+    (333, 2080, "bf16", "fp8", True), (64, 4096, "f16", "fp8", False),
+])
+def test_silu_mul(A, rows, cols, dtype, fmt, fused):
+    say(f"silu_mul_mx {rows}x{cols} {dtype} {fmt} fused {fused}")
+    rng = np.random.default_rng(rows + cols)
+    if fused:
+        GU, gu = to_dev(3 * rng.standard_normal((rows, 2 * cols)), dtype)
+        G, Up, g, up = GU[:, :cols], GU[:, cols:], gu[:, :cols], gu[:, cols:]
+    else:
+        (G, g), (Up, up) = (to_dev(3 * rng.standard_normal((rows, cols)), dtype, cols + 5, 3) for _ in range(2))
+    check_near(A.silu_mul_mx(G, Up, fmt), fmt, O.silu_mul(g, up), 8 * U)
+
+
+def test_silu_mul_far_gates(A):
+    """Gates where exp overflows or vanishes."""
+    import torch
+    say("silu_mul_mx far gates")
+    g = np.zeros((1, 64), np.float32)
+    g[0, :8] = [-87, -88.5, -104, -3e4, 87, 104, 3e4, -20]
+    g[0, 32:] = -200            # a block that vanishes
+    G, gv = to_dev(g, "bf16")
+    Up, uv = to_dev(np.full((1, 64), 2.0), "bf16")
+    y = O.silu_mul(gv, uv)
+    y[np.abs(y) < 2.0 ** -126] = 0.0
+    out = A.silu_mul_mx(G, Up, "fp8")
+    got = O.mx_values(*quantized(out), "fp8")
+    assert np.all(np.abs(got - y) <= np.maximum(np.abs(y) / 16, np.abs(y).max() / 448 * 2.0 ** -9))
+    assert not got[0, 32:].any()
+    G[0, 3] = float("nan")
+    assert A.mx_dequant(*A.silu_mul_mx(G, Up))[0, :32].isnan().all()
+
+
+# ---- the product ----------------------------------------------------------------
+def product_tol(a, w, K, fmt, y, dtype, bound_terms=None):
+    B = np.abs(a) @ np.abs(w).T
+    tol = (K // 128 + 16) * 2 * U * B
+    if fmt == "fp8":
+        m8 = lambda v: np.abs(v).reshape(v.shape[0], -1, 8).max(axis=2)
+        tol += 2.0 ** -10 * (m8(a) @ m8(w).T)
+    small = {"f16": 2.0 ** -25, "bf16": 0.0, "f32": 0.0}[dtype]     # half a subnormal step of fp16
+    return tol + STEP[dtype] * (np.abs(y) + tol) + small
+
+
+def check_product(A, M, N, K, fmt, dtype, seed=0, ld_y=None):
+    import torch
+    rng = np.random.default_rng(seed + M + 3 * N + 7 * K)
+    ac, asc = random_mx(rng, M, K, fmt)
+    wc, wsc = random_mx(rng, N, K, "fp4")
+    a, w = O.mx_values(ac, asc, fmt), O.mx_values(wc, wsc, "fp4")
+    out = None
+    if ld_y is not None:
+        buf = torch.full((M * ld_y + 1,), 7.0, dtype=tdt(dtype), device="cuda")
+        out = buf[1:].view(M, ld_y)[:, :N]
+    Y = A.mx_matmul(*dev_mx(ac, asc, fmt), *dev_mx(wc, wsc, "fp4"), out_dtype=tdt(dtype), out=out)
+    torch.cuda.synchronize()
+    y = a @ w.T
+    err = np.abs(Y.double().cpu().numpy() - y)
+    tol = product_tol(a, w, K, fmt, y, dtype)
+    assert np.all(err <= tol), (float((err / tol).max()), np.argwhere(err > tol)[:4].tolist())
+    if ld_y is not None:
+        assert buf[0] == 7 and buf[1:].view(M, ld_y)[:, N:].eq(7).all()
+    return Y
+
+
+@pytest.mark.parametrize("fmt,dtype", [("fp8", "f16"), ("fp8", "bf16"), ("fp4", "f32"), ("fp4", "f16")])
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 32, 33, 64, 65, 127, 129, 200, 257])
+def test_product_rows(A, M, fmt, dtype):
+    say(f"mx_matmul M {M} {fmt} {dtype}")
+    check_product(A, M, 272, 416, fmt, dtype)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("K", [32, 64, 96, 128, 160, 256, 288, 384, 512, 544, 640, 1056, 2080])
+def test_product_lengths(A, M, K, fmt):
+    say(f"mx_matmul M {M} K {K} {fmt}")
+    check_product(A, M, 72, K, fmt, "f16")
+
+
+@pytest.mark.parametrize("fmt,dtype", [("fp8", "bf16"), ("fp4", "f32")])
+@pytest.mark.parametrize("M,N,ld_y", [(1, 1, None), (5, 7, 9), (30, 17, 17), (70, 255, 257), (260, 1000, 1003),
+                                      (513, 129, 131), (300, 513, 520)])
+def test_product_odd_outputs(A, M, N, ld_y, fmt, dtype):
+    say(f"mx_matmul {M}x{N} ld_y {ld_y} {fmt} {dtype}")
+    check_product(A, M, N, 288, fmt, dtype, ld_y=ld_y)
+
+
+@pytest.mark.parametrize("M,N,K,fmt,dtype", [
+    (1, 24576, 4096, "fp8", "f16"), (24, 4096, 12288, "fp8", "bf16"), (1, 1024, 4096, "fp4", "f32"),
+    (512, 1024, 4096, "fp8", "f16"), (1024, 2048, 4096, "fp4", "bf16"), (2048, 512, 2080, "fp8", "bf16"),
+    (333, 1000, 2080, "fp4", "f32"), (96, 4096, 4096, "fp8", "f16"),
+])
+def test_product_sizes(A, M, N, K, fmt, dtype):
+    say(f"mx_matmul {M}x{N}x{K} {fmt} {dtype}")
+    check_product(A, M, N, K, fmt, dtype)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("M", [4, 50, 300])
+def test_product_nan_scales_stay_in_their_row_and_column(A, M, fmt):
+    import torch
+    say(f"mx_matmul NaN scales M {M} {fmt}")
+    rng = np.random.default_rng(M)
+    N, K = 300, 224
+    ac, asc = random_mx(rng, M, K, fmt)
+    wc, wsc = random_mx(rng, N, K, "fp4")
+    ref = A.mx_matmul(*dev_mx(ac, asc, fmt), *dev_mx(wc, wsc, "fp4"))
+    asc[M - 1, 6], wsc[17, 0] = 255, 255
+    ac[M - 1, -8:] = 0
+    Y = A.mx_matmul(*dev_mx(ac, asc, fmt), *dev_mx(wc, wsc, "fp4"))
+    assert Y[M - 1].isnan().all() and Y[:, 17].isnan().all()
+    keep = [i for i in range(N) if i != 17]
+    assert torch.equal(Y[:M - 1, keep], ref[:M - 1, keep])
+
+
+@pytest.mark.parametrize("M", [2, 80, 400])
+def test_product_extreme_scales(A, M):
+    """Scales at the ends of their range: vanishing blocks, and results past fp16's range."""
+    import torch
+    say(f"mx_matmul extreme scales M {M}")
+    rng = np.random.default_rng(M)
+    ac, asc = random_mx(rng, M, 160, "fp4")
+    wc, wsc = random_mx(rng, 40, 160, "fp4")
+    asc[:, 1], wsc[:, 1] = 0, 0                  # 2^-254: contributes nothing
+    asc[0], wsc[0] = 200, 127
+    a, w = O.mx_values(ac, asc, "fp4"), O.mx_values(wc, wsc, "fp4")
+    Y = A.mx_matmul(*dev_mx(ac, asc, "fp4"), *dev_mx(wc, wsc, "fp4"), out_dtype=torch.float32).double().cpu().numpy()
+    y = a @ w.T
+    assert np.all(np.abs(Y - y) <= product_tol(a, w, 160, "fp4", y, "f32"))
+    Y16 = A.mx_matmul(*dev_mx(ac, asc, "fp4"), *dev_mx(wc, wsc, "fp4"))
+    big = np.abs(y) > 65600
+    assert big.any() and bool(Y16.cpu()[torch.from_numpy(big)].isinf().all())
+
+
+def test_empty_calls(A):
+    import torch
+    say("mx empty calls")
+    X = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda")
+    c, s = A.mx_quantize(X)
+    assert c.shape == (0, 64) and s.shape == (0, 2)
+    assert A.mx_dequant(c, s).shape == (0, 64)
+    assert A.rms_norm_mx(X, torch.ones(64, device="cuda"), residual=X)[2].shape == (0, 64)
+    w = A.mx_quantize(torch.zeros((5, 64), dtype=torch.bfloat16, device="cuda"), "fp4")
+    assert A.mx_matmul(c, s, *w).shape == (0, 5)
+    with pytest.raises(A.AwqError, match="fp32 result"):
+        A.mx_matmul(*A.mx_quantize(torch.zeros((5, 64), dtype=torch.bfloat16, device="cuda")), *w,
+                    out_dtype=torch.float32)
+
+
+# ---- together ---------------------------------------------------------------------
+def mlp(A, x, res, norm, wgu, wd, F, stream=None):
+    """One block's MLP on 4-bit weights: norm, gate/up, gating, down."""
+    ac, asc, h = A.rms_norm_mx(x, norm, 1e-6, residual=res, stream=stream)
+    gu = A.mx_matmul(ac, asc, *wgu, out_dtype=x.dtype, stream=stream)
+    dc, dsc = A.silu_mul_mx(gu[:, :F], gu[:, F:], stream=stream)
+    return A.mx_matmul(dc, dsc, *wd, out_dtype=x.dtype, stream=stream), h
+
+
+@pytest.mark.parametrize("T", [1, 19, 150])
+def test_mlp_block(A, T):
+    """The operators one after the other, each checked against the oracle on the kernel's own inputs."""
+    import torch
+    say(f"mx mlp T {T}")
+    D, F = 416, 544
+    rng = np.random.default_rng(T)
+    X, x = to_dev(values(rng, T, D, 0.5), "bf16")
+    R, r = to_dev(values(rng, T, D, 0.5), "bf16")
+    Wg, _ = to_dev(0.05 * rng.standard_normal((2 * F, D)), "f16")
+    Wd, _ = to_dev(0.05 * rng.standard_normal((D, F)), "f16")
+    s = torch.from_numpy(np.exp(0.3 * rng.standard_normal(D)).astype(np.float32)).cuda()
+    norm = torch.ones(D, device="cuda") / s                     # the scale folded into the norm
+    wgu, wd = A.mx_quantize(Wg, "fp4", s=s), A.mx_quantize(Wd, "fp4")
+    ac, asc, h = A.rms_norm_mx(X, norm, 1e-6, residual=R)
+    check_near((ac, asc), "fp8", O.rms_norm(x, norm.cpu().numpy(), 1e-6, r)[1], 64 * U)
+    gu = A.mx_matmul(ac, asc, *wgu, out_dtype=torch.bfloat16)
+    a, w = O.mx_values(*quantized((ac, asc)), "fp8"), O.mx_values(*quantized(wgu), "fp4")
+    y = a @ w.T
+    assert np.all(np.abs(gu.double().cpu().numpy() - y) <= product_tol(a, w, D, "fp8", y, "bf16"))
+    dc, dsc = A.silu_mul_mx(gu[:, :F], gu[:, F:])
+    g = gu.double().cpu().numpy()
+    check_near((dc, dsc), "fp8", O.silu_mul(g[:, :F], g[:, F:]), 8 * U)
+    Y = A.mx_matmul(dc, dsc, *wd, out_dtype=torch.bfloat16)
+    a, w = O.mx_values(*quantized((dc, dsc)), "fp8"), O.mx_values(*quantized(wd), "fp4")
+    y = a @ w.T
+    assert np.all(np.abs(Y.double().cpu().numpy() - y) <= product_tol(a, w, F, "fp8", y, "bf16"))
+    # the same in one go, and on another stream
+    Y2, h2 = mlp(A, X, R, norm, wgu, wd, F)
+    assert torch.equal(Y, Y2) and torch.equal(h, h2)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    Y3, _ = mlp(A, X, R, norm, wgu, wd, F, stream=st)
+    st.synchronize()
+    assert torch.equal(Y, Y3)
+
+
+@pytest.mark.parametrize("T", [1, 150])
+def test_mlp_captured_and_replayed(A, T):
+    """The chain in a captured graph, replayed on new inputs between eager calls."""
+    import torch
+    say(f"mx mlp captured T {T}")
+    D, F = 416, 544
+    rng = np.random.default_rng(T + 1)
+    X, _ = to_dev(values(rng, T, D, 0.5), "f16")
+    R, _ = to_dev(values(rng, T, D, 0.5), "f16")
+    wgu = A.mx_quantize(to_dev(0.05 * rng.standard_normal((2 * F, D)), "f16")[0], "fp4")
+    wd = A.mx_quantize(to_dev(0.05 * rng.standard_normal((D, F)), "f16")[0], "fp4")
+    norm = torch.ones(D, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        Y, h = mlp(A, X, R, norm, wgu, wd, F)
+    for i in range(4):
+        X.copy_(to_dev(values(np.random.default_rng(50 + i), T, D, 0.5), "f16")[0])
+        g.replay()
+        torch.cuda.synchronize()
+        ref, href = mlp(A, X, R, norm, wgu, wd, F)
+        assert torch.equal(Y, ref) and torch.equal(h, href)
+
+
+def test_product_two_streams(A):
+    """Two products at once on two streams, each with its own workspace and result."""
+    import torch
+    say("mx_matmul two streams")
+    rng = np.random.default_rng(8)
+    ops = [(dev_mx(*random_mx(rng, 140, 1024, "fp8"), "fp8"), dev_mx(*random_mx(rng, 520, 1024, "fp4"), "fp4"))
+           for _ in range(2)]
+    ref = [A.mx_matmul(*a, *w) for a, w in ops]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ops]
+    plans = [A.MxMatmulPlan(*a, *w, stream=s) for (a, w), s in zip(ops, streams)]
+    for _ in range(5):
+        got = [p.run() for p in plans]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
