@@ -54,10 +54,11 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_few_kernel(const uint8_t
   f32x4 acc[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) acc[t] = (f32x4){0, 0, 0, 0};
-  const uint4 zero = make_uint4(0, 0, 0, 0);
   for (int64_t b0 = 4 * wave; b0 < kb; b0 += 4 * kFewWaves) {
     const bool in = b0 + h < kb;
-    const i32x8 w = lo4(in ? *(const uint4*)(wr + 16 * (b0 + h)) : zero);
+    uint4 wv = make_uint4(0, 0, 0, 0);
+    if (in) wv = *(const uint4*)(wr + 16 * (b0 + h));
+    const i32x8 w = lo4(wv);
     const int sw = in ? wsr[b0 + h] : 0;
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
@@ -66,10 +67,14 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_few_kernel(const uint8_t
       i32x8 a;
       if constexpr (AF == kMxFp8) {
         const uint8_t* p = A + m * K + 32 * b0 + 16 * h;
-        const bool in0 = b0 + h / 2 < kb, in1 = b0 + 2 + h / 2 < kb;
-        a = both4(in0 ? *(const uint4*)p : zero, in1 ? *(const uint4*)(p + 64) : zero);
+        uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+        if (b0 + h / 2 < kb) v0 = *(const uint4*)p;
+        if (b0 + 2 + h / 2 < kb) v1 = *(const uint4*)(p + 64);
+        a = both4(v0, v1);
       } else {
-        a = lo4(in ? *(const uint4*)(A + m * (K / 2) + 16 * (b0 + h)) : zero);
+        uint4 v0 = make_uint4(0, 0, 0, 0);
+        if (in) v0 = *(const uint4*)(A + m * (K / 2) + 16 * (b0 + h));
+        a = lo4(v0);
       }
       acc[t] = mfma_mx<AF>(w, a, acc[t], sw, sa);
     }
@@ -85,6 +90,255 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_few_kernel(const uint8_t
 #pragma unroll
     for (int w = 0; w < kFewWaves; ++w) v += red[w][t][o];
     if (m0 + t < M && n0 + o < N) store_y(Y, (m0 + t) * ld_y + n0 + o, v, y_dtype);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens: tiles of BM tokens x BN outputs staged through LDS.
+//
+// K advances in stages of 128 through a ring of three LDS slots, filled by direct
+// loads (16 bytes a lane, no registers) two stages ahead.  A stage is two steps of
+// v_mfma_scale_f32_32x32x64_f8f6f4; the fragments of a step are read from LDS
+// while the matrix cores work on the step before, across the stage boundary too:
+// the block's one barrier a stage stands between the two steps, where the next
+// stage's loads must have landed.
+// ---------------------------------------------------------------------------
+template <int AF>
+__device__ __forceinline__ f32x16 mfma_mx32(const i32x8 w, const i32x8 a, f32x16 c, int ws, int as, int step) {
+  // scale bytes 0 and 2 of the registers: the lane's block of step 0 and 1
+  return step == 0
+             ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, c, 4, AF == kMxFp8 ? 0 : 4, 0, ws, 0, as)
+             : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, c, 4, AF == kMxFp8 ? 0 : 4, 2, ws, 2, as);
+}
+
+typedef __attribute__((address_space(3))) void* mx_lds_ptr;
+constexpr int kMxXcds = 8;
+constexpr int kMxStage = 128;   // K per stage
+
+// 16-byte chunk c of an LDS row sits at slot c ^ swz(row): 8 consecutive rows
+// spread over all positions of a 128-byte window and 16 over those of a 256-byte one
+__device__ __forceinline__ int swz8(int row) { return (row & 7) ^ ((row >> 3) & 1); }         // 8 chunks a row
+__device__ __forceinline__ int swz4(int row) { return ((row >> 1) & 3) ^ ((row >> 3) & 1); }  // 4 chunks a row
+
+// s_waitcnt vmcnt(N) lgkmcnt(0)
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
+}
+
+// 16 bytes a lane from base + off straight into LDS, lane i to 16 i bytes past dst
+__device__ __forceinline__ void load_lds16(const void* base, uint32_t bytes, uint8_t* dst, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000), (mx_lds_ptr)dst, 16,
+      off, 0, 0, 0);
+}
+
+template <int AF, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ as, int64_t M, const uint8_t* __restrict__ W,
+    const uint8_t* __restrict__ ws, int64_t N, int64_t K, int n_mt, int n_nt, int group_m, void* __restrict__ Y,
+    int64_t ld_y, int y_dtype) {
+  constexpr int NW = WM * WN;
+  constexpr int MT = BM / WM / 32, NT = BN / WN / 32;
+  constexpr int AB = AF == kMxFp8 ? 128 : 64;   // bytes of a row's stage
+  constexpr int WB = 64;
+  constexpr int AI = BM * AB / 1024 / NW, WI = BN * WB / 1024 / NW;  // direct loads a wave and stage
+  constexpr int ND = AI + WI;
+  static_assert(BM + BN <= NW * kWave, "one scale row a thread");
+  // one array a slot (A tile, then W tile): fragment reads then visibly do not touch the loads in flight
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[BM * AB + BN * WB];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[BM * AB + BN * WB];
+  __shared__ __attribute__((aligned(1024))) uint8_t s2[BM * AB + BN * WB];
+  __shared__ uint32_t sS[2 * (BM + BN) * 3];     // scale bytes of three stages, a row's side by side
+
+  // tile of this block: each XCD owns a contiguous range of tiles, walked in groups of group_m token tiles
+  const int nblk = (int)gridDim.x, bid = (int)blockIdx.x;
+  const int xcd = bid % kMxXcds, pos = bid / kMxXcds, q = nblk / kMxXcds, rr = nblk % kMxXcds;
+  const int id = xcd * q + (xcd < rr ? xcd : rr) + pos;
+  const int per_group = group_m * n_nt;
+  const int first_m = id / per_group * group_m;
+  const int gsz = n_mt - first_m < group_m ? n_mt - first_m : group_m;
+  const int64_t m0 = (int64_t)(first_m + id % per_group % gsz) * BM;
+  const int64_t n0 = (int64_t)(id % per_group / gsz) * BN;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int kb = (int)(K / kMxBlock);
+  const int nk = (int)((K + kMxStage - 1) / kMxStage);
+  const uint32_t a_row = (uint32_t)(AF == kMxFp8 ? K : K / 2), w_row = (uint32_t)(K / 2);
+  const int m_rows = (int)(M - m0 < BM ? M - m0 : BM), n_rows = (int)(N - n0 < BN ? N - n0 : BN);
+
+  // direct loads: lane i of load j fills 16 bytes i of the wave's j-th KiB.  Rows past the end repeat
+  // the last one (their results are not stored); chunks past K repeat the row's last one (their scales
+  // are the smallest on both sides, so that they add 0).
+  const uint8_t* a_tile = A + m0 * a_row;
+  const uint8_t* w_tile = W + n0 * w_row;
+  const uint32_t a_bytes = (uint32_t)m_rows * a_row, w_bytes = (uint32_t)n_rows * w_row;
+  uint32_t va[AI], ea[AI], vw[WI], ew[WI];  // offset of the first stage's chunk, of the row's last chunk
+#pragma unroll
+  for (int j = 0; j < AI; ++j) {
+    const int row = (wave * AI + j) * (1024 / AB) + lane / (AB / 16), slot = lane % (AB / 16);
+    const uint32_t at = (uint32_t)min(row, m_rows - 1) * a_row;
+    va[j] = at + 16u * (uint32_t)(slot ^ (AF == kMxFp8 ? swz8(row) : swz4(row)));
+    ea[j] = at + a_row - 16;
+  }
+#pragma unroll
+  for (int j = 0; j < WI; ++j) {
+    const int row = (wave * WI + j) * 16 + lane / 4;
+    const uint32_t at = (uint32_t)min(row, n_rows - 1) * w_row;
+    vw[j] = at + 16u * (uint32_t)((lane % 4) ^ swz4(row));
+    ew[j] = at + w_row - 16;
+  }
+  auto load_stage = [&](uint8_t* dst, int kt) {
+#pragma unroll
+    for (int j = 0; j < AI; ++j)
+      load_lds16(a_tile, a_bytes, dst + (wave * AI + j) * 1024, min(va[j] + (uint32_t)kt * AB, ea[j]));
+#pragma unroll
+    for (int j = 0; j < WI; ++j)
+      load_lds16(w_tile, w_bytes, dst + BM * AB + (wave * WI + j) * 1024, min(vw[j] + (uint32_t)kt * WB, ew[j]));
+  };
+
+  // scales: a thread carries the 12 bytes of its row for the next three stages; near the row's end the
+  // 12 last bytes are loaded and shifted down, with zeros behind them
+  const int srow_i = BM + BN == NW * kWave ? tid : min(tid, BM + BN - 1);
+  const uint8_t* srow = srow_i < BM ? as + (m0 + min(srow_i, m_rows - 1)) * kb
+                                    : ws + (n0 + min(srow_i - BM, n_rows - 1)) * kb;
+  uint3 sc;
+  int sc_shift = 0;  // bytes
+  auto load_scales = [&](int ss) {
+    const int at = min(12 * ss, kb - 12);
+    sc_shift = 12 * ss - at;
+    sc = ld_any<uint3>(srow + at);
+  };
+  auto write_scales = [&](int ss) {
+    const uint32_t v[3] = {sc.x, sc.y, sc.z};
+    const int words = sc_shift >> 2, bits = 8 * (sc_shift & 3);
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {
+      uint32_t lo = 0, hi = 0;
+#pragma unroll
+      for (int e = d; e < 3; ++e) {
+        lo = words == e - d ? v[e] : lo;
+        hi = words == e - d - 1 ? v[e] : hi;
+      }
+      sS[((ss & 1) * (BM + BN) + srow_i) * 3 + d] = (uint32_t)((((uint64_t)hi << 32) | lo) >> bits);
+    }
+  };
+
+  // fragments: lane l holds row l % 32 of a tile, h = l / 32
+  const int r = lane & 31, h = lane >> 5;
+  const int a_base = (wm * MT * 32 + r) * AB, w_base = BM * AB + (wn * NT * 32 + r) * WB;
+  struct Frags {
+    i32x8 a[MT];
+    uint4 w[NT];
+  };
+  struct Scales {
+    int a[MT], w[NT];
+  };
+  auto read_frags = [&](Frags& f, const uint8_t* tile, int step) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      f.w[i] = *(const uint4*)(tile + w_base + i * 32 * WB + 16 * ((2 * step + h) ^ swz4(r)));
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const uint8_t* p = tile + a_base + i * 32 * AB;
+      if constexpr (AF == kMxFp8)
+        f.a[i] = both4(*(const uint4*)(p + 16 * ((4 * step + h) ^ swz8(r))),
+                       *(const uint4*)(p + 16 * ((4 * step + 2 + h) ^ swz8(r))));
+      else
+        f.a[i] = lo4(*(const uint4*)(p + 16 * ((2 * step + h) ^ swz4(r))));
+    }
+  };
+  auto read_scales = [&](Scales& s, int ss, int d) {
+    const uint32_t* p = sS + (ss & 1) * (BM + BN) * 3;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) s.a[i] = (int)(p[3 * (wm * MT * 32 + 32 * i + r) + d] >> (8 * h));
+#pragma unroll
+    for (int i = 0; i < NT; ++i) s.w[i] = (int)(p[3 * (BM + wn * NT * 32 + 32 * i + r) + d] >> (8 * h));
+  };
+  f32x16 acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  auto products = [&](const Frags& f, const Scales& s, int step) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i][j] = mfma_mx32<AF>(lo4(f.w[i]), f.a[j], acc[i][j], s.w[i], s.a[j], step);
+  };
+
+  load_stage(s0, 0);
+  load_stage(s1, 1);
+  load_scales(0);
+  write_scales(0);
+  load_scales(1);
+  wait_loads<0>();
+  __builtin_amdgcn_s_barrier();
+  Frags f0, f1;
+  Scales c0, c1;
+  read_frags(f0, s0, 0);
+  read_scales(c0, 0, 0);
+
+  // Stage kt in slot P = kt % 3 (array C), its step-0 fragments read.  Before the barrier every wave has
+  // read the rest of the stage (lgkmcnt 0), so its slot may be filled again by stage kt + 3; and stage
+  // kt + 1 (array X) has landed: only the loads of stage kt + 2 (array F) are younger.  Loads past the
+  // last stage repeat its last chunks.
+#define AWQ_MX_STAGE(P, C, X, F)                  \
+  {                                               \
+    read_frags(f1, C, 1);                         \
+    load_stage(F, kt + 2);                        \
+    if (P == 2) write_scales(ss + 1);             \
+    products(f0, c0, 0);                          \
+    wait_loads<ND>();                             \
+    __builtin_amdgcn_s_barrier();                 \
+    __builtin_amdgcn_sched_barrier(0);            \
+    if (P == 2) load_scales(ss + 2);              \
+    read_frags(f0, X, 0);                         \
+    read_scales(c1, ss + (P == 2), (P + 1) % 3);  \
+    products(f1, c0, 1);                          \
+    __builtin_amdgcn_sched_barrier(0);            \
+    c0 = c1;                                      \
+    ++kt;                                         \
+  }
+  int kt = 0, ss = 0;  // ss = kt / 3
+  for (; kt + 3 <= nk; ++ss) {
+    AWQ_MX_STAGE(0, s0, s1, s2)
+    AWQ_MX_STAGE(1, s1, s2, s0)
+    AWQ_MX_STAGE(2, s2, s0, s1)
+  }
+  if (kt < nk) AWQ_MX_STAGE(0, s0, s1, s2)
+  if (kt < nk) AWQ_MX_STAGE(1, s1, s2, s0)
+#undef AWQ_MX_STAGE
+
+  // lane l holds outputs 8 (e / 4) + 4 h + e % 4 of token l % 32 of each 32 x 32 tile
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int64_t m = m0 + wm * MT * 32 + 32 * j + r;
+    if (m >= M) continue;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int64_t n = n0 + wn * NT * 32 + 32 * i + 8 * g + 4 * h;
+        const float v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+        if (n + 4 <= N) {
+          if (y_dtype == 2) st_any((float*)Y + m * ld_y + n, make_float4(v[0], v[1], v[2], v[3]));
+          else if (y_dtype == 0)
+            st_any((uint16_t*)Y + m * ld_y + n, make_uint2(f2x<0>(v[0]) | (f2x<0>(v[1]) << 16),
+                                                           f2x<0>(v[2]) | (f2x<0>(v[3]) << 16)));
+          else
+            st_any((uint16_t*)Y + m * ld_y + n, make_uint2(f2x<1>(v[0]) | (f2x<1>(v[1]) << 16),
+                                                           f2x<1>(v[2]) | (f2x<1>(v[3]) << 16)));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < N) store_y(Y, m * ld_y + n + e, v[e], y_dtype);
+        }
+      }
   }
 }
 
@@ -106,9 +360,24 @@ static void few_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uin
 #undef AWQ_FEW
 }
 
+template <int AF>
+static void tile_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uint8_t* W, const uint8_t* ws, int64_t N,
+                        int64_t K, void* Y, int64_t ld_y, int y_dtype, hipStream_t stream) {
+  const int n_mt = (int)((M + 255) / 256), n_nt = (int)((N + 255) / 256);
+  mx_tile_kernel<AF, 256, 256, 4, 2><<<(unsigned)(n_mt * n_nt), 512, 0, stream>>>(A, as, M, W, ws, N, K, n_mt, n_nt,
+                                                                                 8, Y, ld_y, y_dtype);
+}
+
 hipError_t launch_mx_matmul(const void* A, const uint8_t* as, int a_fmt, int64_t M, const void* W, const uint8_t* ws,
                             int64_t N, int64_t K, void* Y, int64_t ld_y, int y_dtype, void* work, hipStream_t stream) {
   (void)work;
+  if (M > 64 && K >= 384) {
+    if (a_fmt == kMxFp8)
+      tile_launch<kMxFp8>((const uint8_t*)A, as, M, (const uint8_t*)W, ws, N, K, Y, ld_y, y_dtype, stream);
+    else
+      tile_launch<kMxFp4>((const uint8_t*)A, as, M, (const uint8_t*)W, ws, N, K, Y, ld_y, y_dtype, stream);
+    return hipGetLastError();
+  }
   if (a_fmt == kMxFp8)
     few_launch<kMxFp8>((const uint8_t*)A, as, M, (const uint8_t*)W, ws, N, K, Y, ld_y, y_dtype, stream);
   else
