@@ -126,24 +126,54 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
 }
 
-// 16 bytes a lane from base + off straight into LDS, lane i to 16 i bytes past dst
-__device__ __forceinline__ void load_lds16(const void* base, uint32_t bytes, uint8_t* dst, uint32_t off) {
+// 16 bytes a lane from base + off + k_off straight into LDS, lane i to 16 i bytes past dst
+__device__ __forceinline__ void load_lds16(const void* base, uint32_t bytes, uint8_t* dst, uint32_t off,
+                                           uint32_t k_off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(
       __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000), (mx_lds_ptr)dst, 16,
-      off, 0, 0, 0);
+      off, k_off, 0, 0);
 }
 
-template <int AF, int BM, int BN, int WM, int WN>
+// Issue order of half a stage: two LDS reads and one or two direct loads behind each MFMA, so that
+// they are under way early and the matrix cores never wait for a burst of them
+template <int READS, int LOADS>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < (READS + 1) / 2; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                           // MFMA
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);                           // LDS reads
+    if (2 * i < LOADS) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);        // memory loads
+  }
+}
+
+// 16 bytes of a result row, or as many of its elements as are left
+template <int EB>
+__device__ __forceinline__ void store_row16(uint8_t* p, const uint4 v, int64_t left) {
+  if (left >= 16 / EB) {
+    st_any(p, v);
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 16 / EB; ++e)
+      if (e < left) {
+        if constexpr (EB == 4) ((uint32_t*)p)[e] = w[e];
+        else ((uint16_t*)p)[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+      }
+  }
+}
+
+template <int AF, int YT, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ as, int64_t M, const uint8_t* __restrict__ W,
     const uint8_t* __restrict__ ws, int64_t N, int64_t K, int n_mt, int n_nt, int group_m, void* __restrict__ Y,
-    int64_t ld_y, int y_dtype) {
+    int64_t ld_y) {
   constexpr int NW = WM * WN;
   constexpr int MT = BM / WM / 32, NT = BN / WN / 32;
   constexpr int AB = AF == kMxFp8 ? 128 : 64;   // bytes of a row's stage
   constexpr int WB = 64;
   constexpr int AI = BM * AB / 1024 / NW, WI = BN * WB / 1024 / NW;  // direct loads a wave and stage
   constexpr int ND = AI + WI;
+  constexpr int NR = NT + MT * (AF == kMxFp8 ? 2 : 1);               // LDS reads of a step's fragments
   static_assert(BM + BN <= NW * kWave, "one scale row a thread");
   // one array a slot (A tile, then W tile): fragment reads then visibly do not touch the loads in flight
   __shared__ __attribute__((aligned(1024))) uint8_t s0[BM * AB + BN * WB];
@@ -170,33 +200,28 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
   const int m_rows = (int)(M - m0 < BM ? M - m0 : BM), n_rows = (int)(N - n0 < BN ? N - n0 : BN);
 
   // direct loads: lane i of load j fills 16 bytes i of the wave's j-th KiB.  Rows past the end repeat
-  // the last one (their results are not stored); chunks past K repeat the row's last one (their scales
-  // are the smallest on both sides, so that they add 0).
+  // the last one (their results are not stored).  A last stage that K does not fill takes the row's last
+  // 128 values instead: the scales of those already summed are 0 on both sides, so that they add 0.
   const uint8_t* a_tile = A + m0 * a_row;
   const uint8_t* w_tile = W + n0 * w_row;
   const uint32_t a_bytes = (uint32_t)m_rows * a_row, w_bytes = (uint32_t)n_rows * w_row;
-  uint32_t va[AI], ea[AI], vw[WI], ew[WI];  // offset of the first stage's chunk, of the row's last chunk
+  uint32_t va[AI], vw[WI];
 #pragma unroll
   for (int j = 0; j < AI; ++j) {
     const int row = (wave * AI + j) * (1024 / AB) + lane / (AB / 16), slot = lane % (AB / 16);
-    const uint32_t at = (uint32_t)min(row, m_rows - 1) * a_row;
-    va[j] = at + 16u * (uint32_t)(slot ^ (AF == kMxFp8 ? swz8(row) : swz4(row)));
-    ea[j] = at + a_row - 16;
+    va[j] = (uint32_t)min(row, m_rows - 1) * a_row + 16u * (uint32_t)(slot ^ (AF == kMxFp8 ? swz8(row) : swz4(row)));
   }
 #pragma unroll
   for (int j = 0; j < WI; ++j) {
     const int row = (wave * WI + j) * 16 + lane / 4;
-    const uint32_t at = (uint32_t)min(row, n_rows - 1) * w_row;
-    vw[j] = at + 16u * (uint32_t)((lane % 4) ^ swz4(row));
-    ew[j] = at + w_row - 16;
+    vw[j] = (uint32_t)min(row, n_rows - 1) * w_row + 16u * (uint32_t)((lane % 4) ^ swz4(row));
   }
   auto load_stage = [&](uint8_t* dst, int kt) {
+    const uint32_t ka = min((uint32_t)kt * AB, a_row - AB), kw = min((uint32_t)kt * WB, w_row - WB);
 #pragma unroll
-    for (int j = 0; j < AI; ++j)
-      load_lds16(a_tile, a_bytes, dst + (wave * AI + j) * 1024, min(va[j] + (uint32_t)kt * AB, ea[j]));
+    for (int j = 0; j < AI; ++j) load_lds16(a_tile, a_bytes, dst + (wave * AI + j) * 1024, va[j], ka);
 #pragma unroll
-    for (int j = 0; j < WI; ++j)
-      load_lds16(w_tile, w_bytes, dst + BM * AB + (wave * WI + j) * 1024, min(vw[j] + (uint32_t)kt * WB, ew[j]));
+    for (int j = 0; j < WI; ++j) load_lds16(w_tile, w_bytes, dst + BM * AB + (wave * WI + j) * 1024, vw[j], kw);
   };
 
   // scales: a thread carries the 12 bytes of its row for the next three stages; near the row's end the
@@ -205,15 +230,11 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
   const uint8_t* srow = srow_i < BM ? as + (m0 + min(srow_i, m_rows - 1)) * kb
                                     : ws + (n0 + min(srow_i - BM, n_rows - 1)) * kb;
   uint3 sc;
-  int sc_shift = 0;  // bytes
-  auto load_scales = [&](int ss) {
-    const int at = min(12 * ss, kb - 12);
-    sc_shift = 12 * ss - at;
-    sc = ld_any<uint3>(srow + at);
-  };
+  auto load_scales = [&](int ss) { sc = ld_any<uint3>(srow + min(12 * ss, kb - 12)); };
   auto write_scales = [&](int ss) {
     const uint32_t v[3] = {sc.x, sc.y, sc.z};
-    const int words = sc_shift >> 2, bits = 8 * (sc_shift & 3);
+    const int shift = 12 * ss - min(12 * ss, kb - 12);  // bytes
+    const int words = shift >> 2, bits = 8 * (shift & 3);
 #pragma unroll
     for (int d = 0; d < 3; ++d) {
       uint32_t lo = 0, hi = 0;
@@ -222,7 +243,9 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
         lo = words == e - d ? v[e] : lo;
         hi = words == e - d - 1 ? v[e] : hi;
       }
-      sS[((ss & 1) * (BM + BN) + srow_i) * 3 + d] = (uint32_t)((((uint64_t)hi << 32) | lo) >> bits);
+      const int left = kb - 12 * ss - 4 * d;  // blocks from the stage's first on
+      sS[((ss & 1) * (BM + BN) + srow_i) * 3 + d] =
+          (uint32_t)((((uint64_t)hi << 32) | lo) >> bits) << (left > 0 && left < 4 ? 8 * (4 - left) : 0);
     }
   };
 
@@ -253,9 +276,15 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
   auto read_scales = [&](Scales& s, int ss, int d) {
     const uint32_t* p = sS + (ss & 1) * (BM + BN) * 3;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) s.a[i] = (int)(p[3 * (wm * MT * 32 + 32 * i + r) + d] >> (8 * h));
+    for (int i = 0; i < MT; ++i) s.a[i] = (int)p[3 * (wm * MT * 32 + 32 * i + r) + d];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) s.w[i] = (int)(p[3 * (BM + wn * NT * 32 + 32 * i + r) + d] >> (8 * h));
+    for (int i = 0; i < NT; ++i) s.w[i] = (int)p[3 * (BM + wn * NT * 32 + 32 * i + r) + d];
+  };
+  auto own_bytes = [&](Scales& s, const Scales& raw) {  // the lane's blocks to bytes 0 and 2
+#pragma unroll
+    for (int i = 0; i < MT; ++i) s.a[i] = (int)((uint32_t)raw.a[i] >> (8 * h));
+#pragma unroll
+    for (int i = 0; i < NT; ++i) s.w[i] = (int)((uint32_t)raw.w[i] >> (8 * h));
   };
   f32x16 acc[NT][MT];
 #pragma unroll
@@ -281,7 +310,7 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
   Frags f0, f1;
   Scales c0, c1;
   read_frags(f0, s0, 0);
-  read_scales(c0, 0, 0);
+  read_scales(c1, 0, 0);
 
   // Stage kt in slot P = kt % 3 (array C), its step-0 fragments read.  Before the barrier every wave has
   // read the rest of the stage (lgkmcnt 0), so its slot may be filled again by stage kt + 3; and stage
@@ -289,19 +318,22 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
   // last stage repeat its last chunks.
 #define AWQ_MX_STAGE(P, C, X, F)                  \
   {                                               \
+    own_bytes(c0, c1);                            \
     read_frags(f1, C, 1);                         \
     load_stage(F, kt + 2);                        \
     if (P == 2) write_scales(ss + 1);             \
     products(f0, c0, 0);                          \
+    interleave<NR, ND>();                         \
+    __builtin_amdgcn_sched_barrier(0);            \
     wait_loads<ND>();                             \
     __builtin_amdgcn_s_barrier();                 \
     __builtin_amdgcn_sched_barrier(0);            \
     if (P == 2) load_scales(ss + 2);              \
-    read_frags(f0, X, 0);                         \
     read_scales(c1, ss + (P == 2), (P + 1) % 3);  \
+    read_frags(f0, X, 0);                         \
     products(f1, c0, 1);                          \
+    interleave<NR + (MT + NT) / 2, 0>();          \
     __builtin_amdgcn_sched_barrier(0);            \
-    c0 = c1;                                      \
     ++kt;                                         \
   }
   int kt = 0, ss = 0;  // ss = kt / 3
@@ -314,32 +346,46 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
   if (kt < nk) AWQ_MX_STAGE(1, s1, s2, s0)
 #undef AWQ_MX_STAGE
 
-  // lane l holds outputs 8 (e / 4) + 4 h + e % 4 of token l % 32 of each 32 x 32 tile
+  wait_loads<0>();  // none may land after the block has given its LDS back
+  __builtin_amdgcn_s_barrier();
+
+  // Results: lane l holds outputs 8 (e / 4) + 4 h + e % 4 of token l % 32 of each 32 x 32 tile.  A wave
+  // turns 32 tokens at a time through its own part of the slots, so that 16 bytes a lane and whole rows
+  // of the wave's outputs go to memory together.
+  constexpr int EB = YT == 2 ? 4 : 2;
+  constexpr int CG = EB == 2 || NT == 1 ? NT : NT / 2;  // 32-output tiles per turn
+  constexpr int RB = CG * 32 * EB, RS = RB + 16;        // bytes of a row, and its stride
+  static_assert(NW <= 9 && 3 * 32 * RS <= BM * AB + BN * WB, "three waves a slot");
+  uint8_t* part = (wave < 3 ? s0 : wave < 6 ? s1 : s2) + wave % 3 * (32 * RS);
+  constexpr int LR = RB / 16, RI = kWave / LR;          // lanes a row, rows a store
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int64_t m = m0 + wm * MT * 32 + 32 * j + r;
-    if (m >= M) continue;
+  for (int j = 0; j < MT; ++j)
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i0 = 0; i0 < NT; i0 += CG) {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int64_t n = n0 + wn * NT * 32 + 32 * i + 8 * g + 4 * h;
-        const float v[4] = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-        if (n + 4 <= N) {
-          if (y_dtype == 2) st_any((float*)Y + m * ld_y + n, make_float4(v[0], v[1], v[2], v[3]));
-          else if (y_dtype == 0)
-            st_any((uint16_t*)Y + m * ld_y + n, make_uint2(f2x<0>(v[0]) | (f2x<0>(v[1]) << 16),
-                                                           f2x<0>(v[2]) | (f2x<0>(v[3]) << 16)));
+      for (int i = 0; i < CG; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x16& v = acc[i0 + i][j];
+          uint8_t* at = part + r * RS + (32 * i + 8 * g + 4 * h) * EB;
+          if constexpr (YT == 2) *(float4*)at = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
           else
-            st_any((uint16_t*)Y + m * ld_y + n, make_uint2(f2x<1>(v[0]) | (f2x<1>(v[1]) << 16),
-                                                           f2x<1>(v[2]) | (f2x<1>(v[3]) << 16)));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < N) store_y(Y, m * ld_y + n + e, v[e], y_dtype);
+            *(uint2*)at = make_uint2(f2x<YT>(v[4 * g]) | (f2x<YT>(v[4 * g + 1]) << 16),
+                                     f2x<YT>(v[4 * g + 2]) | (f2x<YT>(v[4 * g + 3]) << 16));
         }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+      for (int it = 0; it < 32 / RI; ++it) {
+        const int row = it * RI + lane / LR, c = lane % LR;
+        const uint4 v = *(const uint4*)(part + row * RS + 16 * c);
+        const int64_t m = m0 + wm * MT * 32 + 32 * j + row;
+        const int64_t n = n0 + wn * NT * 32 + 32 * i0 + c * (16 / EB);
+        if (m < M) store_row16<EB>((uint8_t*)Y + (m * ld_y + n) * EB, v, N - n);
       }
-  }
+      __builtin_amdgcn_wave_barrier();
+    }
 }
 
 size_t mx_matmul_workspace(int a_fmt, int64_t M, int64_t N, int64_t K) {
@@ -360,22 +406,26 @@ static void few_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uin
 #undef AWQ_FEW
 }
 
-template <int AF>
+template <int AF, int YT>
 static void tile_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uint8_t* W, const uint8_t* ws, int64_t N,
-                        int64_t K, void* Y, int64_t ld_y, int y_dtype, hipStream_t stream) {
+                        int64_t K, void* Y, int64_t ld_y, hipStream_t stream) {
   const int n_mt = (int)((M + 255) / 256), n_nt = (int)((N + 255) / 256);
-  mx_tile_kernel<AF, 256, 256, 4, 2><<<(unsigned)(n_mt * n_nt), 512, 0, stream>>>(A, as, M, W, ws, N, K, n_mt, n_nt,
-                                                                                 8, Y, ld_y, y_dtype);
+  mx_tile_kernel<AF, YT, 256, 256, 4, 2><<<(unsigned)(n_mt * n_nt), 512, 0, stream>>>(A, as, M, W, ws, N, K, n_mt,
+                                                                                     n_nt, 8, Y, ld_y);
 }
 
 hipError_t launch_mx_matmul(const void* A, const uint8_t* as, int a_fmt, int64_t M, const void* W, const uint8_t* ws,
                             int64_t N, int64_t K, void* Y, int64_t ld_y, int y_dtype, void* work, hipStream_t stream) {
   (void)work;
   if (M > 64 && K >= 384) {
-    if (a_fmt == kMxFp8)
-      tile_launch<kMxFp8>((const uint8_t*)A, as, M, (const uint8_t*)W, ws, N, K, Y, ld_y, y_dtype, stream);
-    else
-      tile_launch<kMxFp4>((const uint8_t*)A, as, M, (const uint8_t*)W, ws, N, K, Y, ld_y, y_dtype, stream);
+#define AWQ_TILE(F, T) \
+  tile_launch<F, T>((const uint8_t*)A, as, M, (const uint8_t*)W, ws, N, K, Y, ld_y, stream)
+    if (a_fmt == kMxFp8) {
+      if (y_dtype == 0) AWQ_TILE(kMxFp8, 0); else AWQ_TILE(kMxFp8, 1);
+    } else {
+      if (y_dtype == 0) AWQ_TILE(kMxFp4, 0); else if (y_dtype == 1) AWQ_TILE(kMxFp4, 1); else AWQ_TILE(kMxFp4, 2);
+    }
+#undef AWQ_TILE
     return hipGetLastError();
   }
   if (a_fmt == kMxFp8)
