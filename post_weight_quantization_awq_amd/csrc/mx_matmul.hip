@@ -32,51 +32,88 @@ __device__ __forceinline__ void store_y(void* Y, int64_t at, float v, int y_dtyp
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: a block holds 16 outputs and 16 MT tokens; its 8 waves take K
-// steps of 128 in turn and their sums are added in wave order through LDS.
+// Few tokens: a block holds 16 outputs and 16 MT tokens.  Its 8 waves take chunks
+// of 512 K in turn (four MFMA steps; 64 lanes read 16 rows of 64 bytes a load),
+// the next chunk's weights on their way while one is multiplied; their sums are
+// added in wave order through LDS.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
+constexpr int kFewBlocks = 16;  // scale blocks of a chunk
+
+// The 16 scale bytes of a row's chunk c; zeros past the row's end
+__device__ __forceinline__ uint4 few_scales(const uint8_t* row, int c, int kb) {
+  if (kFewBlocks * (c + 1) <= kb) return ld_any<uint4>(row + kFewBlocks * c);
+  uint32_t v[4] = {0, 0, 0, 0};
+  for (int i = 0; i < kb - kFewBlocks * c; ++i) {
+    const uint32_t b = (uint32_t)row[kFewBlocks * c + i] << (8 * (i & 3));
+#pragma unroll
+    for (int d = 0; d < 4; ++d) v[d] |= d == i >> 2 ? b : 0;
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+// 16 bytes of codes that hold values of block b, zeros past the row's end
+__device__ __forceinline__ uint4 few_codes(const uint8_t* p, int b, int kb) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (b < kb) v = *(const uint4*)p;
+  return v;
+}
 
 template <int AF, int MT>
-__global__ __launch_bounds__(kFewWaves * kWave) void mx_few_kernel(const uint8_t* __restrict__ A,
-                                                                  const uint8_t* __restrict__ as, int64_t M,
-                                                                  const uint8_t* __restrict__ W,
-                                                                  const uint8_t* __restrict__ ws, int64_t N, int64_t K,
-                                                                  void* __restrict__ Y, int64_t ld_y, int y_dtype) {
+__global__ __launch_bounds__(kFewWaves * kWave, 2) void mx_few_kernel(const uint8_t* __restrict__ A,
+                                                                     const uint8_t* __restrict__ as, int64_t M,
+                                                                     const uint8_t* __restrict__ W,
+                                                                     const uint8_t* __restrict__ ws, int64_t N,
+                                                                     int64_t K, void* __restrict__ Y, int64_t ld_y,
+                                                                     int y_dtype) {
   __shared__ float red[kFewWaves][MT * 16][17];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, h = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (16 * MT);
-  const int64_t kb = K / kMxBlock;
+  const int kb = (int)(K / kMxBlock), nc = (kb + kFewBlocks - 1) / kFewBlocks;
   const int64_t n = n0 + r < N ? n0 + r : N - 1;  // rows past the end repeat the last one, unused
-  const uint8_t* wr = W + n * (K / 2);
+  const uint8_t* wr = W + n * (K / 2) + 16 * h;
   const uint8_t* wsr = ws + n * kb;
+  const uint8_t* ar[MT];
+  const uint8_t* asr[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int64_t m = m0 + 16 * t + r < M ? m0 + 16 * t + r : M - 1;
+    ar[t] = A + m * (AF == kMxFp8 ? K : K / 2) + 16 * h;
+    asr[t] = as + m * kb;
+  }
   f32x4 acc[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) acc[t] = (f32x4){0, 0, 0, 0};
-  for (int64_t b0 = 4 * wave; b0 < kb; b0 += 4 * kFewWaves) {
-    const bool in = b0 + h < kb;
-    uint4 wv = make_uint4(0, 0, 0, 0);
-    if (in) wv = *(const uint4*)(wr + 16 * (b0 + h));
-    const i32x8 w = lo4(wv);
-    const int sw = in ? wsr[b0 + h] : 0;
+
+  uint4 w[4], sw;
+  auto load_w = [&](int c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = few_codes(wr + 256 * (int64_t)c + 64 * j, kFewBlocks * c + 4 * j + h, kb);
+    sw = few_scales(wsr, c, kb);
+  };
+  if (wave < nc) load_w(wave);
+  for (int c = wave; c < nc; c += kFewWaves) {
+    uint4 wc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) wc[j] = w[j];
+    const uint32_t swc[4] = {sw.x >> (8 * h), sw.y >> (8 * h), sw.z >> (8 * h), sw.w >> (8 * h)};
+    if (c + kFewWaves < nc) load_w(c + kFewWaves);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const int64_t m = m0 + 16 * t + r < M ? m0 + 16 * t + r : M - 1;
-      const int sa = in ? as[m * kb + b0 + h] : 0;
-      i32x8 a;
-      if constexpr (AF == kMxFp8) {
-        const uint8_t* p = A + m * K + 32 * b0 + 16 * h;
-        uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-        if (b0 + h / 2 < kb) v0 = *(const uint4*)p;
-        if (b0 + 2 + h / 2 < kb) v1 = *(const uint4*)(p + 64);
-        a = both4(v0, v1);
-      } else {
-        uint4 v0 = make_uint4(0, 0, 0, 0);
-        if (in) v0 = *(const uint4*)(A + m * (K / 2) + 16 * (b0 + h));
-        a = lo4(v0);
+      const uint4 sa = few_scales(asr[t], c, kb);
+      const uint32_t sac[4] = {sa.x >> (8 * h), sa.y >> (8 * h), sa.z >> (8 * h), sa.w >> (8 * h)};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int b = kFewBlocks * c + 4 * j;
+        i32x8 a;
+        if constexpr (AF == kMxFp8) {
+          const uint8_t* p = ar[t] + 32 * (int64_t)b;
+          a = both4(few_codes(p, b + h / 2, kb), few_codes(p + 64, b + 2 + h / 2, kb));
+        } else {
+          a = lo4(few_codes(ar[t] + 16 * (int64_t)b, b + h, kb));
+        }
+        acc[t] = mfma_mx<AF>(lo4(wc[j]), a, acc[t], (int)swc[j], (int)sac[j]);
       }
-      acc[t] = mfma_mx<AF>(w, a, acc[t], sw, sa);
     }
   }
 #pragma unroll
@@ -88,7 +125,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void mx_few_kernel(const uint8_t
     const int t = i >> 4, o = i & 15;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) v += red[w][t][o];
+    for (int q = 0; q < kFewWaves; ++q) v += red[q][t][o];
     if (m0 + t < M && n0 + o < N) store_y(Y, (m0 + t) * ld_y + n0 + o, v, y_dtype);
   }
 }
@@ -174,7 +211,6 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
   constexpr int AI = BM * AB / 1024 / NW, WI = BN * WB / 1024 / NW;  // direct loads a wave and stage
   constexpr int ND = AI + WI;
   constexpr int NR = NT + MT * (AF == kMxFp8 ? 2 : 1);               // LDS reads of a step's fragments
-  static_assert(BM + BN <= NW * kWave, "one scale row a thread");
   // one array a slot (A tile, then W tile): fragment reads then visibly do not touch the loads in flight
   __shared__ __attribute__((aligned(1024))) uint8_t s0[BM * AB + BN * WB];
   __shared__ __attribute__((aligned(1024))) uint8_t s1[BM * AB + BN * WB];
@@ -224,28 +260,40 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
     for (int j = 0; j < WI; ++j) load_lds16(w_tile, w_bytes, dst + BM * AB + (wave * WI + j) * 1024, vw[j], kw);
   };
 
-  // scales: a thread carries the 12 bytes of its row for the next three stages; near the row's end the
+  // scales: a thread carries the 12 bytes of its rows for the next three stages; near the row's end the
   // 12 last bytes are loaded and shifted down, with zeros behind them
-  const int srow_i = BM + BN == NW * kWave ? tid : min(tid, BM + BN - 1);
-  const uint8_t* srow = srow_i < BM ? as + (m0 + min(srow_i, m_rows - 1)) * kb
-                                    : ws + (n0 + min(srow_i - BM, n_rows - 1)) * kb;
-  uint3 sc;
-  auto load_scales = [&](int ss) { sc = ld_any<uint3>(srow + min(12 * ss, kb - 12)); };
+  constexpr int SR = (BM + BN + NW * kWave - 1) / (NW * kWave);
+  uint3 sc[SR];
+  const uint8_t* srow[SR];
+  int srow_i[SR];
+#pragma unroll
+  for (int q = 0; q < SR; ++q) {
+    srow_i[q] = min(tid + q * NW * kWave, BM + BN - 1);
+    srow[q] = srow_i[q] < BM ? as + (m0 + min(srow_i[q], m_rows - 1)) * kb
+                             : ws + (n0 + min(srow_i[q] - BM, n_rows - 1)) * kb;
+  }
+  auto load_scales = [&](int ss) {
+#pragma unroll
+    for (int q = 0; q < SR; ++q) sc[q] = ld_any<uint3>(srow[q] + min(12 * ss, kb - 12));
+  };
   auto write_scales = [&](int ss) {
-    const uint32_t v[3] = {sc.x, sc.y, sc.z};
     const int shift = 12 * ss - min(12 * ss, kb - 12);  // bytes
     const int words = shift >> 2, bits = 8 * (shift & 3);
 #pragma unroll
-    for (int d = 0; d < 3; ++d) {
-      uint32_t lo = 0, hi = 0;
+    for (int q = 0; q < SR; ++q) {
+      const uint32_t v[3] = {sc[q].x, sc[q].y, sc[q].z};
 #pragma unroll
-      for (int e = d; e < 3; ++e) {
-        lo = words == e - d ? v[e] : lo;
-        hi = words == e - d - 1 ? v[e] : hi;
+      for (int d = 0; d < 3; ++d) {
+        uint32_t lo = 0, hi = 0;
+#pragma unroll
+        for (int e = d; e < 3; ++e) {
+          lo = words == e - d ? v[e] : lo;
+          hi = words == e - d - 1 ? v[e] : hi;
+        }
+        const int left = kb - 12 * ss - 4 * d;  // blocks from the stage's first on
+        sS[((ss & 1) * (BM + BN) + srow_i[q]) * 3 + d] =
+            (uint32_t)((((uint64_t)hi << 32) | lo) >> bits) << (left > 0 && left < 4 ? 8 * (4 - left) : 0);
       }
-      const int left = kb - 12 * ss - 4 * d;  // blocks from the stage's first on
-      sS[((ss & 1) * (BM + BN) + srow_i) * 3 + d] =
-          (uint32_t)((((uint64_t)hi << 32) | lo) >> bits) << (left > 0 && left < 4 ? 8 * (4 - left) : 0);
     }
   };
 
