@@ -2,6 +2,8 @@
 // e2m1 blocks, W in e2m1 blocks, both row-major along K with one scale byte per
 // 32 values.  The matrix cores take the codes and the scale bytes as they are
 // (v_mfma_scale_f32_16x16x128_f8f6f4): no value is dequantized in registers.
+#include <math.h>
+
 #include "awq_launch.h"
 #include "mx_device.h"
 
@@ -151,6 +153,7 @@ __device__ __forceinline__ f32x16 mfma_mx32(const i32x8 w, const i32x8 a, f32x16
 typedef __attribute__((address_space(3))) void* mx_lds_ptr;
 constexpr int kMxXcds = 8;
 constexpr int kMxStage = 128;   // K per stage
+constexpr uint32_t kMxOut = 0x80000000u;  // an offset past the range of every tile's buffer (256 rows of <= 2^22 bytes)
 
 // 16-byte chunk c of an LDS row sits at slot c ^ swz(row): 8 consecutive rows
 // spread over all positions of a 128-byte window and 16 over those of a 256-byte one
@@ -199,11 +202,13 @@ __device__ __forceinline__ void store_row16(uint8_t* p, const uint4 v, int64_t l
   }
 }
 
-template <int AF, int YT, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
+// OCC: waves a SIMD that the registers are to leave room for.  blockIdx.y: one of gridDim.y ranges of
+// `split` stages of K; range z's sums go to Y + z M ld_y (YT 2).
+template <int AF, int YT, int BM, int BN, int WM, int WN, int OCC>
+__global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ as, int64_t M, const uint8_t* __restrict__ W,
-    const uint8_t* __restrict__ ws, int64_t N, int64_t K, int n_mt, int n_nt, int group_m, void* __restrict__ Y,
-    int64_t ld_y) {
+    const uint8_t* __restrict__ ws, int64_t N, int64_t K, int n_mt, int n_nt, int group_m, int split,
+    void* __restrict__ Y, int64_t ld_y) {
   constexpr int NW = WM * WN;
   constexpr int MT = BM / WM / 32, NT = BN / WN / 32;
   constexpr int AB = AF == kMxFp8 ? 128 : 64;   // bytes of a row's stage
@@ -231,12 +236,13 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int kb = (int)(K / kMxBlock);
-  const int nk = (int)((K + kMxStage - 1) / kMxStage);
+  const int k0 = (int)blockIdx.y * split;  // first stage
+  const int nk = min((int)((K + kMxStage - 1) / kMxStage) - k0, split);
   const uint32_t a_row = (uint32_t)(AF == kMxFp8 ? K : K / 2), w_row = (uint32_t)(K / 2);
   const int m_rows = (int)(M - m0 < BM ? M - m0 : BM), n_rows = (int)(N - n0 < BN ? N - n0 : BN);
 
-  // direct loads: lane i of load j fills 16 bytes i of the wave's j-th KiB.  Rows past the end repeat
-  // the last one (their results are not stored).  A last stage that K does not fill takes the row's last
+  // direct loads: lane i of load j fills 16 bytes i of the wave's j-th KiB.  Rows past the end are out of
+  // the buffer's range and read as zeros (their results are not stored).  A last stage that K does not fill takes the row's last
   // 128 values instead: the scales of those already summed are 0 on both sides, so that they add 0.
   const uint8_t* a_tile = A + m0 * a_row;
   const uint8_t* w_tile = W + n0 * w_row;
@@ -245,15 +251,15 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
 #pragma unroll
   for (int j = 0; j < AI; ++j) {
     const int row = (wave * AI + j) * (1024 / AB) + lane / (AB / 16), slot = lane % (AB / 16);
-    va[j] = (uint32_t)min(row, m_rows - 1) * a_row + 16u * (uint32_t)(slot ^ (AF == kMxFp8 ? swz8(row) : swz4(row)));
+    va[j] = row < m_rows ? (uint32_t)row * a_row + 16u * (uint32_t)(slot ^ (AF == kMxFp8 ? swz8(row) : swz4(row))) : kMxOut;
   }
 #pragma unroll
   for (int j = 0; j < WI; ++j) {
     const int row = (wave * WI + j) * 16 + lane / 4;
-    vw[j] = (uint32_t)min(row, n_rows - 1) * w_row + 16u * (uint32_t)((lane % 4) ^ swz4(row));
+    vw[j] = row < n_rows ? (uint32_t)row * w_row + 16u * (uint32_t)((lane % 4) ^ swz4(row)) : kMxOut;
   }
   auto load_stage = [&](uint8_t* dst, int kt) {
-    const uint32_t ka = min((uint32_t)kt * AB, a_row - AB), kw = min((uint32_t)kt * WB, w_row - WB);
+    const uint32_t ka = min((uint32_t)(k0 + kt) * AB, a_row - AB), kw = min((uint32_t)(k0 + kt) * WB, w_row - WB);
 #pragma unroll
     for (int j = 0; j < AI; ++j) load_lds16(a_tile, a_bytes, dst + (wave * AI + j) * 1024, va[j], ka);
 #pragma unroll
@@ -274,10 +280,10 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
   }
   auto load_scales = [&](int ss) {
 #pragma unroll
-    for (int q = 0; q < SR; ++q) sc[q] = ld_any<uint3>(srow[q] + min(12 * ss, kb - 12));
+    for (int q = 0; q < SR; ++q) sc[q] = ld_any<uint3>(srow[q] + min(4 * k0 + 12 * ss, kb - 12));
   };
   auto write_scales = [&](int ss) {
-    const int shift = 12 * ss - min(12 * ss, kb - 12);  // bytes
+    const int b0 = 4 * k0 + 12 * ss, shift = b0 - min(b0, kb - 12);  // blocks, bytes
     const int words = shift >> 2, bits = 8 * (shift & 3);
 #pragma unroll
     for (int q = 0; q < SR; ++q) {
@@ -290,7 +296,7 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
           lo = words == e - d ? v[e] : lo;
           hi = words == e - d - 1 ? v[e] : hi;
         }
-        const int left = kb - 12 * ss - 4 * d;  // blocks from the stage's first on
+        const int left = kb - b0 - 4 * d;  // blocks from the stage's first on
         sS[((ss & 1) * (BM + BN) + srow_i[q]) * 3 + d] =
             (uint32_t)((((uint64_t)hi << 32) | lo) >> bits) << (left > 0 && left < 4 ? 8 * (4 - left) : 0);
       }
@@ -402,9 +408,12 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
   // of the wave's outputs go to memory together.
   constexpr int EB = YT == 2 ? 4 : 2;
   constexpr int CG = EB == 2 || NT == 1 ? NT : NT / 2;  // 32-output tiles per turn
-  constexpr int RB = CG * 32 * EB, RS = RB + 16;        // bytes of a row, and its stride
-  static_assert(NW <= 9 && 3 * 32 * RS <= BM * AB + BN * WB, "three waves a slot");
-  uint8_t* part = (wave < 3 ? s0 : wave < 6 ? s1 : s2) + wave % 3 * (32 * RS);
+  constexpr int RB = CG * 32 * EB;                      // bytes of a row
+  constexpr int WS = (NW + 2) / 3;                      // waves a slot
+  constexpr int RS = RB + (WS * 32 * (RB + 16) <= BM * AB + BN * WB ? 16 : 0);  // stride: padded where there is room
+  static_assert(WS * 32 * RS <= BM * AB + BN * WB, "a slot holds the rows of its waves");
+  if constexpr (YT == 2) Y = (float*)Y + (int64_t)blockIdx.y * M * ld_y;
+  uint8_t* part = (wave < WS ? s0 : wave < 2 * WS ? s1 : s2) + wave % WS * (32 * RS);
   constexpr int LR = RB / 16, RI = kWave / LR;          // lanes a row, rows a store
 #pragma unroll
   for (int j = 0; j < MT; ++j)
@@ -436,9 +445,69 @@ __global__ __launch_bounds__(WM* WN* kWave, WM* WN / 4) void mx_tile_kernel(
     }
 }
 
+// Y = sum over z, in order, of part[z] (fp32 [M, ld_p] each): 4 outputs a thread
+template <int YT>
+__global__ __launch_bounds__(256) void mx_reduce_kernel(const float* __restrict__ part, int n_split, int64_t M,
+                                                        int64_t N, int64_t ld_p, void* __restrict__ Y, int64_t ld_y) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t m = i / (ld_p / 4), n = 4 * (i % (ld_p / 4));
+  if (m >= M) return;
+  float4 v = *(const float4*)(part + m * ld_p + n);
+  for (int z = 1; z < n_split; ++z) {
+    const float4 p = *(const float4*)(part + (z * M + m) * ld_p + n);
+    v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+  }
+  const float f[4] = {v.x, v.y, v.z, v.w};
+  const int64_t at = m * ld_y + n;
+  if (n + 4 <= N) {
+    if constexpr (YT == 2) st_any((float*)Y + at, v);
+    else
+      st_any((uint16_t*)Y + at,
+             make_uint2(f2x<YT>(f[0]) | (f2x<YT>(f[1]) << 16), f2x<YT>(f[2]) | (f2x<YT>(f[3]) << 16)));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < N) store_y(Y, at + e, f[e], YT);
+  }
+}
+
+// The kernel, its tile and the number of K ranges of a product: the ones with the least estimated time.
+// Measured on 8-bit activations (4-bit ones rank alike), in us: a stage of K costs 0.27 / 0.5 / 1.3 a
+// block of 64 / 128 / 256 squared while no compute unit has more than one, and 0.21 / 0.5 / 1.3 for each
+// 256 blocks beyond; K ranges add 2.5 for the second launch and their fp32 sums written and read at 5 TB/s;
+// the few-token kernel reads the weights at 4.2 TB/s and the activations once per 16 outputs at 12 TB/s.
+// E.g. 24 x 4096 x 12288: few tokens 15.7, 64-tiles 29, in 4 ranges 12.6; 512 x 24576 x 4096: 82 / 52 / 46;
+// 2048 x 4096 x 4096: 55 / 34 / 38; 256 x 4096 x 4096: 12 / 16 / 23.
+struct MxTiling {
+  int tile;   // outputs and tokens a tile: 64, 128 or 256; 0: few tokens
+  int split;  // stages a range
+  int ranges;
+};
+static MxTiling mx_tiling(int a_fmt, int64_t M, int64_t N, int64_t K) {
+  const int nk = (int)((K + kMxStage - 1) / kMxStage);
+  const double w_bytes = (double)N * K * (17.0 / 32), a_bytes = (double)M * K * (a_fmt == kMxFp8 ? 1.0 : 0.5);
+  MxTiling best = {0, nk, 1};
+  if (K < 3 * kMxStage) return best;  // a tile's scales are taken three stages at a time
+  double least = 2.5 + w_bytes / 4.2e6 + (double)((N + 15) / 16) * a_bytes / 12e6;
+  for (int tile = 64; tile <= 256; tile *= 2) {
+    const double per = tile == 64 ? 0.21 : tile == 128 ? 0.5 : 1.3;
+    const double blocks = (double)((M + tile - 1) / tile) * (double)((N + tile - 1) / tile);
+    for (int s = 1; s <= 8 && nk / s >= 6; ++s) {
+      const int split = (nk + s - 1) / s, ranges = (nk + split - 1) / split;
+      if (s > 1 && (ranges != s || blocks * s > 512)) continue;
+      const double rounds = ceil(blocks * ranges / 256);
+      double t = 3 + split * (tile == 64 && rounds == 1 ? 0.27 : per * rounds);
+      if (ranges > 1) t += 2.5 + ranges * (double)M * (double)N * 8 / 5e6;
+      if (t < least) least = t, best = {tile, split, ranges};
+    }
+  }
+  return best;
+}
+static int64_t part_ld(int64_t N) { return (N + 3) / 4 * 4; }
+
 size_t mx_matmul_workspace(int a_fmt, int64_t M, int64_t N, int64_t K) {
-  (void)a_fmt, (void)M, (void)N, (void)K;
-  return 0;
+  const MxTiling t = mx_tiling(a_fmt, M, N, K);
+  return t.ranges > 1 ? (size_t)t.ranges * M * part_ld(N) * sizeof(float) : 0;
 }
 
 template <int AF>
@@ -455,31 +524,47 @@ static void few_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uin
 }
 
 template <int AF, int YT>
-static void tile_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uint8_t* W, const uint8_t* ws, int64_t N,
-                        int64_t K, void* Y, int64_t ld_y, hipStream_t stream) {
-  const int n_mt = (int)((M + 255) / 256), n_nt = (int)((N + 255) / 256);
-  mx_tile_kernel<AF, YT, 256, 256, 4, 2><<<(unsigned)(n_mt * n_nt), 512, 0, stream>>>(A, as, M, W, ws, N, K, n_mt,
-                                                                                     n_nt, 8, Y, ld_y);
+static void tile_launch(const MxTiling& t, const uint8_t* A, const uint8_t* as, int64_t M, const uint8_t* W,
+                        const uint8_t* ws, int64_t N, int64_t K, void* Y, int64_t ld_y, hipStream_t stream) {
+  const int n_mt = (int)((M + t.tile - 1) / t.tile), n_nt = (int)((N + t.tile - 1) / t.tile);
+  const dim3 g((unsigned)(n_mt * n_nt), (unsigned)t.ranges);
+#define AWQ_TILE(BM, BN, WM, WN, OCC)                                                                               \
+  mx_tile_kernel<AF, YT, BM, BN, WM, WN, OCC><<<g, WM * WN * kWave, 0, stream>>>(A, as, M, W, ws, N, K, n_mt, n_nt, 8, \
+                                                                               t.split, Y, ld_y)
+  if (t.tile == 64) AWQ_TILE(64, 64, 2, 2, 4);
+  else if (t.tile == 128) AWQ_TILE(128, 128, 2, 2, 2);
+  else AWQ_TILE(256, 256, 4, 2, 2);
+#undef AWQ_TILE
+}
+
+template <int AF, int YT>
+static void product_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uint8_t* W, const uint8_t* ws,
+                           int64_t N, int64_t K, void* Y, int64_t ld_y, float* part, hipStream_t stream) {
+  const MxTiling t = mx_tiling(AF, M, N, K);
+  if (t.tile == 0) {
+    few_launch<AF>(A, as, M, W, ws, N, K, Y, ld_y, YT, stream);
+  } else if (t.ranges == 1) {
+    tile_launch<AF, YT>(t, A, as, M, W, ws, N, K, Y, ld_y, stream);
+  } else {
+    const int64_t ld_p = part_ld(N);
+    tile_launch<AF, 2>(t, A, as, M, W, ws, N, K, part, ld_p, stream);
+    mx_reduce_kernel<YT><<<(unsigned)((M * (ld_p / 4) + 255) / 256), 256, 0, stream>>>(part, t.ranges, M, N, ld_p, Y,
+                                                                                      ld_y);
+  }
 }
 
 hipError_t launch_mx_matmul(const void* A, const uint8_t* as, int a_fmt, int64_t M, const void* W, const uint8_t* ws,
                             int64_t N, int64_t K, void* Y, int64_t ld_y, int y_dtype, void* work, hipStream_t stream) {
-  (void)work;
-  if (M > 64 && K >= 384) {
-#define AWQ_TILE(F, T) \
-  tile_launch<F, T>((const uint8_t*)A, as, M, (const uint8_t*)W, ws, N, K, Y, ld_y, stream)
-    if (a_fmt == kMxFp8) {
-      if (y_dtype == 0) AWQ_TILE(kMxFp8, 0); else AWQ_TILE(kMxFp8, 1);
-    } else {
-      if (y_dtype == 0) AWQ_TILE(kMxFp4, 0); else if (y_dtype == 1) AWQ_TILE(kMxFp4, 1); else AWQ_TILE(kMxFp4, 2);
-    }
-#undef AWQ_TILE
-    return hipGetLastError();
+#define AWQ_PRODUCT(F, T) \
+  product_launch<F, T>((const uint8_t*)A, as, M, (const uint8_t*)W, ws, N, K, Y, ld_y, (float*)work, stream)
+  if (a_fmt == kMxFp8) {
+    if (y_dtype == 0) AWQ_PRODUCT(kMxFp8, 0); else AWQ_PRODUCT(kMxFp8, 1);
+  } else {
+    if (y_dtype == 0) AWQ_PRODUCT(kMxFp4, 0);
+    else if (y_dtype == 1) AWQ_PRODUCT(kMxFp4, 1);
+    else AWQ_PRODUCT(kMxFp4, 2);
   }
-  if (a_fmt == kMxFp8)
-    few_launch<kMxFp8>((const uint8_t*)A, as, M, (const uint8_t*)W, ws, N, K, Y, ld_y, y_dtype, stream);
-  else
-    few_launch<kMxFp4>((const uint8_t*)A, as, M, (const uint8_t*)W, ws, N, K, Y, ld_y, y_dtype, stream);
+#undef AWQ_PRODUCT
   return hipGetLastError();
 }
 
