@@ -29,26 +29,20 @@ __device__ __forceinline__ ChunkPos chunk_pos(int64_t r0, uint32_t c0, uint32_t 
   return {r0 + q, c - q * cpr};
 }
 
-template <int DT, int FMT, bool SCALED>
+template <int DT, int FMT>
 __global__ __launch_bounds__(kEwThreads) void mx_quantize_kernel(const uint16_t* __restrict__ X, int64_t n_chunks,
-                                                                 uint32_t cpr, int64_t ld, const float* __restrict__ s,
-                                                                 uint8_t* __restrict__ out,
+                                                                 uint32_t cpr, int64_t ld, uint8_t* __restrict__ out,
                                                                  uint8_t* __restrict__ scales) {
   const int64_t base = (int64_t)blockIdx.x * (kEwThreads * kEwUnroll);
   const int64_t r0 = base / cpr;
   const uint32_t c0 = (uint32_t)(base - r0 * cpr);
   uint4 x[kEwUnroll];
-  float sv[kEwUnroll][8];
 #pragma unroll
   for (int u = 0; u < kEwUnroll; ++u) {
     const uint32_t off = threadIdx.x + kEwThreads * u;
     if (base + off < n_chunks) {
       const ChunkPos p = chunk_pos(r0, c0, off, cpr);
       x[u] = ld_any<uint4>(X + p.row * ld + 8 * (int64_t)p.col);
-      if constexpr (SCALED) {
-        *(float4*)&sv[u][0] = ld_any<float4>(s + 8 * (int64_t)p.col);
-        *(float4*)&sv[u][4] = ld_any<float4>(s + 8 * (int64_t)p.col + 4);
-      }
     }
   }
 #pragma unroll
@@ -57,15 +51,66 @@ __global__ __launch_bounds__(kEwThreads) void mx_quantize_kernel(const uint16_t*
     if (chunk < n_chunks) {
       float v[8];
       unpack8<DT>(x[u], v);
-      if constexpr (SCALED) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= sv[u][j];
-      }
       uint32_t codes[2];
       const uint32_t byte = mx_quantize8<FMT>(v, codes);
       mx_store8<FMT>(codes, byte, out, scales, chunk);
     }
   }
+}
+
+// With a scale of the columns a lane keeps its 8 columns over kColRows rows, so
+// the scale is loaded (and, in the inverse, its reciprocal taken) once for them:
+// a block is 16 chunks of columns by 16 x kColRows rows.
+constexpr int kColRows = 8;
+__device__ __forceinline__ void col_pos(uint32_t cpr, uint32_t* col, int64_t* row) {
+  const uint32_t nx = (cpr + 15) / 16;
+  const uint32_t by = blockIdx.x / nx, bx = blockIdx.x - by * nx;
+  *col = bx * 16 + threadIdx.x % 16;
+  *row = (int64_t)by * (16 * kColRows) + threadIdx.x / 16;
+}
+
+template <int DT, int FMT>
+__global__ __launch_bounds__(kEwThreads) void mx_quantize_scaled_kernel(const uint16_t* __restrict__ X, int64_t rows,
+                                                                        uint32_t cpr, int64_t ld,
+                                                                        const float* __restrict__ s,
+                                                                        uint8_t* __restrict__ out,
+                                                                        uint8_t* __restrict__ scales) {
+  uint32_t col;
+  int64_t row;
+  col_pos(cpr, &col, &row);
+  if (col >= cpr) return;  // whole groups of 4 lanes: cpr is a multiple of 4
+  float sv[8];
+  *(float4*)&sv[0] = ld_any<float4>(s + 8 * (int64_t)col);
+  *(float4*)&sv[4] = ld_any<float4>(s + 8 * (int64_t)col + 4);
+  uint4 x[kColRows];
+#pragma unroll
+  for (int u = 0; u < kColRows; ++u)
+    if (row + 16 * u < rows) x[u] = ld_any<uint4>(X + (row + 16 * u) * ld + 8 * (int64_t)col);
+#pragma unroll
+  for (int u = 0; u < kColRows; ++u) {
+    if (row + 16 * u < rows) {
+      float v[8];
+      unpack8<DT>(x[u], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= sv[j];
+      uint32_t codes[2];
+      const uint32_t byte = mx_quantize8<FMT>(v, codes);
+      mx_store8<FMT>(codes, byte, out, scales, (row + 16 * u) * cpr + col);
+    }
+  }
+}
+
+// g / (1 + e^-g) to a few units of the last place: -g log2 e in two parts, the
+// second put back as a factor 1 + r ln 2; the sum and g carry a factor 1/4 so
+// that the reciprocal of a sum near the largest float is no subnormal.  Past
+// g = -88.7 the exponential is infinite and the quotient -0, as in the formula.
+__device__ __forceinline__ float silu(float g) {
+  const float kHi = 1.44269502162933349609375f, kLo = 1.92596298909109e-8f, kLn2 = 0.693147182464599609375f;
+  const float t = -g * kHi;
+  const float r = __builtin_fmaf(-g, kLo, __builtin_fmaf(-g, kHi, -t));
+  float e = __builtin_amdgcn_exp2f(t);
+  e = __builtin_fabsf(t) < 128.0f ? __builtin_fmaf(e, r * kLn2, e) : e;  // beyond: 0 or infinity
+  return g * 0.25f * __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0.25f, 0.25f));
 }
 
 template <int DT, int FMT>
@@ -95,7 +140,7 @@ __global__ __launch_bounds__(kEwThreads) void silu_mul_mx_kernel(const uint16_t*
       unpack8<DT>(g[u], v);
       unpack8<DT>(w[u], b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = v[j] / (1.0f + expf(-v[j])) * b[j];
+      for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * b[j];
       uint32_t codes[2];
       const uint32_t byte = mx_quantize8<FMT>(v, codes);
       mx_store8<FMT>(codes, byte, out, scales, chunk);
@@ -108,11 +153,40 @@ __global__ __launch_bounds__(kEwThreads) void silu_mul_mx_kernel(const uint16_t*
 // fp32 (unless it overflows); the quotient is rounded to fp32 and then to a
 // 16-bit output, as unpack_dequant does.
 // ---------------------------------------------------------------------------
-template <int FMT, int OT, bool SCALED>
+template <int FMT>
+__device__ __forceinline__ void decode8(const uint2 c, float (&v)[8]) {  // elements, unscaled
+  f32x2v t;
+  if constexpr (FMT == kMxFp8) {
+    t = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false), v[0] = t[0], v[1] = t[1];
+    t = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true), v[2] = t[0], v[3] = t[1];
+    t = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false), v[4] = t[0], v[5] = t[1];
+    t = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true), v[6] = t[0], v[7] = t[1];
+  } else {
+    t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c.x, 1.0f, 0), v[0] = t[0], v[1] = t[1];
+    t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c.x, 1.0f, 1), v[2] = t[0], v[3] = t[1];
+    t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c.x, 1.0f, 2), v[4] = t[0], v[5] = t[1];
+    t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c.x, 1.0f, 3), v[6] = t[0], v[7] = t[1];
+  }
+}
+template <int FMT>
+__device__ __forceinline__ uint2 load_codes8(const uint8_t* __restrict__ codes, int64_t chunk) {
+  if constexpr (FMT == kMxFp8) return *(const uint2*)(codes + 8 * chunk);
+  else return make_uint2(*(const uint32_t*)(codes + 4 * chunk), 0);
+}
+template <int OT>
+__device__ __forceinline__ void store_values8(void* __restrict__ out, int64_t at, const float (&v)[8]) {
+  if constexpr (OT == 2) {
+    st_any((float*)out + at, make_float4(v[0], v[1], v[2], v[3]));
+    st_any((float*)out + at + 4, make_float4(v[4], v[5], v[6], v[7]));
+  } else {
+    st_any((uint16_t*)out + at, pack8<OT>(v));
+  }
+}
+
+template <int FMT, int OT>
 __global__ __launch_bounds__(kEwThreads) void mx_dequant_kernel(const uint8_t* __restrict__ codes,
                                                                 const uint8_t* __restrict__ scales, int64_t n_chunks,
-                                                                uint32_t cpr, const float* __restrict__ s,
-                                                                void* __restrict__ out, int64_t ld) {
+                                                                uint32_t cpr, void* __restrict__ out, int64_t ld) {
   const int64_t base = (int64_t)blockIdx.x * (kEwThreads * kEwUnroll);
   const int64_t r0 = base / cpr;
   const uint32_t c0 = (uint32_t)(base - r0 * cpr);
@@ -122,8 +196,7 @@ __global__ __launch_bounds__(kEwThreads) void mx_dequant_kernel(const uint8_t* _
   for (int u = 0; u < kEwUnroll; ++u) {
     const int64_t chunk = base + threadIdx.x + kEwThreads * u;
     if (chunk < n_chunks) {
-      if constexpr (FMT == kMxFp8) c[u] = *(const uint2*)(codes + 8 * chunk);
-      else c[u].x = *(const uint32_t*)(codes + 4 * chunk);
+      c[u] = load_codes8<FMT>(codes, chunk);
       e[u] = scales[chunk >> 2];
     }
   }
@@ -134,34 +207,72 @@ __global__ __launch_bounds__(kEwThreads) void mx_dequant_kernel(const uint8_t* _
       const ChunkPos p = chunk_pos(r0, c0, off, cpr);
       const float unit = mx_unit(e[u]);
       float v[8];
-      f32x2v t;
-      if constexpr (FMT == kMxFp8) {
-        t = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[u].x, false), v[0] = t[0], v[1] = t[1];
-        t = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[u].x, true), v[2] = t[0], v[3] = t[1];
-        t = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[u].y, false), v[4] = t[0], v[5] = t[1];
-        t = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[u].y, true), v[6] = t[0], v[7] = t[1];
-      } else {
-        t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u].x, 1.0f, 0), v[0] = t[0], v[1] = t[1];
-        t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u].x, 1.0f, 1), v[2] = t[0], v[3] = t[1];
-        t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u].x, 1.0f, 2), v[4] = t[0], v[5] = t[1];
-        t = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[u].x, 1.0f, 3), v[6] = t[0], v[7] = t[1];
-      }
+      decode8<FMT>(c[u], v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= unit;
-      if constexpr (SCALED) {
-        float sv[8];
-        *(float4*)&sv[0] = ld_any<float4>(s + 8 * (int64_t)p.col);
-        *(float4*)&sv[4] = ld_any<float4>(s + 8 * (int64_t)p.col + 4);
+      store_values8<OT>(out, p.row * ld + 8 * (int64_t)p.col, v);
+    }
+  }
+}
+
+// Divided by the columns' scale.  With y = RN(1 / s), taken once for the lane's
+// rows: q0 = RN(v y), then q0 + RN(v - s q0) y rounded is the IEEE quotient
+// (checked on the host for every mantissa of s and all 8 mantissas of the
+// elements), where nothing leaves the normal range: |s| and 2^e within 2^+-60
+// and 2^+-40.  Elsewhere the division itself.
+__device__ __forceinline__ bool mid_range(float x, uint32_t by) {
+  const uint32_t e = __builtin_bit_cast(uint32_t, x) >> 23 & 255;
+  return e - (127 - by) <= 2 * by;
+}
+
+template <int FMT, int OT>
+__global__ __launch_bounds__(kEwThreads) void mx_dequant_scaled_kernel(const uint8_t* __restrict__ codes,
+                                                                       const uint8_t* __restrict__ scales,
+                                                                       int64_t rows, uint32_t cpr,
+                                                                       const float* __restrict__ s,
+                                                                       void* __restrict__ out, int64_t ld) {
+  uint32_t col;
+  int64_t row;
+  col_pos(cpr, &col, &row);
+  if (col >= cpr) return;
+  uint2 c[kColRows];
+  uint32_t e[kColRows];
+#pragma unroll
+  for (int u = 0; u < kColRows; ++u) {
+    const int64_t chunk = (row + 16 * u) * cpr + col;
+    if (row + 16 * u < rows) {
+      c[u] = load_codes8<FMT>(codes, chunk);
+      e[u] = scales[chunk >> 2];
+    }
+  }
+  float sv[8], y[8];
+  *(float4*)&sv[0] = ld_any<float4>(s + 8 * (int64_t)col);
+  *(float4*)&sv[4] = ld_any<float4>(s + 8 * (int64_t)col + 4);
+  bool usual = true;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    y[j] = 1.0f / sv[j];
+    usual = usual && mid_range(sv[j], 60);
+  }
+#pragma unroll
+  for (int u = 0; u < kColRows; ++u) {
+    if (row + 16 * u < rows) {
+      const float unit = mx_unit(e[u]);
+      float v[8];
+      decode8<FMT>(c[u], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= unit;
+      if (usual && mid_range(unit, 40)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float q = v[j] * y[j];
+          v[j] = __builtin_fmaf(__builtin_fmaf(-sv[j], q, v[j]), y[j], q);
+        }
+      } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = v[j] / sv[j];
       }
-      const int64_t at = p.row * ld + 8 * (int64_t)p.col;
-      if constexpr (OT == 2) {
-        st_any((float*)out + at, make_float4(v[0], v[1], v[2], v[3]));
-        st_any((float*)out + at + 4, make_float4(v[4], v[5], v[6], v[7]));
-      } else {
-        st_any((uint16_t*)out + at, pack8<OT>(v));
-      }
+      store_values8<OT>(out, (row + 16 * u) * ld + 8 * (int64_t)col, v);
     }
   }
 }
@@ -264,21 +375,26 @@ static unsigned ew_blocks(int64_t n_chunks) {
   return (unsigned)((n_chunks + kEwThreads * kEwUnroll - 1) / (kEwThreads * kEwUnroll));
 }
 
+static unsigned col_blocks(int64_t rows, int64_t cols) {
+  return (unsigned)((cols / 8 + 15) / 16 * ((rows + 16 * kColRows - 1) / (16 * kColRows)));
+}
+
 hipError_t launch_mx_quantize(const void* X, int dt, int64_t rows, int64_t cols, int64_t ld, const float* s, int fmt,
                               void* codes, uint8_t* scales, hipStream_t stream) {
   const int64_t n = rows * (cols / 8);
-  const unsigned g = ew_blocks(n);
-#define AWQ_MXQ(D, F, S)                                                                                          \
-  mx_quantize_kernel<D, F, S><<<g, kEwThreads, 0, stream>>>((const uint16_t*)X, n, (uint32_t)(cols / 8), ld, s, \
-                                                            (uint8_t*)codes, scales)
-#define AWQ_MXQ_S(D, F) \
-  if (s) AWQ_MXQ(D, F, true); else AWQ_MXQ(D, F, false)
+  const uint32_t cpr = (uint32_t)(cols / 8);
+#define AWQ_MXQ(D, F)                                                                                                  \
+  if (s)                                                                                                               \
+    mx_quantize_scaled_kernel<D, F><<<col_blocks(rows, cols), kEwThreads, 0, stream>>>((const uint16_t*)X, rows, cpr, ld, \
+                                                                                       s, (uint8_t*)codes, scales);    \
+  else                                                                                                                 \
+    mx_quantize_kernel<D, F><<<ew_blocks(n), kEwThreads, 0, stream>>>((const uint16_t*)X, n, cpr, ld, (uint8_t*)codes, \
+                                                                      scales)
   if (dt == 0) {
-    if (fmt == kMxFp8) { AWQ_MXQ_S(0, kMxFp8); } else { AWQ_MXQ_S(0, kMxFp4); }
+    if (fmt == kMxFp8) { AWQ_MXQ(0, kMxFp8); } else { AWQ_MXQ(0, kMxFp4); }
   } else {
-    if (fmt == kMxFp8) { AWQ_MXQ_S(1, kMxFp8); } else { AWQ_MXQ_S(1, kMxFp4); }
+    if (fmt == kMxFp8) { AWQ_MXQ(1, kMxFp8); } else { AWQ_MXQ(1, kMxFp4); }
   }
-#undef AWQ_MXQ_S
 #undef AWQ_MXQ
   return hipGetLastError();
 }
@@ -302,19 +418,19 @@ hipError_t launch_silu_mul_mx(const void* gate, int64_t ld_g, const void* up, in
 hipError_t launch_mx_dequant(const void* codes, const uint8_t* scales, int fmt, int64_t rows, int64_t cols,
                              const float* s, void* out, int out_dtype, int64_t ld, hipStream_t stream) {
   const int64_t n = rows * (cols / 8);
-  const unsigned g = ew_blocks(n);
-#define AWQ_MXD(F, O, S)                                                                                            \
-  mx_dequant_kernel<F, O, S><<<g, kEwThreads, 0, stream>>>((const uint8_t*)codes, scales, n, (uint32_t)(cols / 8), s, \
-                                                           out, ld)
-#define AWQ_MXD_S(F, O) \
-  if (s) AWQ_MXD(F, O, true); else AWQ_MXD(F, O, false)
-#define AWQ_MXD_O(F)                       \
-  if (out_dtype == 0) { AWQ_MXD_S(F, 0); } \
-  else if (out_dtype == 1) { AWQ_MXD_S(F, 1); } \
-  else { AWQ_MXD_S(F, 2); }
+  const uint32_t cpr = (uint32_t)(cols / 8);
+#define AWQ_MXD(F, O)                                                                                                 \
+  if (s)                                                                                                              \
+    mx_dequant_scaled_kernel<F, O><<<col_blocks(rows, cols), kEwThreads, 0, stream>>>((const uint8_t*)codes, scales, rows, \
+                                                                                      cpr, s, out, ld);               \
+  else                                                                                                                \
+    mx_dequant_kernel<F, O><<<ew_blocks(n), kEwThreads, 0, stream>>>((const uint8_t*)codes, scales, n, cpr, out, ld)
+#define AWQ_MXD_O(F)                          \
+  if (out_dtype == 0) { AWQ_MXD(F, 0); }      \
+  else if (out_dtype == 1) { AWQ_MXD(F, 1); } \
+  else { AWQ_MXD(F, 2); }
   if (fmt == kMxFp8) { AWQ_MXD_O(kMxFp8) } else { AWQ_MXD_O(kMxFp4) }
 #undef AWQ_MXD_O
-#undef AWQ_MXD_S
 #undef AWQ_MXD
   return hipGetLastError();
 }

@@ -494,3 +494,42 @@ def test_product_two_streams(A):
         got = [p.run() for p in plans]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_dequant_scaled_far_scales(A, fmt):
+    """Quotients whose scale or block exponent lies far out: the IEEE quotient there too."""
+    import torch
+    say(f"mx_dequant far scales {fmt}")
+    rng = np.random.default_rng(9)
+    rows, cols = 40, 96
+    codes = rng.integers(0, 256, (rows, cols if fmt == "fp8" else cols // 2)).astype(np.uint8)
+    if fmt == "fp8":
+        codes[(codes & 127) == 127] = 1
+    scales = rng.integers(0, 255, (rows, cols // 32)).astype(np.uint8)
+    s = np.exp2(rng.uniform(-120, 120, cols)).astype(np.float32)
+    s[:32] = np.exp2(rng.uniform(-30, 30, 32)).astype(np.float32)
+    s[33], s[34], s[35] = 0.0, np.inf, -3.0
+    with np.errstate(all="ignore"):
+        want = O.mx_values(codes, scales, fmt).astype(np.float32) / s
+    got = A.mx_dequant(*dev_mx(codes, scales, fmt), s=torch.from_numpy(s).cuda()).cpu().numpy()
+    assert np.array_equal(got, want, equal_nan=True)
+
+
+def test_silu_mul_every_gate(A):
+    """Every finite 16-bit gate, one value a block, so that its own relative error shows."""
+    import torch
+    for dtype in ("f16", "bf16"):
+        say(f"silu_mul_mx every {dtype} gate")
+        g = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(tdt(dtype))
+        g = g[g.isfinite()]
+        G = torch.zeros((g.numel(), 32), dtype=tdt(dtype))
+        G[:, 5] = g
+        Up = torch.ones_like(G)
+        y = O.silu_mul(G.double().numpy(), Up.double().numpy())
+        out = A.silu_mul_mx(G.cuda(), Up.cuda(), "fp8")
+        keep = (g > -87).numpy()     # below, the exact value passes under 2^-119 and the exponential overflows
+        got = O.mx_values(*quantized(out), "fp8")
+        assert np.all(np.abs(got[~keep]) <= np.abs(y[~keep]) * 1.1 + 2.0 ** -127)
+        sel = torch.from_numpy(keep).cuda()
+        check_near([t.view(torch.uint8)[sel].view(t.dtype) for t in out], "fp8", y[keep], 8 * U)
