@@ -57,6 +57,12 @@ __device__ __forceinline__ T ld_any(const void* p) {
   __builtin_memcpy(&v, p, sizeof(T));
   return v;
 }
+// 16 bytes that are read once: the nontemporal hint keeps them from displacing what is read again
+typedef uint32_t u32x4any __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  const u32x4any v = __builtin_nontemporal_load((const u32x4any*)p);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
 template <class T>
 __device__ __forceinline__ void st_any(void* p, const T v) {
   __builtin_memcpy(p, &v, sizeof(T));
