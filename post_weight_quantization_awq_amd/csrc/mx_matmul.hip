@@ -174,6 +174,13 @@ __device__ __forceinline__ void load_lds16(const void* base, uint32_t bytes, uin
       off, k_off, 0, 0);
 }
 
+// the same with 4 bytes a lane
+__device__ __forceinline__ void load_lds4(const void* base, uint32_t bytes, uint8_t* dst, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000), (mx_lds_ptr)dst, 4,
+      off, 0, 0, 0);
+}
+
 // Issue order of half a stage: two LDS reads and one or two direct loads behind each MFMA, so that
 // they are under way early and the matrix cores never wait for a burst of them
 template <int READS, int LOADS>
@@ -202,6 +209,63 @@ __device__ __forceinline__ void store_row16(uint8_t* p, const uint4 v, int64_t l
   }
 }
 
+// Results of a wave's MT x NT tiles of 32 x 32 at (m0, n0): lane l holds outputs 8 (e / 4) + 4 h + e % 4 of
+// token l % 32.  The wave turns 32 tokens at a time through its own part of the block's LDS arrays (SB
+// bytes each), so that 16 bytes a lane and whole rows of its outputs go to memory together.
+template <int YT, int MT, int NT, int NW, int SB>
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[NT][MT], uint8_t* s0, uint8_t* s1, uint8_t* s2,
+                                           int wave, int lane, int64_t m0, int64_t n0, int64_t M, int64_t N, void* Y,
+                                           int64_t ld_y) {
+  constexpr int EB = YT == 2 ? 4 : 2;
+  constexpr int CG = EB == 2 || NT == 1 ? NT : NT / 2;       // 32-output tiles per turn
+  constexpr int RB = CG * 32 * EB;                           // bytes of a row
+  constexpr int WS = (NW + 2) / 3;                           // waves an array
+  constexpr int RS = RB + (WS * 32 * (RB + 16) <= SB ? 16 : 0);  // stride: padded where there is room
+  static_assert(WS * 32 * RS <= SB, "an array holds the rows of its waves");
+  uint8_t* part = (wave < WS ? s0 : wave < 2 * WS ? s1 : s2) + wave % WS * (32 * RS);
+  constexpr int LR = RB / 16, RI = kWave / LR;               // lanes a row, rows a store
+  const int r = lane & 31, h = lane >> 5;
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int i0 = 0; i0 < NT; i0 += CG) {
+#pragma unroll
+      for (int i = 0; i < CG; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x16& v = acc[i0 + i][j];
+          uint8_t* at = part + r * RS + (32 * i + 8 * g + 4 * h) * EB;
+          if constexpr (YT == 2) *(float4*)at = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+          else
+            *(uint2*)at = make_uint2(f2x<YT>(v[4 * g]) | (f2x<YT>(v[4 * g + 1]) << 16),
+                                     f2x<YT>(v[4 * g + 2]) | (f2x<YT>(v[4 * g + 3]) << 16));
+        }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+      for (int it = 0; it < 32 / RI; ++it) {
+        const int row = it * RI + lane / LR, c = lane % LR;
+        const uint4 v = *(const uint4*)(part + row * RS + 16 * c);
+        const int64_t m = m0 + 32 * j + row, n = n0 + 32 * i0 + c * (16 / EB);
+        if (m < M) store_row16<EB>((uint8_t*)Y + (m * ld_y + n) * EB, v, N - n);
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// The tile of a block: each XCD owns a contiguous range of tiles, walked in groups of group_m token tiles
+__device__ __forceinline__ void block_tile(int n_mt, int n_nt, int group_m, int* mt, int* nt) {
+  const int nblk = (int)gridDim.x, bid = (int)blockIdx.x;
+  const int xcd = bid % kMxXcds, pos = bid / kMxXcds, q = nblk / kMxXcds, rr = nblk % kMxXcds;
+  const int id = xcd * q + (xcd < rr ? xcd : rr) + pos;
+  const int per_group = group_m * n_nt;
+  const int first_m = id / per_group * group_m;
+  const int gsz = n_mt - first_m < group_m ? n_mt - first_m : group_m;
+  *mt = first_m + id % per_group % gsz;
+  *nt = id % per_group / gsz;
+}
+
 // OCC: waves a SIMD that the registers are to leave room for.  blockIdx.y: one of gridDim.y ranges of
 // `split` stages of K; range z's sums go to Y + z M ld_y (YT 2).
 template <int AF, int YT, int BM, int BN, int WM, int WN, int OCC>
@@ -222,16 +286,9 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
   __shared__ __attribute__((aligned(1024))) uint8_t s2[BM * AB + BN * WB];
   __shared__ uint32_t sS[2 * (BM + BN) * 3];     // scale bytes of three stages, a row's side by side
 
-  // tile of this block: each XCD owns a contiguous range of tiles, walked in groups of group_m token tiles
-  const int nblk = (int)gridDim.x, bid = (int)blockIdx.x;
-  const int xcd = bid % kMxXcds, pos = bid / kMxXcds, q = nblk / kMxXcds, rr = nblk % kMxXcds;
-  const int id = xcd * q + (xcd < rr ? xcd : rr) + pos;
-  const int per_group = group_m * n_nt;
-  const int first_m = id / per_group * group_m;
-  const int gsz = n_mt - first_m < group_m ? n_mt - first_m : group_m;
-  const int64_t m0 = (int64_t)(first_m + id % per_group % gsz) * BM;
-  const int64_t n0 = (int64_t)(id % per_group / gsz) * BN;
-
+  int mt, nt;
+  block_tile(n_mt, n_nt, group_m, &mt, &nt);
+  const int64_t m0 = (int64_t)mt * BM, n0 = (int64_t)nt * BN;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -403,46 +460,240 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
   wait_loads<0>();  // none may land after the block has given its LDS back
   __builtin_amdgcn_s_barrier();
 
-  // Results: lane l holds outputs 8 (e / 4) + 4 h + e % 4 of token l % 32 of each 32 x 32 tile.  A wave
-  // turns 32 tokens at a time through its own part of the slots, so that 16 bytes a lane and whole rows
-  // of the wave's outputs go to memory together.
-  constexpr int EB = YT == 2 ? 4 : 2;
-  constexpr int CG = EB == 2 || NT == 1 ? NT : NT / 2;  // 32-output tiles per turn
-  constexpr int RB = CG * 32 * EB;                      // bytes of a row
-  constexpr int WS = (NW + 2) / 3;                      // waves a slot
-  constexpr int RS = RB + (WS * 32 * (RB + 16) <= BM * AB + BN * WB ? 16 : 0);  // stride: padded where there is room
-  static_assert(WS * 32 * RS <= BM * AB + BN * WB, "a slot holds the rows of its waves");
-  if constexpr (YT == 2) Y = (float*)Y + (int64_t)blockIdx.y * M * ld_y;
-  uint8_t* part = (wave < WS ? s0 : wave < 2 * WS ? s1 : s2) + wave % WS * (32 * RS);
-  constexpr int LR = RB / 16, RI = kWave / LR;          // lanes a row, rows a store
+  store_tile<YT, MT, NT, NW, BM * AB + BN * WB>(acc, s0, s1, s2, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M, N,
+                                               YT == 2 ? (float*)Y + (int64_t)blockIdx.y * M * ld_y : Y, ld_y);
+}
+
+// ---------------------------------------------------------------------------
+// Large products: 256 x 256 tiles, where the loads that reach the second-level
+// cache bound the kernel (measured with everything else left out: 297 us of the
+// 388 us of an 8-bit 8192^3 product, 252 of 301 us of a 4-bit one).  So every row
+// of a stage is a whole 128-byte line where LDS allows it: a stage is 128 K in
+// three slots for 8-bit activations (W rows then half a line) and 256 K in two
+// slots for 4-bit ones; and the scales, whose bytes of a stage lie in a line of
+// their own for each row, are first laid out stage by stage (stage_scales), so
+// that a stage takes 16 or 32 lines of them instead of 512.
+// ---------------------------------------------------------------------------
+template <int AF>
+constexpr int kBigStage = AF == kMxFp8 ? 128 : 256;
+template <int AF>
+constexpr int kBigSlots = AF == kMxFp8 ? 3 : 2;
+constexpr int kBigTile = 256;
+
+// out[w][row] (rows: the A rows, then the W rows, each padded to whole tiles): word w % (SB / 4) of stage
+// w / (SB / 4), the scale bytes of SB = K / 32 blocks.  A last stage that K does not fill holds the row's
+// last SB blocks, 0 in the place of those of earlier stages; padded rows hold 0.
+template <int SB>
+__global__ __launch_bounds__(256) void stage_scales_kernel(const uint8_t* __restrict__ as, int64_t M,
+                                                           const uint8_t* __restrict__ ws, int64_t N, int kb,
+                                                           int64_t m_pad, int64_t rows, uint32_t* __restrict__ out) {
+  const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;  // rows is a multiple of 256
+  const bool is_a = row < m_pad;
+  const int64_t r = is_a ? row : row - m_pad;
+  const bool live = r < (is_a ? M : N);
+  const uint8_t* p = (is_a ? as : ws) + (live ? r : 0) * kb;
+  const int s0 = (int)blockIdx.y * (16 / SB), n_stage = (kb + SB - 1) / SB;  // 16 blocks a thread
+  uint32_t v[4] = {0, 0, 0, 0};
+  if (live) {
+    if ((s0 + 16 / SB) * SB <= kb) {
+      const uint4 u = ld_any<uint4>(p + s0 * SB);
+      v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+    } else {
 #pragma unroll
-  for (int j = 0; j < MT; ++j)
-#pragma unroll
-    for (int i0 = 0; i0 < NT; i0 += CG) {
-#pragma unroll
-      for (int i = 0; i < CG; ++i)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f32x16& v = acc[i0 + i][j];
-          uint8_t* at = part + r * RS + (32 * i + 8 * g + 4 * h) * EB;
-          if constexpr (YT == 2) *(float4*)at = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
-          else
-            *(uint2*)at = make_uint2(f2x<YT>(v[4 * g]) | (f2x<YT>(v[4 * g + 1]) << 16),
-                                     f2x<YT>(v[4 * g + 2]) | (f2x<YT>(v[4 * g + 3]) << 16));
-        }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-      for (int it = 0; it < 32 / RI; ++it) {
-        const int row = it * RI + lane / LR, c = lane % LR;
-        const uint4 v = *(const uint4*)(part + row * RS + 16 * c);
-        const int64_t m = m0 + wm * MT * 32 + 32 * j + row;
-        const int64_t n = n0 + wn * NT * 32 + 32 * i0 + c * (16 / EB);
-        if (m < M) store_row16<EB>((uint8_t*)Y + (m * ld_y + n) * EB, v, N - n);
+      for (int i = 0; i < 16; ++i) {
+        const int b0 = (s0 + i / SB) * SB;                          // the stage's first block
+        const int b = (b0 + SB <= kb ? b0 : kb - SB) + i % SB;      // the byte's
+        if (b0 < kb && b >= b0) v[i / 4] |= (uint32_t)p[b] << (8 * (i % 4));
       }
-      __builtin_amdgcn_wave_barrier();
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (s0 + i * 4 / SB < n_stage) out[(int64_t)(s0 * (SB / 4) + i) * rows + row] = v[i];
+}
+
+template <int AF, int YT>
+__global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restrict__ A, int64_t M,
+                                                        const uint8_t* __restrict__ W, int64_t N, int64_t K,
+                                                        const uint32_t* __restrict__ sc, int64_t m_pad, int64_t rows,
+                                                        int n_mt, int n_nt, int group_m, void* __restrict__ Y,
+                                                        int64_t ld_y) {
+  constexpr int KS = kBigStage<AF>, SL = kBigSlots<AF>, T = kBigTile;
+  constexpr int WM = 4, WN = 2, NW = 8, MT = T / WM / 32, NT = T / WN / 32;
+  constexpr int AB = 128, WB = KS / 2;                 // bytes of a row's stage
+  constexpr int SW = KS / 128;                         // scale words of a row's stage
+  constexpr int AI = T * AB / 1024 / NW, WI = T * WB / 1024 / NW, SI = SW;  // direct loads a wave and stage
+  constexpr int ND = AI + WI + SI;
+  constexpr int ST = KS / 64;                          // MFMA steps a stage
+  constexpr int NR = NT + MT * (AF == kMxFp8 ? 2 : 1);  // LDS reads of a step's fragments
+  constexpr int oW = T * AB, oS = oW + T * WB, SB = oS + SW * 2 * T * 4;
+  // one array a slot (A tile, W tile, scale words): fragment reads then visibly do not touch the loads in flight
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t s2[SL == 3 ? SB : 16];
+
+  int mt, nt;
+  block_tile(n_mt, n_nt, group_m, &mt, &nt);
+  const int64_t m0 = (int64_t)mt * T, n0 = (int64_t)nt * T;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int nk = (int)((K + KS - 1) / KS);
+  const uint32_t a_row = (uint32_t)(AF == kMxFp8 ? K : K / 2), w_row = (uint32_t)(K / 2);
+  const int m_rows = (int)(M - m0 < T ? M - m0 : T), n_rows = (int)(N - n0 < T ? N - n0 : T);
+
+  // direct loads: lane i of load j fills 16 bytes i of the wave's j-th KiB.  Rows past the end are out of
+  // the buffer's range and read as zeros.  A last stage that K does not fill takes the row's last KS values.
+  const uint8_t* a_tile = A + m0 * a_row;
+  const uint8_t* w_tile = W + n0 * w_row;
+  const uint32_t a_bytes = (uint32_t)m_rows * a_row, w_bytes = (uint32_t)n_rows * w_row;
+  uint32_t va[AI], vw[WI];
+#pragma unroll
+  for (int j = 0; j < AI; ++j) {
+    const int row = (wave * AI + j) * (1024 / AB) + lane / (AB / 16);
+    va[j] = row < m_rows ? (uint32_t)row * a_row + 16u * (uint32_t)(lane % (AB / 16) ^ swz8(row)) : kMxOut;
+  }
+#pragma unroll
+  for (int j = 0; j < WI; ++j) {
+    const int row = (wave * WI + j) * (1024 / WB) + lane / (WB / 16), c = lane % (WB / 16);
+    vw[j] = row < n_rows ? (uint32_t)row * w_row + 16u * (uint32_t)(c ^ (WB == 128 ? swz8(row) : swz4(row))) : kMxOut;
+  }
+  // scales: the wave's 64 of the tile's 256 + 256 rows; words past the last stage's are not read
+  const int64_t s_row = wave < 4 ? m0 + 64 * wave : m_pad + n0 + 64 * (wave - 4);
+  auto load_stage = [&](uint8_t* dst, int kt) {
+    const uint32_t ka = min((uint32_t)kt * AB, a_row - AB), kw = min((uint32_t)kt * WB, w_row - WB);
+#pragma unroll
+    for (int j = 0; j < AI; ++j) load_lds16(a_tile, a_bytes, dst + (wave * AI + j) * 1024, va[j], ka);
+#pragma unroll
+    for (int j = 0; j < WI; ++j) load_lds16(w_tile, w_bytes, dst + oW + (wave * WI + j) * 1024, vw[j], kw);
+#pragma unroll
+    for (int j = 0; j < SI; ++j)
+      load_lds4(sc + ((int64_t)min(kt, nk - 1) * SW + j) * rows + s_row, 256, dst + oS + (j * 2 * T + 64 * wave) * 4,
+                4u * (uint32_t)lane);
+  };
+
+  // fragments: lane l holds row l % 32 of a tile, h = l / 32
+  const int r = lane & 31, h = lane >> 5;
+  const int a_base = (wm * MT * 32 + r) * AB, w_base = oW + (wn * NT * 32 + r) * WB;
+  struct Frags {
+    i32x8 a[MT];
+    uint4 w[NT];
+  };
+  struct Scales {
+    uint32_t a[MT][SW], w[NT][SW];
+  };
+  auto read_frags = [&](Frags& f, const uint8_t* tile, int step) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      f.w[i] = *(const uint4*)(tile + w_base + i * 32 * WB +
+                               16 * ((2 * step + h) ^ (WB == 128 ? swz8(r) : swz4(r))));
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const uint8_t* p = tile + a_base + i * 32 * AB;
+      if constexpr (AF == kMxFp8)
+        f.a[i] = both4(*(const uint4*)(p + 16 * ((4 * step + h) ^ swz8(r))),
+                       *(const uint4*)(p + 16 * ((4 * step + 2 + h) ^ swz8(r))));
+      else
+        f.a[i] = lo4(*(const uint4*)(p + 16 * ((2 * step + h) ^ swz8(r))));
+    }
+  };
+  auto read_scales = [&](Scales& s, const uint8_t* tile) {
+    const uint32_t* p = (const uint32_t*)(tile + oS);
+#pragma unroll
+    for (int w = 0; w < SW; ++w) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) s.a[i][w] = p[w * 2 * T + wm * MT * 32 + 32 * i + r];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) s.w[i][w] = p[w * 2 * T + T + wn * NT * 32 + 32 * i + r];
+    }
+  };
+  auto own_bytes = [&](Scales& s, const Scales& raw) {  // the lane's blocks to bytes 0 and 2
+#pragma unroll
+    for (int w = 0; w < SW; ++w) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) s.a[i][w] = raw.a[i][w] >> (8 * h);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) s.w[i][w] = raw.w[i][w] >> (8 * h);
+    }
+  };
+  f32x16 acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  auto products = [&](const Frags& f, const Scales& s, int step) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        acc[i][j] = mfma_mx32<AF>(lo4(f.w[i]), f.a[j], acc[i][j], (int)s.w[i][step / 2], (int)s.a[j][step / 2],
+                                  step % 2);
+  };
+
+  Frags f0, f1;
+  Scales c0, c1;
+  load_stage(s0, 0);
+  load_stage(s1, 1);
+  if constexpr (SL == 3) load_stage(s2, 2);
+  wait_loads<ND*(SL - 1)>();
+  __builtin_amdgcn_s_barrier();
+  read_scales(c1, s0);
+  read_frags(f0, s0, 0);
+
+  // Stage kt (array C), its step-0 fragments and scales read.  At the barrier, ahead of the last step, every
+  // wave has read the whole stage (lgkmcnt 0) and stage kt + 1 (array X) has landed, only loads of later
+  // stages being younger: C may be filled again.  Loads past the last stage repeat it.
+#define AWQ_MX_STEP(F, G, C, S)          \
+  read_frags(G, C, S + 1);               \
+  products(F, c0, S);                    \
+  interleave<NR, 0>();                   \
+  __builtin_amdgcn_sched_barrier(0);
+#define AWQ_MX_STAGE(C, X)                       \
+  {                                              \
+    own_bytes(c0, c1);                           \
+    AWQ_MX_STEP(f0, f1, C, 0)                    \
+    if constexpr (ST == 4) {                     \
+      AWQ_MX_STEP(f1, f0, C, 1)                  \
+      AWQ_MX_STEP(f0, f1, C, 2)                  \
+    }                                            \
+    wait_loads<ND*(SL - 2)>();                   \
+    __builtin_amdgcn_s_barrier();                \
+    __builtin_amdgcn_sched_barrier(0);           \
+    load_stage(C, kt + SL);                      \
+    read_scales(c1, X);                          \
+    read_frags(f0, X, 0);                        \
+    products(f1, c0, ST - 1);                    \
+    interleave<NR + SW * (MT + NT) / 2, ND>();   \
+    __builtin_amdgcn_sched_barrier(0);           \
+    ++kt;                                        \
+  }
+  int kt = 0;
+  if constexpr (SL == 3) {
+    while (kt + 3 <= nk) {
+      AWQ_MX_STAGE(s0, s1)
+      AWQ_MX_STAGE(s1, s2)
+      AWQ_MX_STAGE(s2, s0)
+    }
+    if (kt < nk) AWQ_MX_STAGE(s0, s1)
+    if (kt < nk) AWQ_MX_STAGE(s1, s2)
+  } else {
+    while (kt + 2 <= nk) {
+      AWQ_MX_STAGE(s0, s1)
+      AWQ_MX_STAGE(s1, s0)
+    }
+    if (kt < nk) AWQ_MX_STAGE(s0, s1)
+  }
+#undef AWQ_MX_STAGE
+#undef AWQ_MX_STEP
+  wait_loads<0>();  // none may land after the block has given its LDS back
+  __builtin_amdgcn_s_barrier();
+  if constexpr (SL == 3)
+    store_tile<YT, MT, NT, NW, SB>(acc, s0, s1, s2, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M, N, Y, ld_y);
+  else  // the second half of the second array takes the third's place
+    store_tile<YT, MT, NT, NW, SB / 2>(acc, s0, s1, s1 + SB / 2, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M,
+                                       N, Y, ld_y);
 }
 
 // Y = sum over z, in order, of part[z] (fp32 [M, ld_p] each): 4 outputs a thread
@@ -494,7 +745,7 @@ static MxTiling mx_tiling(int a_fmt, int64_t M, int64_t N, int64_t K) {
     const double blocks = (double)((M + tile - 1) / tile) * (double)((N + tile - 1) / tile);
     for (int s = 1; s <= 8 && nk / s >= 6; ++s) {
       const int split = (nk + s - 1) / s, ranges = (nk + split - 1) / split;
-      if (s > 1 && (ranges != s || blocks * s > 512)) continue;
+      if (s > 1 && (ranges != s || blocks * s > 512 || tile == 256)) continue;
       const double rounds = ceil(blocks * ranges / 256);
       double t = 3 + split * (tile == 64 && rounds == 1 ? 0.27 : per * rounds);
       if (ranges > 1) t += 2.5 + ranges * (double)M * (double)N * 8 / 5e6;
@@ -505,8 +756,15 @@ static MxTiling mx_tiling(int a_fmt, int64_t M, int64_t N, int64_t K) {
 }
 static int64_t part_ld(int64_t N) { return (N + 3) / 4 * 4; }
 
+static int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
+static int64_t big_scale_words(int a_fmt, int64_t M, int64_t N, int64_t K) {
+  const int64_t ks = a_fmt == kMxFp8 ? kBigStage<kMxFp8> : kBigStage<kMxFp4>;
+  return (tiles_of(M, kBigTile) + tiles_of(N, kBigTile)) * kBigTile * ((K + ks - 1) / ks * (ks / 128));
+}
+
 size_t mx_matmul_workspace(int a_fmt, int64_t M, int64_t N, int64_t K) {
   const MxTiling t = mx_tiling(a_fmt, M, N, K);
+  if (t.tile == kBigTile) return (size_t)big_scale_words(a_fmt, M, N, K) * sizeof(uint32_t);
   return t.ranges > 1 ? (size_t)t.ranges * M * part_ld(N) * sizeof(float) : 0;
 }
 
@@ -526,15 +784,26 @@ static void few_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uin
 template <int AF, int YT>
 static void tile_launch(const MxTiling& t, const uint8_t* A, const uint8_t* as, int64_t M, const uint8_t* W,
                         const uint8_t* ws, int64_t N, int64_t K, void* Y, int64_t ld_y, hipStream_t stream) {
-  const int n_mt = (int)((M + t.tile - 1) / t.tile), n_nt = (int)((N + t.tile - 1) / t.tile);
+  const int n_mt = (int)tiles_of(M, t.tile), n_nt = (int)tiles_of(N, t.tile);
   const dim3 g((unsigned)(n_mt * n_nt), (unsigned)t.ranges);
 #define AWQ_TILE(BM, BN, WM, WN, OCC)                                                                               \
   mx_tile_kernel<AF, YT, BM, BN, WM, WN, OCC><<<g, WM * WN * kWave, 0, stream>>>(A, as, M, W, ws, N, K, n_mt, n_nt, 8, \
                                                                                t.split, Y, ld_y)
   if (t.tile == 64) AWQ_TILE(64, 64, 2, 2, 4);
-  else if (t.tile == 128) AWQ_TILE(128, 128, 2, 2, 2);
-  else AWQ_TILE(256, 256, 4, 2, 2);
+  else AWQ_TILE(128, 128, 2, 2, 2);
 #undef AWQ_TILE
+}
+
+template <int AF, int YT>
+static void big_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uint8_t* W, const uint8_t* ws, int64_t N,
+                       int64_t K, void* Y, int64_t ld_y, uint32_t* sc, hipStream_t stream) {
+  constexpr int SB = kBigStage<AF> / kMxBlock;
+  const int n_mt = (int)tiles_of(M, kBigTile), n_nt = (int)tiles_of(N, kBigTile), kb = (int)(K / kMxBlock);
+  const int64_t m_pad = (int64_t)n_mt * kBigTile, rows = m_pad + (int64_t)n_nt * kBigTile;
+  stage_scales_kernel<SB><<<dim3((unsigned)(rows / 256), (unsigned)((kb + 15) / 16)), 256, 0, stream>>>(
+      as, M, ws, N, kb, m_pad, rows, sc);
+  mx_big_kernel<AF, YT><<<(unsigned)(n_mt * n_nt), 512, 0, stream>>>(A, M, W, N, K, sc, m_pad, rows, n_mt, n_nt,
+                                                                    AF == kMxFp8 ? 4 : 8, Y, ld_y);
 }
 
 template <int AF, int YT>
@@ -543,6 +812,8 @@ static void product_launch(const uint8_t* A, const uint8_t* as, int64_t M, const
   const MxTiling t = mx_tiling(AF, M, N, K);
   if (t.tile == 0) {
     few_launch<AF>(A, as, M, W, ws, N, K, Y, ld_y, YT, stream);
+  } else if (t.tile == kBigTile) {
+    big_launch<AF, YT>(A, as, M, W, ws, N, K, Y, ld_y, (uint32_t*)part, stream);
   } else if (t.ranges == 1) {
     tile_launch<AF, YT>(t, A, as, M, W, ws, N, K, Y, ld_y, stream);
   } else {

@@ -533,3 +533,14 @@ def test_silu_mul_every_gate(A):
         assert np.all(np.abs(got[~keep]) <= np.abs(y[~keep]) * 1.1 + 2.0 ** -127)
         sel = torch.from_numpy(keep).cuda()
         check_near([t.view(torch.uint8)[sel].view(t.dtype) for t in out], "fp8", y[keep], 8 * U)
+
+
+@pytest.mark.parametrize("M,N,K,fmt,dtype", [
+    (1000, 12250, 384, "fp8", "bf16"), (1000, 12250, 416, "fp8", "f16"), (1024, 12288, 608, "fp8", "bf16"),
+    (1023, 12288, 1088, "fp8", "f16"), (1000, 12250, 384, "fp4", "f32"), (1000, 12249, 416, "fp4", "bf16"),
+    (1024, 12288, 608, "fp4", "f16"), (1000, 12250, 704, "fp4", "f32"), (900, 12250, 1088, "fp4", "bf16"),
+])
+def test_product_large(A, M, N, K, fmt, dtype):
+    """Enough outputs for the largest tiles; lengths that leave 1, 2, 3 blocks and more in the last stage."""
+    say(f"mx_matmul large {M}x{N}x{K} {fmt} {dtype}")
+    check_product(A, M, N, K, fmt, dtype, ld_y=N + 3)
