@@ -613,18 +613,30 @@ _FLOATS = {torch.float16: AWQ_F16, torch.bfloat16: AWQ_BF16, torch.float32: AWQ_
 
 class _MxPrepared(_Prepared):
     """A prepared call on the device of `like`: its current stream unless one is given, and that
-    device made current around the launch when it is not."""
+    device made current around the launch when it is not.  The arguments are kept as C values for
+    a function without argument types, which spares their conversion in every run."""
 
     def _place(self, like: torch.Tensor, stream) -> int:
         self._device = like.device
+        self._alone = torch.cuda.device_count() == 1
         return torch.cuda.current_stream(like.device).cuda_stream if stream is None else stream.cuda_stream
 
+    def _bind(self, *args) -> None:
+        types = getattr(lib(), self._fn).argtypes
+        if len(types) != len(args):
+            raise TypeError(f"{self._fn} takes {len(types)} arguments, got {len(args)}")
+        self._f = lib()[self._fn]
+        self._f.restype = ctypes.c_int32
+        self._args = tuple(t(a) for t, a in zip(types, args))
+
     def launch(self) -> None:
-        if torch.cuda.current_device() == self._device.index:
-            _check(self._f(*self._args))
+        if self._alone or torch.cuda.current_device() == self._device.index:
+            st = self._f(*self._args)
         else:
             with torch.cuda.device(self._device):
-                _check(self._f(*self._args))
+                st = self._f(*self._args)
+        if st != AWQ_OK:
+            _check(st)
 
 
 def _mx_fmt(fmt: str) -> int:

@@ -33,126 +33,7 @@ __device__ __forceinline__ void store_y(void* Y, int64_t at, float v, int y_dtyp
   else ((uint16_t*)Y)[at] = (uint16_t)(y_dtype == 0 ? f2x<0>(v) : f2x<1>(v));
 }
 
-// ---------------------------------------------------------------------------
-// Few tokens: a block holds 16 outputs and 16 MT tokens.  Its 8 waves take chunks
-// of 512 K in turn (four MFMA steps; 64 lanes read 16 rows of 64 bytes a load),
-// the next chunk's weights on their way while one is multiplied; their sums are
-// added in wave order through LDS.
-// ---------------------------------------------------------------------------
-constexpr int kFewWaves = 8;
-constexpr int kFewBlocks = 16;  // scale blocks of a chunk
-
-// The 16 scale bytes of a row's chunk c; zeros past the row's end
-__device__ __forceinline__ uint4 few_scales(const uint8_t* row, int c, int kb) {
-  if (kFewBlocks * (c + 1) <= kb) return ld_any<uint4>(row + kFewBlocks * c);
-  uint32_t v[4] = {0, 0, 0, 0};
-  for (int i = 0; i < kb - kFewBlocks * c; ++i) {
-    const uint32_t b = (uint32_t)row[kFewBlocks * c + i] << (8 * (i & 3));
-#pragma unroll
-    for (int d = 0; d < 4; ++d) v[d] |= d == i >> 2 ? b : 0;
-  }
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
-// 16 bytes of codes that hold values of block b, zeros past the row's end
-__device__ __forceinline__ uint4 few_codes(const uint8_t* p, int b, int kb) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (b < kb) v = *(const uint4*)p;
-  return v;
-}
-
-template <int AF, int MT>
-__global__ __launch_bounds__(kFewWaves * kWave, 2) void mx_few_kernel(const uint8_t* __restrict__ A,
-                                                                     const uint8_t* __restrict__ as, int64_t M,
-                                                                     const uint8_t* __restrict__ W,
-                                                                     const uint8_t* __restrict__ ws, int64_t N,
-                                                                     int64_t K, void* __restrict__ Y, int64_t ld_y,
-                                                                     int y_dtype) {
-  __shared__ float red[kFewWaves][MT * 16][17];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, h = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (16 * MT);
-  const int kb = (int)(K / kMxBlock), nc = (kb + kFewBlocks - 1) / kFewBlocks;
-  const int64_t n = n0 + r < N ? n0 + r : N - 1;  // rows past the end repeat the last one, unused
-  const uint8_t* wr = W + n * (K / 2) + 16 * h;
-  const uint8_t* wsr = ws + n * kb;
-  const uint8_t* ar[MT];
-  const uint8_t* asr[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int64_t m = m0 + 16 * t + r < M ? m0 + 16 * t + r : M - 1;
-    ar[t] = A + m * (AF == kMxFp8 ? K : K / 2) + 16 * h;
-    asr[t] = as + m * kb;
-  }
-  f32x4 acc[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = (f32x4){0, 0, 0, 0};
-
-  uint4 w[4], sw;
-  auto load_w = [&](int c) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = few_codes(wr + 256 * (int64_t)c + 64 * j, kFewBlocks * c + 4 * j + h, kb);
-    sw = few_scales(wsr, c, kb);
-  };
-  if (wave < nc) load_w(wave);
-  for (int c = wave; c < nc; c += kFewWaves) {
-    uint4 wc[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) wc[j] = w[j];
-    const uint32_t swc[4] = {sw.x >> (8 * h), sw.y >> (8 * h), sw.z >> (8 * h), sw.w >> (8 * h)};
-    if (c + kFewWaves < nc) load_w(c + kFewWaves);
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const uint4 sa = few_scales(asr[t], c, kb);
-      const uint32_t sac[4] = {sa.x >> (8 * h), sa.y >> (8 * h), sa.z >> (8 * h), sa.w >> (8 * h)};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int b = kFewBlocks * c + 4 * j;
-        i32x8 a;
-        if constexpr (AF == kMxFp8) {
-          const uint8_t* p = ar[t] + 32 * (int64_t)b;
-          a = both4(few_codes(p, b + h / 2, kb), few_codes(p + 64, b + 2 + h / 2, kb));
-        } else {
-          a = lo4(few_codes(ar[t] + 16 * (int64_t)b, b + h, kb));
-        }
-        acc[t] = mfma_mx<AF>(lo4(wc[j]), a, acc[t], (int)swc[j], (int)sac[j]);
-      }
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) red[wave][16 * t + r][4 * h + e] = acc[t][e];
-  __syncthreads();
-  for (int i = threadIdx.x; i < MT * 256; i += kFewWaves * kWave) {
-    const int t = i >> 4, o = i & 15;
-    float v = 0.0f;
-#pragma unroll
-    for (int q = 0; q < kFewWaves; ++q) v += red[q][t][o];
-    if (m0 + t < M && n0 + o < N) store_y(Y, (m0 + t) * ld_y + n0 + o, v, y_dtype);
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Many tokens: tiles of BM tokens x BN outputs staged through LDS.
-//
-// K advances in stages of 128 through a ring of three LDS slots, filled by direct
-// loads (16 bytes a lane, no registers) two stages ahead.  A stage is two steps of
-// v_mfma_scale_f32_32x32x64_f8f6f4; the fragments of a step are read from LDS
-// while the matrix cores work on the step before, across the stage boundary too:
-// the block's one barrier a stage stands between the two steps, where the next
-// stage's loads must have landed.
-// ---------------------------------------------------------------------------
-template <int AF>
-__device__ __forceinline__ f32x16 mfma_mx32(const i32x8 w, const i32x8 a, f32x16 c, int ws, int as, int step) {
-  // scale bytes 0 and 2 of the registers: the lane's block of step 0 and 1
-  return step == 0
-             ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, c, 4, AF == kMxFp8 ? 0 : 4, 0, ws, 0, as)
-             : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, c, 4, AF == kMxFp8 ? 0 : 4, 2, ws, 2, as);
-}
-
 typedef __attribute__((address_space(3))) void* mx_lds_ptr;
-constexpr int kMxXcds = 8;
-constexpr int kMxStage = 128;   // K per stage
 constexpr uint32_t kMxOut = 0x80000000u;  // an offset past the range of every tile's buffer (256 rows of <= 2^22 bytes)
 
 // 16-byte chunk c of an LDS row sits at slot c ^ swz(row): 8 consecutive rows
@@ -180,6 +61,211 @@ __device__ __forceinline__ void load_lds4(const void* base, uint32_t bytes, uint
       __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000), (mx_lds_ptr)dst, 4,
       off, 0, 0, 0);
 }
+
+// ---------------------------------------------------------------------------
+// Few tokens, bound by reading the weights: a block holds 16 NT outputs and AR
+// tokens.  Its 8 waves take chunks of ST MFMA steps of 128 K in turn, the next
+// chunk's loads on their way while one is multiplied, and their sums are added in
+// wave order through LDS.  The matrix cores want 16 lanes side by side in 16 rows;
+// loaded like that, every lane is an access of its own (measured at one token,
+// 24576 x 4096: 14.3 us).  So the weights, used once, are read 64 bytes of a row by
+// 4 lanes and turned by lane permutations (12.5 us), and the activations go through
+// LDS, each wave's through buffers of its own and by direct loads of whole rows,
+// which cost nothing for rows past the last token (16 tokens, 4096 x 12288: 11.7 us
+// loaded by the lanes, 8.3 us so).  For up to 4 tokens 4 LDS rows leave room for
+// more blocks (11.8 us, 4.5 TB/s).
+// ---------------------------------------------------------------------------
+constexpr int kFewWaves = 8;
+
+// The scale bytes of the 4 ST blocks of a row's chunk c; zeros past the row's end
+template <int ST>
+struct FewScales {
+  uint32_t v[ST];
+};
+template <int ST>
+__device__ __forceinline__ FewScales<ST> few_scales(const uint8_t* row, int c, int kb) {
+  if (4 * ST * (c + 1) <= kb) return ld_any<FewScales<ST>>(row + 4 * ST * c);
+  FewScales<ST> s = {};
+  for (int i = 0; i < kb - 4 * ST * c; ++i) {
+    const uint32_t b = (uint32_t)row[4 * ST * c + i] << (8 * (i & 3));
+#pragma unroll
+    for (int d = 0; d < ST; ++d) s.v[d] |= d == i >> 2 ? b : 0;
+  }
+  return s;
+}
+
+// AR: LDS rows of activations (4, or 16 a tile of tokens); with 4 the lanes of the 12 other rows read these
+template <int AF, int AR, int NT, int ST, int OCC>
+__global__ __launch_bounds__(kFewWaves * kWave, OCC) void mx_few_kernel(const uint8_t* __restrict__ A,
+                                                                       const uint8_t* __restrict__ as, int64_t M,
+                                                                       const uint8_t* __restrict__ W,
+                                                                       const uint8_t* __restrict__ ws, int64_t N,
+                                                                       int64_t K, void* __restrict__ Y, int64_t ld_y,
+                                                                       int y_dtype) {
+  constexpr int MT = (AR + 15) / 16;                     // tiles of 16 tokens
+  constexpr int RB = (AF == kMxFp8 ? 128 : 64) * ST;     // bytes of a row's chunk
+  constexpr int CR = RB / 16;                            // 16-byte pieces of it
+  constexpr int DI = AR * RB / 1024;                     // direct loads of a chunk, a KiB each
+  static_assert(DI >= 1, "whole loads");
+  constexpr int BS = AR * RB > 4 * NT * MT * 16 * 17 ? AR * RB : 4 * NT * MT * 16 * 17;  // a wave's buffer: chunk, later sums
+  __shared__ __attribute__((aligned(1024))) uint8_t b0[kFewWaves][(BS + 1023) / 1024 * 1024];
+  __shared__ __attribute__((aligned(1024))) uint8_t b1[kFewWaves][AR * RB];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, h = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * NT), m0 = (int64_t)blockIdx.y * AR;
+  const int kb = (int)(K / kMxBlock), nc = (kb + 4 * ST - 1) / (4 * ST);
+  const int m_rows = (int)(M - m0 < AR ? M - m0 : AR);
+  const uint32_t a_row = (uint32_t)(AF == kMxFp8 ? K : K / 2);
+  // weights: 4 lanes side by side read 64 bytes of a row, and turn() hands each lane the piece that the
+  // matrix cores want of it.  Rows past the end repeat the last one, unused.
+  const uint8_t* wr[NT];
+  const uint8_t* wsr[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int64_t nl = n0 + 16 * i + lane / 4, n = n0 + 16 * i + r;
+    wr[i] = W + (nl < N ? nl : N - 1) * (K / 2) + 16 * (lane % 4);
+    wsr[i] = ws + (n < N ? n : N - 1) * kb;
+  }
+  auto turn = [&](const uint4 v) {
+    const int from = 4 * (4 * r + h);
+    return lo4(make_uint4((uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.x),
+                          (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.y),
+                          (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.z),
+                          (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v.w)));
+  };
+  const uint8_t* asr[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) asr[t] = as + (m0 + min(16 * t + r, m_rows - 1)) * kb;
+  const uint8_t* a_tile = A + m0 * a_row;
+  const uint32_t a_bytes = (uint32_t)m_rows * a_row;
+  // piece c of row m sits at slot c ^ (m % 16) of its LDS row, or c ^ swz8(m) of one of 8 pieces
+  uint32_t va[DI], vc[DI];  // offset of the lane's row (past the range for rows past the end), of its piece
+#pragma unroll
+  for (int j = 0; j < DI; ++j) {
+    const int piece = kWave * j + lane, m = piece / CR;
+    va[j] = m < m_rows ? (uint32_t)m * a_row : kMxOut;
+    vc[j] = 16u * (uint32_t)(piece % CR ^ (CR >= 16 ? m & 15 : swz8(m)));
+  }
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[t][i] = (f32x4){0, 0, 0, 0};
+
+  struct Chunk {
+    uint4 w[NT][ST];
+    FewScales<ST> sw[NT], sa[MT];
+  };
+  // Loads of a whole chunk, the direct ones first.  A last chunk may take fewer of the others; those of the
+  // chunk before it that a wait for all but NL then leaves out are loads to registers, which the compiler
+  // waits for itself.
+  constexpr int NL = DI + NT * (ST + 1) + MT;
+  static_assert(NT * (ST + 1) + MT >= NT * (ST - 1), "what a last chunk may lack");
+  auto load_chunk = [&](Chunk& f, uint8_t* buf, int c) {
+    const uint32_t k = (uint32_t)c * RB;
+#pragma unroll
+    for (int j = 0; j < DI; ++j)  // pieces past the row's end: past the range too
+      load_lds16(a_tile, a_bytes, buf + 1024 * j, k + vc[j] < a_row ? va[j] + k + vc[j] : kMxOut, 0);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int j = 0; j < ST; ++j) {
+        f.w[i][j] = make_uint4(0, 0, 0, 0);
+        if (4 * (ST * c + j) + lane % 4 < kb) f.w[i][j] = *(const uint4*)(wr[i] + 64 * (int64_t)(ST * c + j));
+      }
+      f.sw[i] = few_scales<ST>(wsr[i], c, kb);
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) f.sa[t] = few_scales<ST>(asr[t], c, kb);
+  };
+  auto multiply = [&](const Chunk& f, const uint8_t* buf) {
+    i32x8 w[NT][ST];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < ST; ++j) w[i][j] = turn(f.w[i][j]);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int m = AR < 16 ? r % AR : 16 * t + r;
+      auto piece = [&](int c) { return *(const uint4*)(buf + m * RB + 16 * (c ^ (CR >= 16 ? m & 15 : swz8(m)))); };
+#pragma unroll
+      for (int j = 0; j < ST; ++j) {
+        i32x8 a;
+        if constexpr (AF == kMxFp8) a = both4(piece(8 * j + h), piece(8 * j + 4 + h));
+        else a = lo4(piece(4 * j + h));
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          acc[t][i] = mfma_mx<AF>(w[i][j], a, acc[t][i], (int)(f.sw[i].v[j] >> (8 * h)),
+                                  (int)(f.sa[t].v[j] >> (8 * h)));
+      }
+    }
+  };
+  Chunk f0, f1;
+  int c = wave;
+  if (c < nc) {
+    load_chunk(f0, b0[wave], c);
+    for (;;) {
+      // chunk c in f0 / b0; before its buffer is filled again its reads are done (lgkmcnt 0)
+      if (c + kFewWaves < nc) {
+        load_chunk(f1, b1[wave], c + kFewWaves);
+        wait_loads<NL>();
+      } else {
+        wait_loads<0>();
+      }
+      multiply(f0, b0[wave]);
+      if ((c += kFewWaves) >= nc) break;
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+      if (c + kFewWaves < nc) {
+        load_chunk(f0, b0[wave], c + kFewWaves);
+        wait_loads<NL>();
+      } else {
+        wait_loads<0>();
+      }
+      multiply(f1, b1[wave]);
+      if ((c += kFewWaves) >= nc) break;
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+    }
+  }
+  // the wave's sums, in its first buffer's place
+  float* sums = (float*)b0[wave];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sums[((t * NT + i) * 16 + r) * 17 + 4 * h + e] = acc[t][i][e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < MT * NT * 256; i += kFewWaves * kWave) {
+    const int m = i / (16 * NT), o = i % (16 * NT);
+    const int at = ((m / 16 * NT + o / 16) * 16 + m % 16) * 17 + o % 16;
+    float v = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kFewWaves; ++q) v += ((const float*)b0[q])[at];
+    if (m0 + m < M && m < AR && n0 + o < N) store_y(Y, (m0 + m) * ld_y + n0 + o, v, y_dtype);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens: tiles of BM tokens x BN outputs staged through LDS.
+//
+// K advances in stages of 128 through a ring of three LDS slots, filled by direct
+// loads (16 bytes a lane, no registers) two stages ahead.  A stage is two steps of
+// v_mfma_scale_f32_32x32x64_f8f6f4; the fragments of a step are read from LDS
+// while the matrix cores work on the step before, across the stage boundary too:
+// the block's one barrier a stage stands between the two steps, where the next
+// stage's loads must have landed.
+// ---------------------------------------------------------------------------
+template <int AF>
+__device__ __forceinline__ f32x16 mfma_mx32(const i32x8 w, const i32x8 a, f32x16 c, int ws, int as, int step) {
+  // scale bytes 0 and 2 of the registers: the lane's block of step 0 and 1
+  return step == 0
+             ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, c, 4, AF == kMxFp8 ? 0 : 4, 0, ws, 0, as)
+             : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, c, 4, AF == kMxFp8 ? 0 : 4, 2, ws, 2, as);
+}
+
+constexpr int kMxXcds = 8;
+constexpr int kMxStage = 128;   // K per stage
+
 
 // Issue order of half a stage: two LDS reads and one or two direct loads behind each MFMA, so that
 // they are under way early and the matrix cores never wait for a burst of them
@@ -299,8 +385,9 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
   const int m_rows = (int)(M - m0 < BM ? M - m0 : BM), n_rows = (int)(N - n0 < BN ? N - n0 : BN);
 
   // direct loads: lane i of load j fills 16 bytes i of the wave's j-th KiB.  Rows past the end are out of
-  // the buffer's range and read as zeros (their results are not stored).  A last stage that K does not fill takes the row's last
-  // 128 values instead: the scales of those already summed are 0 on both sides, so that they add 0.
+  // the buffer's range and read as zeros (their results are not stored).  A last stage that K does not fill
+  // takes the row's last 128 values instead: the scales of those already summed are 0 on both sides, so that
+  // they add 0.
   const uint8_t* a_tile = A + m0 * a_row;
   const uint8_t* w_tile = W + n0 * w_row;
   const uint32_t a_bytes = (uint32_t)m_rows * a_row, w_bytes = (uint32_t)n_rows * w_row;
@@ -465,29 +552,26 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Large products: 256 x 256 tiles, where the loads that reach the second-level
-// cache bound the kernel (measured with everything else left out: 297 us of the
-// 388 us of an 8-bit 8192^3 product, 252 of 301 us of a 4-bit one).  So every row
-// of a stage is a whole 128-byte line where LDS allows it: a stage is 128 K in
-// three slots for 8-bit activations (W rows then half a line) and 256 K in two
-// slots for 4-bit ones; and the scales, whose bytes of a stage lie in a line of
-// their own for each row, are first laid out stage by stage (stage_scales), so
-// that a stage takes 16 or 32 lines of them instead of 512.
+// Large products of 4-bit activations: 256 x 256 tiles in stages of 256 K.  The
+// loads that reach the second-level cache bound them (8192^3 in stages of 128 K:
+// 301 us, of which 252 remain with the loads alone), so every row of a stage is a
+// whole 128-byte line, in two LDS slots; and the scales, whose bytes of a stage
+// lie in a line of their own for each row, are first laid out stage by stage
+// (stage_scales), so that a stage takes 32 lines of them instead of 512.  264 us,
+// 4.2 PFLOP/s; the matrix cores alone take 203 us at the clock that they leave.
+// 8-bit activations gain 3% from the latter alone and lose it to the extra pass
+// below 300 us: they stay with mx_tile_kernel.
 // ---------------------------------------------------------------------------
-template <int AF>
-constexpr int kBigStage = AF == kMxFp8 ? 128 : 256;
-template <int AF>
-constexpr int kBigSlots = AF == kMxFp8 ? 3 : 2;
-constexpr int kBigTile = 256;
+constexpr int kBigStage = 256, kBigTile = 256;
 
-// out[w][row] (rows: the A rows, then the W rows, each padded to whole tiles): word w % (SB / 4) of stage
-// w / (SB / 4), the scale bytes of SB = K / 32 blocks.  A last stage that K does not fill holds the row's
-// last SB blocks, 0 in the place of those of earlier stages; padded rows hold 0.
-template <int SB>
+// out[w][row] (rows: the A rows, then the W rows, each padded to whole tiles): word w % 2 of stage w / 2, 4
+// scale bytes each.  A last stage that K does not fill holds the row's last 8 blocks, 0 in the place of those
+// of earlier stages; padded rows hold 0.
 __global__ __launch_bounds__(256) void stage_scales_kernel(const uint8_t* __restrict__ as, int64_t M,
                                                            const uint8_t* __restrict__ ws, int64_t N, int kb,
                                                            int64_t m_pad, int64_t rows, uint32_t* __restrict__ out) {
   const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;  // rows is a multiple of 256
+  constexpr int SB = kBigStage / kMxBlock;                      // blocks of a stage
   const bool is_a = row < m_pad;
   const int64_t r = is_a ? row : row - m_pad;
   const bool live = r < (is_a ? M : N);
@@ -512,25 +596,22 @@ __global__ __launch_bounds__(256) void stage_scales_kernel(const uint8_t* __rest
     if (s0 + i * 4 / SB < n_stage) out[(int64_t)(s0 * (SB / 4) + i) * rows + row] = v[i];
 }
 
-template <int AF, int YT>
+template <int YT>
 __global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restrict__ A, int64_t M,
                                                         const uint8_t* __restrict__ W, int64_t N, int64_t K,
                                                         const uint32_t* __restrict__ sc, int64_t m_pad, int64_t rows,
                                                         int n_mt, int n_nt, int group_m, void* __restrict__ Y,
                                                         int64_t ld_y) {
-  constexpr int KS = kBigStage<AF>, SL = kBigSlots<AF>, T = kBigTile;
+  constexpr int T = kBigTile;
   constexpr int WM = 4, WN = 2, NW = 8, MT = T / WM / 32, NT = T / WN / 32;
-  constexpr int AB = 128, WB = KS / 2;                 // bytes of a row's stage
-  constexpr int SW = KS / 128;                         // scale words of a row's stage
-  constexpr int AI = T * AB / 1024 / NW, WI = T * WB / 1024 / NW, SI = SW;  // direct loads a wave and stage
-  constexpr int ND = AI + WI + SI;
-  constexpr int ST = KS / 64;                          // MFMA steps a stage
-  constexpr int NR = NT + MT * (AF == kMxFp8 ? 2 : 1);  // LDS reads of a step's fragments
-  constexpr int oW = T * AB, oS = oW + T * WB, SB = oS + SW * 2 * T * 4;
+  constexpr int RB = kBigStage / 2;                    // bytes of a row's stage
+  constexpr int DI = T * RB / 1024 / NW;               // direct loads of codes a wave and stage, for each operand
+  constexpr int SW = 2;                                // scale words of a row's stage
+  constexpr int NR = NT + MT;                          // LDS reads of a step's fragments
+  constexpr int oW = T * RB, oS = 2 * T * RB, SB = oS + SW * 2 * T * 4;
   // one array a slot (A tile, W tile, scale words): fragment reads then visibly do not touch the loads in flight
   __shared__ __attribute__((aligned(1024))) uint8_t s0[SB];
   __shared__ __attribute__((aligned(1024))) uint8_t s1[SB];
-  __shared__ __attribute__((aligned(1024))) uint8_t s2[SL == 3 ? SB : 16];
 
   int mt, nt;
   block_tile(n_mt, n_nt, group_m, &mt, &nt);
@@ -538,64 +619,53 @@ __global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restric
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int nk = (int)((K + KS - 1) / KS);
-  const uint32_t a_row = (uint32_t)(AF == kMxFp8 ? K : K / 2), w_row = (uint32_t)(K / 2);
+  const int nk = (int)((K + kBigStage - 1) / kBigStage);
+  const uint32_t row_bytes = (uint32_t)(K / 2);
   const int m_rows = (int)(M - m0 < T ? M - m0 : T), n_rows = (int)(N - n0 < T ? N - n0 : T);
 
   // direct loads: lane i of load j fills 16 bytes i of the wave's j-th KiB.  Rows past the end are out of
-  // the buffer's range and read as zeros.  A last stage that K does not fill takes the row's last KS values.
-  const uint8_t* a_tile = A + m0 * a_row;
-  const uint8_t* w_tile = W + n0 * w_row;
-  const uint32_t a_bytes = (uint32_t)m_rows * a_row, w_bytes = (uint32_t)n_rows * w_row;
-  uint32_t va[AI], vw[WI];
+  // the buffer's range and read as zeros.  A last stage that K does not fill takes the row's last 256
+  // values.
+  const uint8_t* a_tile = A + m0 * row_bytes;
+  const uint8_t* w_tile = W + n0 * row_bytes;
+  const uint32_t a_bytes = (uint32_t)m_rows * row_bytes, w_bytes = (uint32_t)n_rows * row_bytes;
+  uint32_t va[DI], vw[DI];
 #pragma unroll
-  for (int j = 0; j < AI; ++j) {
-    const int row = (wave * AI + j) * (1024 / AB) + lane / (AB / 16);
-    va[j] = row < m_rows ? (uint32_t)row * a_row + 16u * (uint32_t)(lane % (AB / 16) ^ swz8(row)) : kMxOut;
-  }
-#pragma unroll
-  for (int j = 0; j < WI; ++j) {
-    const int row = (wave * WI + j) * (1024 / WB) + lane / (WB / 16), c = lane % (WB / 16);
-    vw[j] = row < n_rows ? (uint32_t)row * w_row + 16u * (uint32_t)(c ^ (WB == 128 ? swz8(row) : swz4(row))) : kMxOut;
+  for (int j = 0; j < DI; ++j) {
+    const int row = (wave * DI + j) * 8 + lane / 8;
+    const uint32_t at = (uint32_t)row * row_bytes + 16u * (uint32_t)(lane % 8 ^ swz8(row));
+    va[j] = row < m_rows ? at : kMxOut;
+    vw[j] = row < n_rows ? at : kMxOut;
   }
   // scales: the wave's 64 of the tile's 256 + 256 rows; words past the last stage's are not read
   const int64_t s_row = wave < 4 ? m0 + 64 * wave : m_pad + n0 + 64 * (wave - 4);
   auto load_stage = [&](uint8_t* dst, int kt) {
-    const uint32_t ka = min((uint32_t)kt * AB, a_row - AB), kw = min((uint32_t)kt * WB, w_row - WB);
+    const uint32_t kt_off = min((uint32_t)kt * RB, row_bytes - RB);
 #pragma unroll
-    for (int j = 0; j < AI; ++j) load_lds16(a_tile, a_bytes, dst + (wave * AI + j) * 1024, va[j], ka);
+    for (int j = 0; j < DI; ++j) load_lds16(a_tile, a_bytes, dst + (wave * DI + j) * 1024, va[j], kt_off);
 #pragma unroll
-    for (int j = 0; j < WI; ++j) load_lds16(w_tile, w_bytes, dst + oW + (wave * WI + j) * 1024, vw[j], kw);
+    for (int j = 0; j < DI; ++j) load_lds16(w_tile, w_bytes, dst + oW + (wave * DI + j) * 1024, vw[j], kt_off);
 #pragma unroll
-    for (int j = 0; j < SI; ++j)
+    for (int j = 0; j < SW; ++j)
       load_lds4(sc + ((int64_t)min(kt, nk - 1) * SW + j) * rows + s_row, 256, dst + oS + (j * 2 * T + 64 * wave) * 4,
                 4u * (uint32_t)lane);
   };
 
   // fragments: lane l holds row l % 32 of a tile, h = l / 32
   const int r = lane & 31, h = lane >> 5;
-  const int a_base = (wm * MT * 32 + r) * AB, w_base = oW + (wn * NT * 32 + r) * WB;
+  const int a_base = (wm * MT * 32 + r) * RB, w_base = oW + (wn * NT * 32 + r) * RB;
   struct Frags {
-    i32x8 a[MT];
-    uint4 w[NT];
+    uint4 a[MT], w[NT];
   };
   struct Scales {
     uint32_t a[MT][SW], w[NT][SW];
   };
   auto read_frags = [&](Frags& f, const uint8_t* tile, int step) {
+    const int c = 16 * ((2 * step + h) ^ swz8(r));
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-      f.w[i] = *(const uint4*)(tile + w_base + i * 32 * WB +
-                               16 * ((2 * step + h) ^ (WB == 128 ? swz8(r) : swz4(r))));
+    for (int i = 0; i < NT; ++i) f.w[i] = *(const uint4*)(tile + w_base + i * 32 * RB + c);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const uint8_t* p = tile + a_base + i * 32 * AB;
-      if constexpr (AF == kMxFp8)
-        f.a[i] = both4(*(const uint4*)(p + 16 * ((4 * step + h) ^ swz8(r))),
-                       *(const uint4*)(p + 16 * ((4 * step + 2 + h) ^ swz8(r))));
-      else
-        f.a[i] = lo4(*(const uint4*)(p + 16 * ((2 * step + h) ^ swz8(r))));
-    }
+    for (int i = 0; i < MT; ++i) f.a[i] = *(const uint4*)(tile + a_base + i * 32 * RB + c);
   };
   auto read_scales = [&](Scales& s, const uint8_t* tile) {
     const uint32_t* p = (const uint32_t*)(tile + oS);
@@ -628,73 +698,59 @@ __global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restric
     for (int j = 0; j < MT; ++j)
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-        acc[i][j] = mfma_mx32<AF>(lo4(f.w[i]), f.a[j], acc[i][j], (int)s.w[i][step / 2], (int)s.a[j][step / 2],
-                                  step % 2);
+        acc[i][j] = mfma_mx32<kMxFp4>(lo4(f.w[i]), lo4(f.a[j]), acc[i][j], (int)s.w[i][step / 2],
+                                      (int)s.a[j][step / 2], step % 2);
   };
 
   Frags f0, f1;
   Scales c0, c1;
   load_stage(s0, 0);
   load_stage(s1, 1);
-  if constexpr (SL == 3) load_stage(s2, 2);
-  wait_loads<ND*(SL - 1)>();
+  wait_loads<2 * DI + SW>();
   __builtin_amdgcn_s_barrier();
   read_scales(c1, s0);
   read_frags(f0, s0, 0);
 
   // Stage kt (array C), its step-0 fragments and scales read.  At the barrier, ahead of the last step, every
-  // wave has read the whole stage (lgkmcnt 0) and stage kt + 1 (array X) has landed, only loads of later
-  // stages being younger: C may be filled again.  Loads past the last stage repeat it.
+  // wave has read the whole stage (lgkmcnt 0) and stage kt + 1 (array X) has landed: C may be filled again.
+  // Loads past the last stage repeat it.
 #define AWQ_MX_STEP(F, G, C, S)          \
   read_frags(G, C, S + 1);               \
   products(F, c0, S);                    \
   interleave<NR, 0>();                   \
   __builtin_amdgcn_sched_barrier(0);
-#define AWQ_MX_STAGE(C, X)                       \
-  {                                              \
-    own_bytes(c0, c1);                           \
-    AWQ_MX_STEP(f0, f1, C, 0)                    \
-    if constexpr (ST == 4) {                     \
-      AWQ_MX_STEP(f1, f0, C, 1)                  \
-      AWQ_MX_STEP(f0, f1, C, 2)                  \
-    }                                            \
-    wait_loads<ND*(SL - 2)>();                   \
-    __builtin_amdgcn_s_barrier();                \
-    __builtin_amdgcn_sched_barrier(0);           \
-    load_stage(C, kt + SL);                      \
-    read_scales(c1, X);                          \
-    read_frags(f0, X, 0);                        \
-    products(f1, c0, ST - 1);                    \
-    interleave<NR + SW * (MT + NT) / 2, ND>();   \
-    __builtin_amdgcn_sched_barrier(0);           \
-    ++kt;                                        \
+#define AWQ_MX_STAGE(C, X)                               \
+  {                                                      \
+    own_bytes(c0, c1);                                   \
+    AWQ_MX_STEP(f0, f1, C, 0)                            \
+    AWQ_MX_STEP(f1, f0, C, 1)                            \
+    AWQ_MX_STEP(f0, f1, C, 2)                            \
+    wait_loads<0>();                                     \
+    __builtin_amdgcn_s_barrier();                        \
+    __builtin_amdgcn_sched_barrier(0);                   \
+    load_stage(C, kt + 2);                               \
+    read_scales(c1, X);                                  \
+    read_frags(f0, X, 0);                                \
+    products(f1, c0, 3);                                 \
+    interleave<NR + SW * (MT + NT) / 2, 2 * DI + SW>();  \
+    __builtin_amdgcn_sched_barrier(0);                   \
+    ++kt;                                                \
   }
   int kt = 0;
-  if constexpr (SL == 3) {
-    while (kt + 3 <= nk) {
-      AWQ_MX_STAGE(s0, s1)
-      AWQ_MX_STAGE(s1, s2)
-      AWQ_MX_STAGE(s2, s0)
-    }
-    if (kt < nk) AWQ_MX_STAGE(s0, s1)
-    if (kt < nk) AWQ_MX_STAGE(s1, s2)
-  } else {
-    while (kt + 2 <= nk) {
-      AWQ_MX_STAGE(s0, s1)
-      AWQ_MX_STAGE(s1, s0)
-    }
-    if (kt < nk) AWQ_MX_STAGE(s0, s1)
+  while (kt + 2 <= nk) {
+    AWQ_MX_STAGE(s0, s1)
+    AWQ_MX_STAGE(s1, s0)
   }
+  if (kt < nk) AWQ_MX_STAGE(s0, s1)
 #undef AWQ_MX_STAGE
 #undef AWQ_MX_STEP
   wait_loads<0>();  // none may land after the block has given its LDS back
   __builtin_amdgcn_s_barrier();
-  if constexpr (SL == 3)
-    store_tile<YT, MT, NT, NW, SB>(acc, s0, s1, s2, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M, N, Y, ld_y);
-  else  // the second half of the second array takes the third's place
-    store_tile<YT, MT, NT, NW, SB / 2>(acc, s0, s1, s1 + SB / 2, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M,
-                                       N, Y, ld_y);
+  store_tile<YT, MT, NT, NW, SB / 2>(acc, s0, s1, s1 + SB / 2, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M, N,
+                                     Y, ld_y);
 }
+
+constexpr int kMaxRanges = 8;
 
 // Y = sum over z, in order, of part[z] (fp32 [M, ld_p] each): 4 outputs a thread
 template <int YT>
@@ -703,11 +759,14 @@ __global__ __launch_bounds__(256) void mx_reduce_kernel(const float* __restrict_
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t m = i / (ld_p / 4), n = 4 * (i % (ld_p / 4));
   if (m >= M) return;
-  float4 v = *(const float4*)(part + m * ld_p + n);
-  for (int z = 1; z < n_split; ++z) {
-    const float4 p = *(const float4*)(part + (z * M + m) * ld_p + n);
-    v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
-  }
+  float4 p[kMaxRanges];
+#pragma unroll
+  for (int z = 0; z < kMaxRanges; ++z)
+    if (z < n_split) p[z] = *(const float4*)(part + (z * M + m) * ld_p + n);
+  float4 v = p[0];
+#pragma unroll
+  for (int z = 1; z < kMaxRanges; ++z)
+    if (z < n_split) v.x += p[z].x, v.y += p[z].y, v.z += p[z].z, v.w += p[z].w;
   const float f[4] = {v.x, v.y, v.z, v.w};
   const int64_t at = m * ld_y + n;
   if (n + 4 <= N) {
@@ -722,33 +781,69 @@ __global__ __launch_bounds__(256) void mx_reduce_kernel(const float* __restrict_
   }
 }
 
+// Few tokens: LDS rows of activations, and 16-output tiles a block: two where that still leaves every
+// compute unit a block (16 tokens, us: 24576 x 4096 14.8 -> 11.9, 6144 x 4096 6.5 -> 5.5; but 4096 x 12288,
+// 256 tiles, 8.3 -> 10.5), one for up to 4 tokens (24576 x 4096 11.8, 12.9 with two).
+struct FewTile {
+  int rows, tiles;
+};
+static FewTile few_tile(int64_t M, int64_t N) {
+  if (M <= 4) return {4, 1};
+  const int rows = M <= 16 ? 16 : 32;
+  return {rows, (N + 15) / 16 * ((M + rows - 1) / rows) > 256 ? 2 : 1};
+}
+
 // The kernel, its tile and the number of K ranges of a product: the ones with the least estimated time.
-// Measured on 8-bit activations (4-bit ones rank alike), in us: a stage of K costs 0.27 / 0.5 / 1.3 a
-// block of 64 / 128 / 256 squared while no compute unit has more than one, and 0.21 / 0.5 / 1.3 for each
-// 256 blocks beyond; K ranges add 2.5 for the second launch and their fp32 sums written and read at 5 TB/s;
-// the few-token kernel reads the weights at 4.2 TB/s and the activations once per 16 outputs at 12 TB/s.
-// E.g. 24 x 4096 x 12288: few tokens 15.7, 64-tiles 29, in 4 ranges 12.6; 512 x 24576 x 4096: 82 / 52 / 46;
-// 2048 x 4096 x 4096: 55 / 34 / 38; 256 x 4096 x 4096: 12 / 16 / 23.
+// The estimates are fitted to measurements of N, K in {4096, 12288, 24576} x {1024, 4096, 12288} at 1 to 4096
+// tokens.  E.g. (us, 8 bits; few tokens / tiles of 64 / 128 / 256) 16 x 24576 x 4096: 11.9 / 14.4 / - / -;
+// 24 x 4096 x 12288: 10.7 / 11.3 in 8 ranges / - / -; 256 x 4096 x 4096: - / 12 / 15 / 35; 256 x 4096 x 12288:
+// - / 29 / 24 in 4 ranges / 97; 512 x 24576 x 4096: - / 82 / 54 / 46; 2048 x 4096 x 4096: - / 55 / 35 / 41;
+// (4 bits) 512 x 24576 x 4096: - / - / 46 / 35; 2048 x 4096 x 12288: - / - / 87 / 73.
 struct MxTiling {
   int tile;   // outputs and tokens a tile: 64, 128 or 256; 0: few tokens
   int split;  // stages a range
   int ranges;
 };
+// us: the weights at 5 TB/s, for every further block row at 10 TB/s, and the activations that all blocks
+// read at 50 TB/s for 16 rows, 22 TB/s (and 1.3 more) for 32, these in whole rounds of 256 blocks
+static double few_time(int a_fmt, int64_t M, int64_t N, int64_t K) {
+  const FewTile f = few_tile(M, N);
+  const double w_mb = (double)N * (double)K * (17.0 / 32) * 1e-6;
+  const double a_mb = (double)M * (double)K * (a_fmt == kMxFp8 ? 1.0 : 0.5) * 1e-6;
+  const double cols = (double)((N + 16 * f.tiles - 1) / (16 * f.tiles)), rows = (double)((M + f.rows - 1) / f.rows);
+  double t = w_mb / 5 + (rows - 1) * w_mb / 10 + (f.rows == 4 ? 0.0 : f.rows == 16 ? 0.02 : 0.045) * cols * a_mb;
+  if (f.rows == 32) {
+    t += 1.3;
+    if (cols * rows > 256) t *= ceil(cols * rows / 256) * 256 / (cols * rows);
+  }
+  return 1.1 + t;
+}
+// us: for each stage, and for a few more that stand for a tile's start and end, `one` + `more` x load while
+// no compute unit has more than one block (load: blocks for each of the 256), else `full` for a load of 1,
+// a third of that by whole rounds
+static double tile_time(int a_fmt, int tile, double blocks, int stages) {
+  struct Cost {
+    double base, ends, one, more, full;
+  };
+  static const Cost cost[2][3] = {{{3, 0, 0.17, 0.10, 0.20}, {3, 1.5, 0.30, 0.20, 0.50}, {3, 3.5, 0.82, 0.60, 1.45}},
+                                  {{3, 0, 0.15, 0.09, 0.18}, {3, 1.5, 0.26, 0.17, 0.43}, {7, 3.5, 0.50, 0.40, 1.02}}};
+  const Cost& c = cost[a_fmt == kMxFp8 ? 0 : 1][tile == 64 ? 0 : tile == 128 ? 1 : 2];
+  const double load = blocks / 256;
+  return c.base + (stages + c.ends) * (load <= 1 ? c.one + c.more * load : c.full * (ceil(load) + 2 * load) / 3);
+}
 static MxTiling mx_tiling(int a_fmt, int64_t M, int64_t N, int64_t K) {
   const int nk = (int)((K + kMxStage - 1) / kMxStage);
-  const double w_bytes = (double)N * K * (17.0 / 32), a_bytes = (double)M * K * (a_fmt == kMxFp8 ? 1.0 : 0.5);
   MxTiling best = {0, nk, 1};
   if (K < 3 * kMxStage) return best;  // a tile's scales are taken three stages at a time
-  double least = 2.5 + w_bytes / 4.2e6 + (double)((N + 15) / 16) * a_bytes / 12e6;
+  double least = M <= 64 ? few_time(a_fmt, M, N, K) : HUGE_VAL;
   for (int tile = 64; tile <= 256; tile *= 2) {
-    const double per = tile == 64 ? 0.21 : tile == 128 ? 0.5 : 1.3;
     const double blocks = (double)((M + tile - 1) / tile) * (double)((N + tile - 1) / tile);
-    for (int s = 1; s <= 8 && nk / s >= 6; ++s) {
+    for (int s = 1; s == 1 || (s <= kMaxRanges && nk / s >= 6); ++s) {
       const int split = (nk + s - 1) / s, ranges = (nk + split - 1) / split;
       if (s > 1 && (ranges != s || blocks * s > 512 || tile == 256)) continue;
-      const double rounds = ceil(blocks * ranges / 256);
-      double t = 3 + split * (tile == 64 && rounds == 1 ? 0.27 : per * rounds);
-      if (ranges > 1) t += 2.5 + ranges * (double)M * (double)N * 8 / 5e6;
+      double t = tile_time(a_fmt, tile, blocks * ranges, split);
+      // a second launch, and the ranges' fp32 sums written and read at 5 TB/s
+      if (ranges > 1) t += 2.3 + ranges * (double)M * (double)N * 8 / 5e6;
       if (t < least) least = t, best = {tile, split, ranges};
     }
   }
@@ -757,27 +852,29 @@ static MxTiling mx_tiling(int a_fmt, int64_t M, int64_t N, int64_t K) {
 static int64_t part_ld(int64_t N) { return (N + 3) / 4 * 4; }
 
 static int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
-static int64_t big_scale_words(int a_fmt, int64_t M, int64_t N, int64_t K) {
-  const int64_t ks = a_fmt == kMxFp8 ? kBigStage<kMxFp8> : kBigStage<kMxFp4>;
-  return (tiles_of(M, kBigTile) + tiles_of(N, kBigTile)) * kBigTile * ((K + ks - 1) / ks * (ks / 128));
+static int64_t big_scale_words(int64_t M, int64_t N, int64_t K) {
+  return (tiles_of(M, kBigTile) + tiles_of(N, kBigTile)) * kBigTile * ((K + kBigStage - 1) / kBigStage * 2);
 }
 
 size_t mx_matmul_workspace(int a_fmt, int64_t M, int64_t N, int64_t K) {
   const MxTiling t = mx_tiling(a_fmt, M, N, K);
-  if (t.tile == kBigTile) return (size_t)big_scale_words(a_fmt, M, N, K) * sizeof(uint32_t);
+  if (t.tile == kBigTile && a_fmt == kMxFp4) return (size_t)big_scale_words(M, N, K) * sizeof(uint32_t);
   return t.ranges > 1 ? (size_t)t.ranges * M * part_ld(N) * sizeof(float) : 0;
 }
 
 template <int AF>
 static void few_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uint8_t* W, const uint8_t* ws, int64_t N,
                        int64_t K, void* Y, int64_t ld_y, int y_dtype, hipStream_t stream) {
-  const unsigned gx = (unsigned)((N + 15) / 16);
-#define AWQ_FEW(MT)                                                                                       \
-  mx_few_kernel<AF, MT><<<dim3(gx, (unsigned)((M + 16 * MT - 1) / (16 * MT))), kFewWaves * kWave, 0, stream>>>( \
-      A, as, M, W, ws, N, K, Y, ld_y, y_dtype)
-  if (M <= 16) AWQ_FEW(1);
-  else if (M <= 32) AWQ_FEW(2);
-  else AWQ_FEW(4);
+  const FewTile f = few_tile(M, N);
+#define AWQ_FEW(AR, NT, ST, OCC)                                                                                   \
+  mx_few_kernel<AF, AR, NT, ST, OCC><<<dim3((unsigned)((N + 16 * NT - 1) / (16 * NT)), (unsigned)((M + AR - 1) / AR)), \
+                                       kFewWaves * kWave, 0, stream>>>(A, as, M, W, ws, N, K, Y, ld_y, y_dtype)
+  constexpr int kOcc32 = AF == kMxFp8 ? 2 : 4;  // the LDS of 32 rows holds one or two blocks
+  if (f.rows == 4) AWQ_FEW(4, 1, 4, 4);
+  else if (f.rows == 16 && f.tiles == 1) AWQ_FEW(16, 1, 2, 4);
+  else if (f.rows == 16) AWQ_FEW(16, 2, 2, 4);
+  else if (f.tiles == 1) AWQ_FEW(32, 1, 2, kOcc32);
+  else AWQ_FEW(32, 2, 2, 2);
 #undef AWQ_FEW
 }
 
@@ -787,23 +884,23 @@ static void tile_launch(const MxTiling& t, const uint8_t* A, const uint8_t* as, 
   const int n_mt = (int)tiles_of(M, t.tile), n_nt = (int)tiles_of(N, t.tile);
   const dim3 g((unsigned)(n_mt * n_nt), (unsigned)t.ranges);
 #define AWQ_TILE(BM, BN, WM, WN, OCC)                                                                               \
-  mx_tile_kernel<AF, YT, BM, BN, WM, WN, OCC><<<g, WM * WN * kWave, 0, stream>>>(A, as, M, W, ws, N, K, n_mt, n_nt, 8, \
+  mx_tile_kernel<AF, YT, BM, BN, WM, WN, OCC><<<g, WM * WN * kWave, 0, stream>>>(A, as, M, W, ws, N, K, n_mt, n_nt, 4, \
                                                                                t.split, Y, ld_y)
   if (t.tile == 64) AWQ_TILE(64, 64, 2, 2, 4);
-  else AWQ_TILE(128, 128, 2, 2, 2);
+  else if (t.tile == 128) AWQ_TILE(128, 128, 2, 2, 2);
+  else if constexpr (AF == kMxFp8 && YT != 2) AWQ_TILE(256, 256, 4, 2, 2);
 #undef AWQ_TILE
 }
 
-template <int AF, int YT>
+template <int YT>
 static void big_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uint8_t* W, const uint8_t* ws, int64_t N,
                        int64_t K, void* Y, int64_t ld_y, uint32_t* sc, hipStream_t stream) {
-  constexpr int SB = kBigStage<AF> / kMxBlock;
   const int n_mt = (int)tiles_of(M, kBigTile), n_nt = (int)tiles_of(N, kBigTile), kb = (int)(K / kMxBlock);
   const int64_t m_pad = (int64_t)n_mt * kBigTile, rows = m_pad + (int64_t)n_nt * kBigTile;
-  stage_scales_kernel<SB><<<dim3((unsigned)(rows / 256), (unsigned)((kb + 15) / 16)), 256, 0, stream>>>(
-      as, M, ws, N, kb, m_pad, rows, sc);
-  mx_big_kernel<AF, YT><<<(unsigned)(n_mt * n_nt), 512, 0, stream>>>(A, M, W, N, K, sc, m_pad, rows, n_mt, n_nt,
-                                                                    AF == kMxFp8 ? 4 : 8, Y, ld_y);
+  stage_scales_kernel<<<dim3((unsigned)(rows / 256), (unsigned)((kb + 15) / 16)), 256, 0, stream>>>(as, M, ws, N, kb,
+                                                                                                   m_pad, rows, sc);
+  mx_big_kernel<YT><<<(unsigned)(n_mt * n_nt), 512, 0, stream>>>(A, M, W, N, K, sc, m_pad, rows, n_mt, n_nt, 4, Y,
+                                                                ld_y);
 }
 
 template <int AF, int YT>
@@ -812,8 +909,8 @@ static void product_launch(const uint8_t* A, const uint8_t* as, int64_t M, const
   const MxTiling t = mx_tiling(AF, M, N, K);
   if (t.tile == 0) {
     few_launch<AF>(A, as, M, W, ws, N, K, Y, ld_y, YT, stream);
-  } else if (t.tile == kBigTile) {
-    big_launch<AF, YT>(A, as, M, W, ws, N, K, Y, ld_y, (uint32_t*)part, stream);
+  } else if (AF == kMxFp4 && t.tile == kBigTile) {
+    big_launch<YT>(A, as, M, W, ws, N, K, Y, ld_y, (uint32_t*)part, stream);
   } else if (t.ranges == 1) {
     tile_launch<AF, YT>(t, A, as, M, W, ws, N, K, Y, ld_y, stream);
   } else {
