@@ -431,8 +431,8 @@ awq_status awq_w4a16_matmul(const void* X, int64_t M, int64_t ld_x, const int32_
  *   element = v / 2^e rounded to nearest even, saturated at +-448 or +-6
  * (an all-zero block has e = -127).  A block that holds a NaN or an infinity
  * gets the scale 255 and zero elements.
- * cols % 32 == 0 and rows * cols < 2^33 (AWQ_ESHAPE otherwise); rows = 0 or
- * cols = 0 returns AWQ_OK at once.  16-bit inputs and outputs need the
+ * cols % 32 == 0, rows <= 2^27 and rows * cols < 2^33 (AWQ_ESHAPE otherwise);
+ * rows = 0 or cols = 0 returns AWQ_OK at once.  16-bit inputs and outputs need the
  * alignment of their elements only, and row strides (ld_*, in elements) >= cols
  * of any parity.  No workspace; one launch each.
  * ------------------------------------------------------------------------- */
@@ -465,7 +465,8 @@ awq_status awq_mx_dequant(const void* codes, const uint8_t* scales, int32_t fmt,
  * X, residual, residual_out: fp16 or bf16 (x_dtype) [rows, ld_*]; residual and
  * residual_out are both given or both NULL; residual_out may be residual or X
  * itself (same row stride), else the buffers do not overlap.  norm: [cols] of
- * norm_dtype (fp16, bf16 or fp32).  eps >= 0.  cols <= 65536 (AWQ_ESHAPE).
+ * norm_dtype (fp16, bf16 or fp32).  eps >= 0 (with 0 a row of zeros is 0 / 0,
+ * NaN).  cols <= 65536 (AWQ_ESHAPE).
  * A row's result depends on that row alone, not on how many there are.
  * ------------------------------------------------------------------------- */
 awq_status awq_rms_norm_mx(const void* X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
@@ -498,8 +499,8 @@ awq_status awq_silu_mul_mx(const void* gate, int64_t ld_g, const void* up, int64
  * fp32 result with AWQ_MX_FP8 activations is therefore refused (AWQ_EDTYPE).
  * A NaN scale makes every result of its row (a) or column (w) NaN; finite
  * results past the range of y_dtype become infinite.
- * M, N <= 2^26, K <= 2^22, K % 32 == 0 (AWQ_ESHAPE).  M = 0 or N = 0 returns
- * AWQ_OK at once.  ws: awq_mx_matmul_workspace bytes (possibly 0; ws may then
+ * M, N <= 2^26, M N <= 2^37, K <= 2^22, K % 32 == 0 (AWQ_ESHAPE).  M = 0 or N = 0
+ * returns AWQ_OK at once.  ws: awq_mx_matmul_workspace bytes (possibly 0; ws may then
  * be NULL), 256-byte aligned.  Deterministic.
  * ------------------------------------------------------------------------- */
 awq_status awq_mx_matmul_workspace(int32_t a_fmt, int64_t M, int64_t N, int64_t K, size_t* bytes /* [host] */);

@@ -750,12 +750,14 @@ awq_status awq_unpack_dequant(const int32_t* qweight, const uint16_t* scales, co
                     "awq_unpack_dequant");
 }
 
-// Shapes shared by the microscaled operators: whole blocks of 32, and fewer than
-// 2^33 values (the launches hold a lane index for 8 or more of them in 32 bits).
+// Shapes shared by the microscaled operators: whole blocks of 32, fewer than 2^33
+// values and at most 2^27 rows (a launch holds fewer than 2^32 lanes, at 8 or more
+// values each and at least 16 a row).
 static awq_status mx_shape(int32_t fmt, int64_t rows, int64_t cols) {
   if (fmt != AWQ_MX_FP8 && fmt != AWQ_MX_FP4) return fail(AWQ_EDTYPE, "format %d: need AWQ_MX_FP8 or AWQ_MX_FP4", fmt);
   if (rows < 0 || cols < 0) return fail(AWQ_EINVAL, "negative size");
   if (cols % 32) return fail(AWQ_ESHAPE, "cols %lld not a multiple of 32", (long long)cols);
+  if (rows > (int64_t)1 << 27) return fail(AWQ_ESHAPE, "rows %lld > 2^27", (long long)rows);
   if (cols > 0 && rows >= ((int64_t)1 << 33) / cols)
     return fail(AWQ_ESHAPE, "%lld x %lld: 2^33 values or more", (long long)rows, (long long)cols);
   return ok();
@@ -847,9 +849,9 @@ static awq_status mx_matmul_shape(int32_t a_fmt, int64_t M, int64_t N, int64_t K
     return fail(AWQ_EDTYPE, "a_fmt %d: need AWQ_MX_FP8 or AWQ_MX_FP4", a_fmt);
   if (M < 0 || N < 0 || K < 0) return fail(AWQ_EINVAL, "negative size");
   if (K % 32) return fail(AWQ_ESHAPE, "K %lld not a multiple of 32", (long long)K);
-  if (M > kMxMaxRows || N > kMxMaxRows || K > kMxMaxK)
-    return fail(AWQ_ESHAPE, "M %lld, N %lld or K %lld: need M, N <= 2^26 and K <= 2^22", (long long)M, (long long)N,
-                (long long)K);
+  if (M > kMxMaxRows || N > kMxMaxRows || K > kMxMaxK || M * N > (int64_t)1 << 37)
+    return fail(AWQ_ESHAPE, "M %lld, N %lld or K %lld: need M, N <= 2^26, M N <= 2^37 and K <= 2^22", (long long)M,
+                (long long)N, (long long)K);
   return ok();
 }
 

@@ -76,6 +76,7 @@ def test_quantize_validation(A):
     assert q(ld=63) == A.AWQ_ESHAPE
     assert q(rows=2 ** 27, cols=64) == A.AWQ_ESHAPE and "2^33" in err(A)
     assert q(rows=2 ** 62, cols=64) == A.AWQ_ESHAPE
+    assert q(rows=2 ** 27 + 1, cols=32, ld=32) == A.AWQ_ESHAPE and "2^27" in err(A)
     assert q(X=None) == A.AWQ_EINVAL and q(codes=None) == A.AWQ_EINVAL and q(scales=None) == A.AWQ_EINVAL
     assert q(X=ODD) == A.AWQ_EALIGN and q(s=FAKE + 2) == A.AWQ_EALIGN and q(codes=FAKE + 8) == A.AWQ_EALIGN
     assert q(rows=0, X=None, codes=None, scales=None) == A.AWQ_OK and err(A) == ""
@@ -131,6 +132,7 @@ def test_matmul_validation(A):
     assert m(dt=A.AWQ_F32) == A.AWQ_EDTYPE and "fp32 result" in err(A)
     assert m(K=40) == A.AWQ_ESHAPE and m(K=0) == A.AWQ_ESHAPE and m(ld=47) == A.AWQ_ESHAPE
     assert m(M=-1) == A.AWQ_EINVAL and m(M=2 ** 27) == A.AWQ_ESHAPE and m(K=2 ** 22 + 32) == A.AWQ_ESHAPE
+    assert m(M=2 ** 20, N=2 ** 18, ld=2 ** 18) == A.AWQ_ESHAPE and "2^37" in err(A)
     for k in ("a", "a_s", "w", "w_s", "Y"):
         assert m(**{k: None}) == A.AWQ_EINVAL
     assert m(a=FAKE + 8) == A.AWQ_EALIGN and m(w=FAKE + 8) == A.AWQ_EALIGN and m(Y=ODD) == A.AWQ_EALIGN
