@@ -47,6 +47,15 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
 }
 
+// The compiler keeps memory accesses on their side of this point
+__device__ __forceinline__ void hold_order() { asm volatile("" ::: "memory"); }
+// The block's barrier, without waiting for the loads in flight as __syncthreads would
+__device__ __forceinline__ void block_barrier() {
+  hold_order();
+  __builtin_amdgcn_s_barrier();
+  hold_order();
+}
+
 // 16 bytes a lane from base + off + k_off straight into LDS, lane i to 16 i bytes past dst
 __device__ __forceinline__ void load_lds16(const void* base, uint32_t bytes, uint8_t* dst, uint32_t off,
                                            uint32_t k_off) {
@@ -156,16 +165,13 @@ __global__ __launch_bounds__(kFewWaves * kWave, OCC) void mx_few_kernel(const ui
     uint4 w[NT][ST];
     FewScales<ST> sw[NT], sa[MT];
   };
-  // Loads of a whole chunk, the direct ones first.  A last chunk may take fewer of the others; those of the
-  // chunk before it that a wait for all but NL then leaves out are loads to registers, which the compiler
-  // waits for itself.
-  constexpr int NL = DI + NT * (ST + 1) + MT;
-  static_assert(NT * (ST + 1) + MT >= NT * (ST - 1), "what a last chunk may lack");
+  constexpr int NL = DI + NT * (ST + 1) + MT;  // loads of a whole chunk (a row's last one may take others)
   auto load_chunk = [&](Chunk& f, uint8_t* buf, int c) {
     const uint32_t k = (uint32_t)c * RB;
 #pragma unroll
-    for (int j = 0; j < DI; ++j)  // pieces past the row's end: past the range too
-      load_lds16(a_tile, a_bytes, buf + 1024 * j, k + vc[j] < a_row ? va[j] + k + vc[j] : kMxOut, 0);
+    for (int j = 0; j < DI; ++j)  // past the row's end its last piece again: the weights there are 0
+      load_lds16(a_tile, a_bytes, buf + 1024 * j, va[j] + min(k + vc[j], a_row - 16), 0);
+    hold_order();
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
@@ -177,6 +183,12 @@ __global__ __launch_bounds__(kFewWaves * kWave, OCC) void mx_few_kernel(const ui
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t) f.sa[t] = few_scales<ST>(asr[t], c, kb);
+    hold_order();
+  };
+  auto wait_chunk = [&](int next) {  // for all but the loads of chunk `next`, the youngest
+    if (4 * ST * (next + 1) <= kb) wait_loads<NL>();
+    else wait_loads<0>();
+    hold_order();
   };
   auto multiply = [&](const Chunk& f, const uint8_t* buf) {
     i32x8 w[NT][ST];
@@ -206,24 +218,18 @@ __global__ __launch_bounds__(kFewWaves * kWave, OCC) void mx_few_kernel(const ui
     load_chunk(f0, b0[wave], c);
     for (;;) {
       // chunk c in f0 / b0; before its buffer is filled again its reads are done (lgkmcnt 0)
-      if (c + kFewWaves < nc) {
-        load_chunk(f1, b1[wave], c + kFewWaves);
-        wait_loads<NL>();
-      } else {
-        wait_loads<0>();
-      }
+      if (c + kFewWaves < nc) load_chunk(f1, b1[wave], c + kFewWaves);
+      wait_chunk(c + kFewWaves);
       multiply(f0, b0[wave]);
       if ((c += kFewWaves) >= nc) break;
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-      if (c + kFewWaves < nc) {
-        load_chunk(f0, b0[wave], c + kFewWaves);
-        wait_loads<NL>();
-      } else {
-        wait_loads<0>();
-      }
+      hold_order();
+      if (c + kFewWaves < nc) load_chunk(f0, b0[wave], c + kFewWaves);
+      wait_chunk(c + kFewWaves);
       multiply(f1, b1[wave]);
       if ((c += kFewWaves) >= nc) break;
       __builtin_amdgcn_s_waitcnt(0xC07F);
+      hold_order();
     }
   }
   // the wave's sums, in its first buffer's place
@@ -504,7 +510,7 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
   write_scales(0);
   load_scales(1);
   wait_loads<0>();
-  __builtin_amdgcn_s_barrier();
+  block_barrier();
   Frags f0, f1;
   Scales c0, c1;
   read_frags(f0, s0, 0);
@@ -524,7 +530,7 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
     interleave<NR, ND>();                         \
     __builtin_amdgcn_sched_barrier(0);            \
     wait_loads<ND>();                             \
-    __builtin_amdgcn_s_barrier();                 \
+    block_barrier();                              \
     __builtin_amdgcn_sched_barrier(0);            \
     if (P == 2) load_scales(ss + 2);              \
     read_scales(c1, ss + (P == 2), (P + 1) % 3);  \
@@ -545,7 +551,7 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
 #undef AWQ_MX_STAGE
 
   wait_loads<0>();  // none may land after the block has given its LDS back
-  __builtin_amdgcn_s_barrier();
+  block_barrier();
 
   store_tile<YT, MT, NT, NW, BM * AB + BN * WB>(acc, s0, s1, s2, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M, N,
                                                YT == 2 ? (float*)Y + (int64_t)blockIdx.y * M * ld_y : Y, ld_y);
@@ -707,7 +713,7 @@ __global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restric
   load_stage(s0, 0);
   load_stage(s1, 1);
   wait_loads<2 * DI + SW>();
-  __builtin_amdgcn_s_barrier();
+  block_barrier();
   read_scales(c1, s0);
   read_frags(f0, s0, 0);
 
@@ -726,7 +732,7 @@ __global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restric
     AWQ_MX_STEP(f1, f0, C, 1)                            \
     AWQ_MX_STEP(f0, f1, C, 2)                            \
     wait_loads<0>();                                     \
-    __builtin_amdgcn_s_barrier();                        \
+    block_barrier();                                     \
     __builtin_amdgcn_sched_barrier(0);                   \
     load_stage(C, kt + 2);                               \
     read_scales(c1, X);                                  \
@@ -745,7 +751,7 @@ __global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restric
 #undef AWQ_MX_STAGE
 #undef AWQ_MX_STEP
   wait_loads<0>();  // none may land after the block has given its LDS back
-  __builtin_amdgcn_s_barrier();
+  block_barrier();
   store_tile<YT, MT, NT, NW, SB / 2>(acc, s0, s1, s1 + SB / 2, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M, N,
                                      Y, ld_y);
 }
@@ -838,6 +844,7 @@ static MxTiling mx_tiling(int a_fmt, int64_t M, int64_t N, int64_t K) {
   double least = M <= 64 ? few_time(a_fmt, M, N, K) : HUGE_VAL;
   for (int tile = 64; tile <= 256; tile *= 2) {
     const double blocks = (double)((M + tile - 1) / tile) * (double)((N + tile - 1) / tile);
+    if (blocks > (1 << 22)) continue;  // a launch holds fewer than 2^32 lanes
     for (int s = 1; s == 1 || (s <= kMaxRanges && nk / s >= 6); ++s) {
       const int split = (nk + s - 1) / s, ranges = (nk + split - 1) / split;
       if (s > 1 && (ranges != s || blocks * s > 512 || tile == 256)) continue;
@@ -866,15 +873,22 @@ template <int AF>
 static void few_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uint8_t* W, const uint8_t* ws, int64_t N,
                        int64_t K, void* Y, int64_t ld_y, int y_dtype, hipStream_t stream) {
   const FewTile f = few_tile(M, N);
+  const int64_t a_row = AF == kMxFp8 ? K : K / 2, y_bytes = y_dtype == 2 ? 4 : 2;
+  constexpr int64_t kRows = 65535 * 4;  // of a launch: the grid's second dimension holds 65535 blocks
+  for (int64_t m = 0; m < M; m += kRows) {
+    const int64_t n_rows = M - m < kRows ? M - m : kRows;
 #define AWQ_FEW(AR, NT, ST, OCC)                                                                                   \
-  mx_few_kernel<AF, AR, NT, ST, OCC><<<dim3((unsigned)((N + 16 * NT - 1) / (16 * NT)), (unsigned)((M + AR - 1) / AR)), \
-                                       kFewWaves * kWave, 0, stream>>>(A, as, M, W, ws, N, K, Y, ld_y, y_dtype)
-  constexpr int kOcc32 = AF == kMxFp8 ? 2 : 4;  // the LDS of 32 rows holds one or two blocks
-  if (f.rows == 4) AWQ_FEW(4, 1, 4, 4);
-  else if (f.rows == 16 && f.tiles == 1) AWQ_FEW(16, 1, 2, 4);
-  else if (f.rows == 16) AWQ_FEW(16, 2, 2, 4);
-  else if (f.tiles == 1) AWQ_FEW(32, 1, 2, kOcc32);
-  else AWQ_FEW(32, 2, 2, 2);
+  mx_few_kernel<AF, AR, NT, ST, OCC><<<dim3((unsigned)((N + 16 * NT - 1) / (16 * NT)), (unsigned)((n_rows + AR - 1) / AR)), \
+                                       kFewWaves * kWave, 0, stream>>>(A + m * a_row, as + m * (K / kMxBlock), n_rows, \
+                                                                       W, ws, N, K, (uint8_t*)Y + m * ld_y * y_bytes, \
+                                                                       ld_y, y_dtype)
+    constexpr int kOcc32 = AF == kMxFp8 ? 2 : 4;  // the LDS of 32 rows holds one or two blocks
+    if (f.rows == 4) AWQ_FEW(4, 1, 4, 4);
+    else if (f.rows == 16 && f.tiles == 1) AWQ_FEW(16, 1, 2, 4);
+    else if (f.rows == 16) AWQ_FEW(16, 2, 2, 4);
+    else if (f.tiles == 1) AWQ_FEW(32, 1, 2, kOcc32);
+    else AWQ_FEW(32, 2, 2, 2);
+  }
 #undef AWQ_FEW
 }
 

@@ -109,6 +109,7 @@ def check_near(out, fmt, y, d):
 @pytest.mark.parametrize("rows,cols,ld,offset,scaled", [
     (1, 32, None, 0, False), (1, 4096, None, 0, True), (3, 96, 97, 1, False), (257, 160, 163, 3, True),
     (130, 2080, None, 0, True), (1000, 1056, 1064, 8, False), (7, 12288, 24576, 0, False),
+    (300, 32, None, 0, True), (1027, 64, 67, 1, True), (77, 128, None, 0, True), (5, 480, None, 2, True),
 ])
 def test_quantize_bit_exact(A, fmt, dtype, rows, cols, ld, offset, scaled):
     import torch
@@ -355,6 +356,34 @@ def test_product_odd_outputs(A, M, N, ld_y, fmt, dtype):
 def test_product_sizes(A, M, N, K, fmt, dtype):
     say(f"mx_matmul {M}x{N}x{K} {fmt} {dtype}")
     check_product(A, M, N, K, fmt, dtype)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("M", [1, 3, 4, 5, 16, 17, 40])
+@pytest.mark.parametrize("N,K", [(4112, 544), (8208, 1184), (48, 4640), (16, 8192)])
+def test_product_few_rows(A, M, N, K, fmt):
+    """Few tokens against few and many outputs: every tile of them, K in one chunk a wave and in several."""
+    say(f"mx_matmul few M {M} N {N} K {K} {fmt}")
+    check_product(A, M, N, K, fmt, "bf16")
+
+
+def test_product_many_rows_short(A):
+    """More rows than one launch's grid holds, K too short for the tiles."""
+    import torch
+    say("mx_matmul 600000 x 17 x 64")
+    M, N, K = 600_000, 17, 64
+    rng = np.random.default_rng(2)
+    wc, wsc = random_mx(rng, N, K, "fp4")
+    X = torch.zeros((M, K), dtype=torch.float16, device="cuda")
+    at = [0, 1, 262139, 262140, 262141, 524279, 524280, M - 1]
+    X[at] = to_dev(values(rng, len(at), K), "f16")[0]
+    ac, asc = A.mx_quantize(X, "fp4")
+    Y = A.mx_matmul(ac, asc, *dev_mx(wc, wsc, "fp4"), out_dtype=torch.float32)
+    a, w = O.mx_values(codes_np(ac[at]), codes_np(asc[at]), "fp4"), O.mx_values(wc, wsc, "fp4")
+    y = a @ w.T
+    assert np.all(np.abs(Y[at].double().cpu().numpy() - y) <= product_tol(a, w, K, "fp4", y, "f32"))
+    Y[at] = 0
+    assert not Y.any()
 
 
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
