@@ -23,6 +23,7 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -619,7 +620,11 @@ class _MxPrepared(_Prepared):
     def _place(self, like: torch.Tensor, stream) -> int:
         self._device = like.device
         self._alone = torch.cuda.device_count() == 1
-        return torch.cuda.current_stream(like.device).cuda_stream if stream is None else stream.cuda_stream
+        if stream is None:
+            return torch.cuda.current_stream(like.device).cuda_stream
+        if stream.device != like.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {like.device}")
+        return stream.cuda_stream
 
     def _bind(self, *args) -> None:
         types = getattr(lib(), self._fn).argtypes
@@ -637,6 +642,12 @@ class _MxPrepared(_Prepared):
                 st = self._f(*self._args)
         if st != AWQ_OK:
             _check(st)
+
+
+def _mx_alloc(stream):
+    """Results and workspaces come from the memory pool of the stream that uses them: freed, they are
+    handed out again in that stream's order."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _mx_fmt(fmt: str) -> int:
@@ -667,12 +678,13 @@ def _mx_out(out, rows: int, cols: int, fmt: str, like: torch.Tensor):
         _tensor(scales, "scales", torch.float8_e8m0fnu, (rows, cols // 32), like=like)
 
 
-def _mx_empty(out, rows: int, cols: int, fmt: str, device):
+def _mx_empty(out, rows: int, cols: int, fmt: str, device, stream):
     if out is not None:
         return tuple(out)
-    codes = (torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device) if fmt == "fp8" else
-             torch.empty((rows, cols // 2), dtype=torch.uint8, device=device))
-    return codes, torch.empty((rows, cols // 32), dtype=torch.float8_e8m0fnu, device=device)
+    with _mx_alloc(stream):
+        codes = (torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=device) if fmt == "fp8" else
+                 torch.empty((rows, cols // 2), dtype=torch.uint8, device=device))
+        return codes, torch.empty((rows, cols // 32), dtype=torch.float8_e8m0fnu, device=device)
 
 
 def _mx_operand(codes: torch.Tensor, scales: torch.Tensor, name: str, like=None):
@@ -696,7 +708,7 @@ class MxQuantPlan(_MxPrepared):
         _tensor(s, "s", torch.float32, (cols,), like=X, optional=True)
         _mx_out(out, rows, cols, fmt, X)
         _dev(X, "X")
-        self.out = _mx_empty(out, rows, cols, fmt, X.device)
+        self.out = _mx_empty(out, rows, cols, fmt, X.device, stream)
         self._keep = (X, s)
         self._bind(_ptr(X), _FLOATS[X.dtype], rows, cols, ld, _ptr(s), _mx_fmt(fmt), _ptr(self.out[0]),
                    _ptr(self.out[1]), self._place(X, stream))
@@ -725,7 +737,8 @@ class MxDequantPlan(_MxPrepared):
         if out is not None:
             _mx_rows(out, "out", tuple(_FLOATS), (rows, cols), like=codes)
         _dev(codes, "codes")
-        self.out = torch.empty((rows, cols), dtype=out_dtype, device=codes.device) if out is None else out
+        with _mx_alloc(stream):
+            self.out = torch.empty((rows, cols), dtype=out_dtype, device=codes.device) if out is None else out
         ld = self.out.stride(0) if rows > 1 else max(self.out.stride(0), cols)
         self._keep = (codes, scales, s)
         self._bind(_ptr(codes), _ptr(scales), _MX_FMT[fmt], rows, cols, _ptr(s), _ptr(self.out),
@@ -760,9 +773,10 @@ class RmsNormMxPlan(_MxPrepared):
         _mx_out(out, rows, cols, fmt, X)
         _dev(X, "X")
         if residual is not None and residual_out is None:
-            residual_out = torch.empty((rows, cols), dtype=X.dtype, device=X.device)
+            with _mx_alloc(stream):
+                residual_out = torch.empty((rows, cols), dtype=X.dtype, device=X.device)
             ld_ro = cols
-        self.out = (*_mx_empty(out, rows, cols, fmt, X.device), residual_out)
+        self.out = (*_mx_empty(out, rows, cols, fmt, X.device, stream), residual_out)
         self._keep = (X, weight, residual)
         self._bind(_ptr(X), _FLOATS[X.dtype], rows, cols, ld_x, _ptr(residual), ld_r, _ptr(weight),
                    _FLOATS[weight.dtype], eps, _ptr(residual_out), ld_ro, _mx_fmt(fmt), _ptr(self.out[0]),
@@ -790,7 +804,7 @@ class SiluMulMxPlan(_MxPrepared):
         ld_u = _mx_rows(up, "up", gate.dtype, (rows, cols), like=gate)
         _mx_out(out, rows, cols, fmt, gate)
         _dev(gate, "gate")
-        self.out = _mx_empty(out, rows, cols, fmt, gate.device)
+        self.out = _mx_empty(out, rows, cols, fmt, gate.device, stream)
         self._keep = (gate, up)
         self._bind(_ptr(gate), ld_g, _ptr(up), ld_u, _FLOATS[gate.dtype], rows, cols, _mx_fmt(fmt),
                    _ptr(self.out[0]), _ptr(self.out[1]), self._place(gate, stream))
@@ -832,8 +846,9 @@ class MxMatmulPlan(_MxPrepared):
         _tensor(ws, "ws", torch.uint8, (None,), like=a_codes, optional=True)
         _dev(a_codes, "a_codes")
         need = mx_matmul_workspace_bytes(fmt, M, N, K)
-        self.ws = workspace(need, a_codes.device) if (ws is None or ws.numel() < need) else ws
-        self.out = torch.empty((M, N), dtype=out_dtype, device=a_codes.device) if out is None else out
+        with _mx_alloc(stream):
+            self.ws = workspace(need, a_codes.device) if (ws is None or ws.numel() < need) else ws
+            self.out = torch.empty((M, N), dtype=out_dtype, device=a_codes.device) if out is None else out
         ld = self.out.stride(0) if M > 1 else max(self.out.stride(0), N)
         self._keep = (a_codes, a_scales, w_codes, w_scales)
         self._bind(_ptr(a_codes), _ptr(a_scales), _MX_FMT[fmt], M, _ptr(w_codes), _ptr(w_scales), N, K,

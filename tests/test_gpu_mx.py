@@ -525,6 +525,34 @@ def test_product_two_streams(A):
     assert all(torch.equal(a, b) for a, b in zip(got, ref))
 
 
+def test_other_stream_owns_its_memory(A):
+    """Workspaces and results of a call on another stream go back to that stream: what the current one
+    allocates next does not lie in them, though the call may still run."""
+    import torch
+    say("mx operators on another stream")
+    rng = np.random.default_rng(9)
+    a, w = dev_mx(*random_mx(rng, 200, 4096, "fp8"), "fp8"), dev_mx(*random_mx(rng, 520, 4096, "fp4"), "fp4")
+    X = to_dev(values(rng, 60, 1024), "bf16")[0]
+    norm = torch.ones(1024, device="cuda")
+    ref = [A.mx_matmul(*a, *w), *A.rms_norm_mx(X, norm, residual=X), *A.silu_mul_mx(X, X), *A.mx_quantize(X, "fp4")]
+    ref.append(A.mx_dequant(*ref[-2:]))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    plan = A.MxMatmulPlan(*a, *w, stream=s)
+    assert plan.ws.numel() > 256
+    got = [plan.run(), *A.rms_norm_mx(X, norm, residual=X, stream=s), *A.silu_mul_mx(X, X, stream=s),
+           *A.mx_quantize(X, "fp4", stream=s)]
+    got.append(A.mx_dequant(*got[-2:], stream=s))
+    held = [(t.data_ptr(), t.numel() * t.element_size()) for t in (plan.ws, *got)]
+    s.synchronize()
+    for g, r in zip(got, ref):
+        assert torch.equal(g.view(torch.uint8), r.view(torch.uint8))
+    del plan, got, g
+    for _, n in held:
+        p = torch.empty(n, dtype=torch.uint8, device="cuda").data_ptr()
+        assert all(p + n <= q or q + m <= p for q, m in held)
+
+
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
 def test_dequant_scaled_far_scales(A, fmt):
     """Quotients whose scale or block exponent lies far out: the IEEE quotient there too."""
