@@ -69,9 +69,11 @@ __global__ __launch_bounds__(kEwThreads) void mx_quantize_kernel(const uint16_t*
 
 // With a scale of the columns a lane keeps its 8 columns over kColRows rows, so
 // the scale is loaded (and, in the inverse, its reciprocal taken) once for them.
-// A block is 2^tx chunks of columns (4, 16 or 64: as many as a row has) by
-// 256 / 2^tx x kColRows rows.  Measured at 4096 x 12288 to 4 bits: 25.7 us, the
-// inverse 27.8 us (16 chunks by 128 rows: 31.8 and 35.2 us).
+// A block is 2^tx chunks of columns (as many as a row has, rounded up to a power of
+// two, from 4 to 64) by 256 / 2^tx x kColRows rows.  Measured at 4096 x 12288 to 4
+// bits: 25.7 us, the inverse 23.9 us, 5 TB/s; on 48 million values (us, 16 / 64
+// chunks a block, quantized): 128 columns 23.5 / 48, 480 columns 32.6 / 24.1, 4096
+// columns 28.4 / 24.0.
 constexpr int kColRows = 4;
 struct ColPos {
   uint32_t col;
@@ -167,7 +169,8 @@ __global__ __launch_bounds__(kEwThreads) void silu_mul_mx_kernel(const uint16_t*
 // ---------------------------------------------------------------------------
 // dequant: out = RN(RN32(code 2^e / s[col])), s optional.  code 2^e is exact in
 // fp32 (unless it overflows); the quotient is rounded to fp32 and then to a
-// 16-bit output, as unpack_dequant does.
+// 16-bit output, as unpack_dequant does.  Bound by the stores: 16384 x 4096 to
+// bf16 takes 33 us from 4 bits (5.1 TB/s), 40 us from 8.
 // ---------------------------------------------------------------------------
 template <int FMT>
 __device__ __forceinline__ void decode8(const uint2 c, float (&v)[8]) {  // elements, unscaled
@@ -295,9 +298,14 @@ __global__ __launch_bounds__(kEwThreads) void mx_dequant_scaled_kernel(const uin
 // RMS norm: h = x + residual (fp32), residual_out = RN16(h),
 // y = h / sqrt(mean h^2 + eps) * weight -> codes, scales.  The mean is taken
 // over the unrounded fp32 h.  A row stays in registers between its sum of
-// squares and its scaling, so the inputs are read once.  Lanes of a row: GL
-// lanes of a wave (several rows a wave) up to 1024 columns, else a whole block
-// with one exchange of wave sums through LDS.  The split depends on the row
+// squares and its scaling, so the inputs are read once: 6001 x 4096 fp16 with a
+// residual takes 30.4 us, 5.7 TB/s.  Lanes of a row: the GL lanes of a wave that
+// its chunks of 8 need (several rows a wave) up to 256 columns, 32 lanes with two
+// chunks each up to 512, else a whole block with one exchange of wave sums through
+// LDS.  Measured on 24 million values in bf16 with a residual, us: 128 columns 30
+// with 16 lanes, 78 with 64; 288 columns 37.6 with 2 x 32, 41 with a block of 64;
+// 1024 columns 28.4 with a block (two chunks a lane), 29.2 with a wave; 4096
+// columns 29.7 with two chunks a lane, 30.4 with one.  The split depends on the row
 // length alone: a row's result is the same in every batch.
 // ---------------------------------------------------------------------------
 struct NormArgs {
@@ -389,7 +397,11 @@ static unsigned ew_blocks(int64_t n_chunks, int unroll) {
   return (unsigned)((n_chunks + kEwThreads * unroll - 1) / (kEwThreads * unroll));
 }
 
-static int col_tx(int64_t cols) { return cols >= 512 ? 6 : cols >= 128 ? 4 : 2; }
+static int col_tx(int64_t cols) {
+  int tx = 2;
+  while (tx < 6 && 8 << tx < cols) ++tx;
+  return tx;
+}
 static unsigned col_blocks(int64_t rows, int64_t cols) {
   const int tx = col_tx(cols);
   const int64_t nx = (cols / 8 + (1 << tx) - 1) >> tx, per = (kEwThreads >> tx) * kColRows;
@@ -462,10 +474,11 @@ static void rms_norm_launch(const NormArgs& a, hipStream_t stream) {
 #define AWQ_NORM_B(CH)                                                                                             \
   rms_norm_mx_kernel<DT, FMT, 0, CH><<<(unsigned)a.rows, (unsigned)(((cpr + CH - 1) / CH + 63) / 64 * 64), 0, stream>>>( \
       a)
-  if (cpr <= 16) AWQ_NORM_W(16, 1);
+  if (cpr <= 4) AWQ_NORM_W(4, 1);
+  else if (cpr <= 8) AWQ_NORM_W(8, 1);
+  else if (cpr <= 16) AWQ_NORM_W(16, 1);
   else if (cpr <= 32) AWQ_NORM_W(32, 1);
-  else if (cpr <= 64) AWQ_NORM_W(64, 1);
-  else if (cpr <= 128) AWQ_NORM_W(64, 2);
+  else if (cpr <= 64) AWQ_NORM_W(32, 2);
   else if (cpr <= 512) AWQ_NORM_B(2);
   else if (cpr <= 1024) AWQ_NORM_B(1);
   else if (cpr <= 2048) AWQ_NORM_B(2);

@@ -109,6 +109,7 @@ def check_near(out, fmt, y, d):
 @pytest.mark.parametrize("rows,cols,ld,offset,scaled", [
     (1, 32, None, 0, False), (1, 4096, None, 0, True), (3, 96, 97, 1, False), (257, 160, 163, 3, True),
     (130, 2080, None, 0, True), (1000, 1056, 1064, 8, False), (7, 12288, 24576, 0, False),
+    (95, 224, 227, 2, True), (130, 544, None, 0, True),
     (300, 32, None, 0, True), (1027, 64, 67, 1, True), (77, 128, None, 0, True), (5, 480, None, 2, True),
 ])
 def test_quantize_bit_exact(A, fmt, dtype, rows, cols, ld, offset, scaled):
@@ -204,6 +205,8 @@ def test_quantize_offsets_past_32_bits(A):
     (21, 2080, "bf16", "f32", True, "fp8", 2081, 3), (3, 8192, "f16", "f16", True, "fp8", None, 0),
     (3, 8224, "bf16", "bf16", True, "fp8", None, 0), (2, 32768, "bf16", "f32", True, "fp8", None, 0),
     (2, 65536, "f16", "f16", False, "fp4", None, 0),
+    (131, 32, "bf16", "f32", True, "fp4", 33, 1), (35, 64, "f16", "bf16", True, "fp8", None, 0),
+    (17, 288, "bf16", "f16", True, "fp8", 291, 1), (2, 544, "f16", "f32", False, "fp4", None, 0),
 ])
 def test_rms_norm(A, rows, cols, dtype, wdtype, residual, fmt, ld, offset):
     import torch
