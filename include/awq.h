@@ -501,7 +501,9 @@ awq_status awq_silu_mul_mx(const void* gate, int64_t ld_g, const void* up, int64
  * results past the range of y_dtype become infinite.
  * M, N <= 2^26, M N <= 2^37, K <= 2^22, K % 32 == 0 (AWQ_ESHAPE).  M = 0 or N = 0
  * returns AWQ_OK at once.  ws: awq_mx_matmul_workspace bytes (possibly 0; ws may then
- * be NULL), 256-byte aligned.  Deterministic.
+ * be NULL), 256-byte aligned, for this call alone while it runs: sums of ranges of K
+ * where the outputs alone do not fill the device, or scales laid out for the large
+ * tiles.  Deterministic.
  * ------------------------------------------------------------------------- */
 awq_status awq_mx_matmul_workspace(int32_t a_fmt, int64_t M, int64_t N, int64_t K, size_t* bytes /* [host] */);
 awq_status awq_mx_matmul(const void* a_codes, const uint8_t* a_scales, int32_t a_fmt, int64_t M, const void* w_codes,
@@ -516,7 +518,8 @@ awq_status awq_mx_matmul(const void* a_codes, const uint8_t* a_scales, int32_t a
  * kernel (weight score) or the chunked dW-build + GEMM launches (output score)
  * of awq_search_scales; the pack kernel of awq_quantize_pack; every launch of
  * awq_w4a16_matmul (GEMV or GEMM and, where used, the reduction); every launch
- * of the microscaled operators.  Pass NULL, NULL to clear.  The library records the events and nothing else.
+ * of the microscaled operators.  Pass NULL, NULL to clear.  The library records the
+ * events and nothing else.
  * ------------------------------------------------------------------------- */
 awq_status awq_set_timing_events(void* before, void* after);
 
