@@ -47,6 +47,8 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
 }
 
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }  // lgkmcnt(0)
+
 // The compiler keeps memory accesses on their side of this point
 __device__ __forceinline__ void hold_order() { asm volatile("" ::: "memory"); }
 // The block's barrier, without waiting for the loads in flight as __syncthreads would
@@ -271,8 +273,6 @@ __device__ __forceinline__ f32x16 mfma_mx32(const i32x8 w, const i32x8 a, f32x16
 
 constexpr int kMxXcds = 8;
 constexpr int kMxStage = 128;   // K per stage
-
-
 // Issue order of half a stage: two LDS reads and one or two direct loads behind each MFMA, so that
 // they are under way early and the matrix cores never wait for a burst of them
 template <int READS, int LOADS>
@@ -304,14 +304,14 @@ __device__ __forceinline__ void store_row16(uint8_t* p, const uint4 v, int64_t l
 // Results of a wave's MT x NT tiles of 32 x 32 at (m0, n0): lane l holds outputs 8 (e / 4) + 4 h + e % 4 of
 // token l % 32.  The wave turns 32 tokens at a time through its own part of the block's LDS arrays (SB
 // bytes each), so that 16 bytes a lane and whole rows of its outputs go to memory together.
-template <int YT, int MT, int NT, int NW, int SB>
+template <int YT, int MT, int NT, int NW, int SB, int NA = 3, bool WHOLE = false>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[NT][MT], uint8_t* s0, uint8_t* s1, uint8_t* s2,
                                            int wave, int lane, int64_t m0, int64_t n0, int64_t M, int64_t N, void* Y,
                                            int64_t ld_y) {
   constexpr int EB = YT == 2 ? 4 : 2;
-  constexpr int CG = EB == 2 || NT == 1 ? NT : NT / 2;       // 32-output tiles per turn
+  constexpr int CG = (EB == 2 && NA > 1) || NT == 1 ? NT : NT / 2;  // 32-output tiles per turn
   constexpr int RB = CG * 32 * EB;                           // bytes of a row
-  constexpr int WS = (NW + 2) / 3;                           // waves an array
+  constexpr int WS = (NW + NA - 1) / NA;                     // waves an array
   constexpr int RS = RB + (WS * 32 * (RB + 16) <= SB ? 16 : 0);  // stride: padded where there is room
   static_assert(WS * 32 * RS <= SB, "an array holds the rows of its waves");
   uint8_t* part = (wave < WS ? s0 : wave < 2 * WS ? s1 : s2) + wave % WS * (32 * RS);
@@ -340,15 +340,15 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[NT][MT], uint8_t*
         const int row = it * RI + lane / LR, c = lane % LR;
         const uint4 v = *(const uint4*)(part + row * RS + 16 * c);
         const int64_t m = m0 + 32 * j + row, n = n0 + 32 * i0 + c * (16 / EB);
-        if (m < M) store_row16<EB>((uint8_t*)Y + (m * ld_y + n) * EB, v, N - n);
+        if constexpr (WHOLE) st_any((uint8_t*)Y + (m * ld_y + n) * EB, v);
+        else if (m < M) store_row16<EB>((uint8_t*)Y + (m * ld_y + n) * EB, v, N - n);
       }
       __builtin_amdgcn_wave_barrier();
     }
 }
 
 // The tile of a block: each XCD owns a contiguous range of tiles, walked in groups of group_m token tiles
-__device__ __forceinline__ void block_tile(int n_mt, int n_nt, int group_m, int* mt, int* nt) {
-  const int nblk = (int)gridDim.x, bid = (int)blockIdx.x;
+__device__ __forceinline__ void block_tile(int bid, int nblk, int n_mt, int n_nt, int group_m, int* mt, int* nt) {
   const int xcd = bid % kMxXcds, pos = bid / kMxXcds, q = nblk / kMxXcds, rr = nblk % kMxXcds;
   const int id = xcd * q + (xcd < rr ? xcd : rr) + pos;
   const int per_group = group_m * n_nt;
@@ -379,7 +379,7 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
   __shared__ uint32_t sS[2 * (BM + BN) * 3];     // scale bytes of three stages, a row's side by side
 
   int mt, nt;
-  block_tile(n_mt, n_nt, group_m, &mt, &nt);
+  block_tile((int)blockIdx.x, (int)gridDim.x, n_mt, n_nt, group_m, &mt, &nt);
   const int64_t m0 = (int64_t)mt * BM, n0 = (int64_t)nt * BN;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -558,26 +558,24 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Large products of 4-bit activations: 256 x 256 tiles in stages of 256 K.  The
-// loads that reach the second-level cache bound them (8192^3 in stages of 128 K:
-// 301 us, of which 252 remain with the loads alone), so every row of a stage is a
-// whole 128-byte line, in two LDS slots; and the scales, whose bytes of a stage
-// lie in a line of their own for each row, are first laid out stage by stage
-// (stage_scales), so that a stage takes 32 lines of them instead of 512.  264 us,
-// 4.2 PFLOP/s; the matrix cores alone take 203 us at the clock that they leave.
-// 8-bit activations gain 3% from the latter alone and lose it to the extra pass
-// below 300 us: they stay with mx_tile_kernel.
+// Large products: 256 x 256 tiles.  The scale bytes of a stage lie in a line of
+// their own for each row, so they are first laid out stage by stage
+// (stage_scales_kernel): a stage then takes 16 or 32 lines of them instead of 512.
+//
+// 4-bit activations, stages of 256 K: the loads that reach the second-level cache
+// bound them (8192^3 in stages of 128 K: 301 us, of which 252 remain with the loads
+// alone), so every row of a stage is a whole 128-byte line, in two LDS slots.
 // ---------------------------------------------------------------------------
 constexpr int kBigStage = 256, kBigTile = 256;
 
-// out[w][row] (rows: the A rows, then the W rows, each padded to whole tiles): word w % 2 of stage w / 2, 4
-// scale bytes each.  A last stage that K does not fill holds the row's last 8 blocks, 0 in the place of those
-// of earlier stages; padded rows hold 0.
+// out[w][row] (rows: the A rows, then the W rows, each padded to whole tiles): word w of the row's scale bytes,
+// SB / 4 words a stage.  A last stage that K does not fill holds the row's last SB blocks, 0 in the place of
+// those of earlier stages; padded rows hold 0.
+template <int SB>
 __global__ __launch_bounds__(256) void stage_scales_kernel(const uint8_t* __restrict__ as, int64_t M,
                                                            const uint8_t* __restrict__ ws, int64_t N, int kb,
                                                            int64_t m_pad, int64_t rows, uint32_t* __restrict__ out) {
   const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;  // rows is a multiple of 256
-  constexpr int SB = kBigStage / kMxBlock;                      // blocks of a stage
   const bool is_a = row < m_pad;
   const int64_t r = is_a ? row : row - m_pad;
   const bool live = r < (is_a ? M : N);
@@ -620,7 +618,7 @@ __global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restric
   __shared__ __attribute__((aligned(1024))) uint8_t s1[SB];
 
   int mt, nt;
-  block_tile(n_mt, n_nt, group_m, &mt, &nt);
+  block_tile((int)blockIdx.x, (int)gridDim.x, n_mt, n_nt, group_m, &mt, &nt);
   const int64_t m0 = (int64_t)mt * T, n0 = (int64_t)nt * T;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -756,6 +754,226 @@ __global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restric
                                      Y, ld_y);
 }
 
+// 8-bit activations, stages of 128 K in three LDS slots as in mx_tile_kernel, each with its scale words.  At
+// most a block for each compute unit: it goes on to its next tile without a stop, whose first two stages are
+// loaded behind the last two of the one before.  A tile that starts in a block of its own costs 6.3 us, one
+// that follows 3.6 (the results, stored by way of the slot that the last stage leaves, go out while all other
+// blocks store theirs).  4096 x 24576 x 4096: 299-306 us, 315 with a block for each tile; 8192^3: 378 us, 2.9
+// PFLOP/s (383); the matrix cores alone take 301 us there at the clock that they leave.
+template <int YT>
+__global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restrict__ A, int64_t M,
+                                                         const uint8_t* __restrict__ W, int64_t N, int64_t K,
+                                                         const uint32_t* __restrict__ sc, int64_t m_pad, int64_t rows,
+                                                         int n_mt, int n_nt, int group_m, void* __restrict__ Y,
+                                                         int64_t ld_y) {
+  constexpr int T = kBigTile;
+  constexpr int WM = 4, WN = 2, NW = 8, MT = T / WM / 32, NT = T / WN / 32;
+  constexpr int AB = 128, WB = 64;                                    // bytes of a row's stage
+  constexpr int AI = T * AB / 1024 / NW, WI = T * WB / 1024 / NW;     // direct loads of codes a wave and stage
+  constexpr int ND = AI + WI + 1;                                     // and one of scales
+  constexpr int NR = NT + 2 * MT;                                     // LDS reads of a step's fragments
+  constexpr int oW = T * AB, oS = oW + T * WB, SB = oS + 2 * T * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t s2[SB];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int nk = (int)((K + kMxStage - 1) / kMxStage), tiles = n_mt * n_nt;
+  const uint32_t a_row = (uint32_t)K, w_row = (uint32_t)(K / 2);
+
+  // loads: the tile and stage that come next
+  uint32_t va[AI], vw[WI];
+#pragma unroll
+  for (int j = 0; j < AI; ++j) {
+    const int row = (wave * AI + j) * (1024 / AB) + lane / (AB / 16);
+    va[j] = (uint32_t)row * a_row + 16u * (uint32_t)(lane % (AB / 16) ^ swz8(row));
+  }
+#pragma unroll
+  for (int j = 0; j < WI; ++j) {
+    const int row = (wave * WI + j) * 16 + lane / 4;
+    vw[j] = (uint32_t)row * w_row + 16u * (uint32_t)((lane % 4) ^ swz4(row));
+  }
+  struct Tile {
+    int m0, n0;
+  };
+  auto tile_at = [&](int id) {  // past the last one: behind all rows, where nothing is in range
+    int mt, nt;
+    block_tile(id < tiles ? id : 0, tiles, n_mt, n_nt, group_m, &mt, &nt);
+    return Tile{id < tiles ? mt * T : (int)M, id < tiles ? nt * T : (int)N};
+  };
+  Tile now = tile_at((int)blockIdx.x), then = tile_at((int)(blockIdx.x + gridDim.x));  // computed, computed next
+  Tile src = now;  // loaded
+  int l_k = 0;     // and its stage that is loaded next
+  auto load_stage = [&](uint8_t* dst) {
+    const int m0 = __builtin_amdgcn_readfirstlane(src.m0), n0 = __builtin_amdgcn_readfirstlane(src.n0);
+    const int k = __builtin_amdgcn_readfirstlane(l_k);
+    const uint8_t* a_tile = A + (int64_t)m0 * a_row;
+    const uint8_t* w_tile = W + (int64_t)n0 * w_row;
+    const uint32_t a_bytes = (uint32_t)min((int)M - m0, T) * a_row, w_bytes = (uint32_t)min((int)N - n0, T) * w_row;
+    const uint32_t ka = min((uint32_t)k * AB, a_row - AB), kw = min((uint32_t)k * WB, w_row - WB);
+#pragma unroll
+    for (int j = 0; j < AI; ++j) load_lds16(a_tile, a_bytes, dst + (wave * AI + j) * 1024, va[j], ka);
+#pragma unroll
+    for (int j = 0; j < WI; ++j) load_lds16(w_tile, w_bytes, dst + oW + (wave * WI + j) * 1024, vw[j], kw);
+    load_lds4(sc + k * rows + (wave < 4 ? m0 + 64 * wave : m_pad + n0 + 64 * (wave - 4)), a_bytes > 0 ? 256 : 0,
+              dst + oS + 256 * wave, 4u * (uint32_t)lane);
+    const bool wrap = k + 1 == nk;  // without a branch, which would part the stage's products
+    l_k = wrap ? 0 : k + 1;
+    src.m0 = wrap ? then.m0 : m0;
+    src.n0 = wrap ? then.n0 : n0;
+  };
+
+  const int r = lane & 31, h = lane >> 5;
+  const int a_base = (wm * MT * 32 + r) * AB, w_base = oW + (wn * NT * 32 + r) * WB;
+  int kt = 0;
+  // An offset that the compiler takes for one of this stage: it then adds the slot's place to it here instead of
+  // keeping the sums of all slots in registers
+  auto here = [&](int off) {
+    asm("" : "+v"(off) : "s"(kt));
+    return off;
+  };
+  struct Frags {
+    i32x8 a[MT];
+    uint4 w[NT];
+  };
+  struct Scales {
+    uint32_t a[MT], w[NT];
+  };
+  auto read_frags = [&](Frags& f, const uint8_t* tile, int step) {
+    const int ow = here(w_base + 16 * ((2 * step + h) ^ swz4(r)));
+    const int oa0 = here(a_base + 16 * ((4 * step + h) ^ swz8(r))), oa1 = here(a_base + 16 * ((4 * step + 2 + h) ^ swz8(r)));
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      f.w[i] = *(const uint4*)(tile + ow + i * 32 * WB);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      f.a[i] = both4(*(const uint4*)(tile + oa0 + i * 32 * AB), *(const uint4*)(tile + oa1 + i * 32 * AB));
+    }
+  };
+  auto read_scales = [&](Scales& s, const uint8_t* tile) {
+    const uint32_t* pa = (const uint32_t*)(tile + here(oS + 4 * (wm * MT * 32 + r)));
+    const uint32_t* pw = (const uint32_t*)(tile + here(oS + 4 * (T + wn * NT * 32 + r)));
+#pragma unroll
+    for (int i = 0; i < MT; ++i) s.a[i] = pa[32 * i];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) s.w[i] = pw[32 * i];
+  };
+  auto own_bytes = [&](Scales& s, const Scales& raw) {  // the lane's blocks to bytes 0 and 2
+#pragma unroll
+    for (int i = 0; i < MT; ++i) s.a[i] = raw.a[i] >> (8 * h);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) s.w[i] = raw.w[i] >> (8 * h);
+  };
+  f32x16 acc[NT][MT];
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  };
+  auto products = [&](const Frags& f, const Scales& s, int step) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        acc[i][j] = mfma_mx32<kMxFp8>(lo4(f.w[i]), f.a[j], acc[i][j], (int)s.w[i], (int)s.a[j], step);
+  };
+
+  Frags f0, f1;
+  Scales c0, c1;
+  clear();
+
+  // A stage in slot C (its step-0 fragments and scales read), the next one in X, loading the one after into F.
+  // Before the barrier every wave has read the rest of C (lgkmcnt 0), so that it may be filled again, and X has
+  // landed: only the loads into F are younger.
+#define AWQ_MX_STAGE(C, X, F)            \
+  {                                      \
+    own_bytes(c0, c1);                   \
+    read_frags(f1, C, 1);                \
+    load_stage(F);                       \
+    products(f0, c0, 0);                 \
+    interleave<NR, ND>();                \
+    __builtin_amdgcn_sched_barrier(0);   \
+    wait_loads<ND>();                    \
+    block_barrier();                     \
+    __builtin_amdgcn_sched_barrier(0);   \
+    read_scales(c1, X);                  \
+    read_frags(f0, X, 0);                \
+    products(f1, c0, 1);                 \
+    interleave<NR + (MT + NT) / 2, 0>(); \
+    __builtin_amdgcn_sched_barrier(0);   \
+    ++kt;                                \
+  }
+  // The end of a tile, whose last stage was in C: its results go out by way of C
+#define AWQ_MX_STORE(C)                                                                                    \
+  int own = lane; /* opaque, so that nothing made of it is kept in registers meanwhile */                  \
+  asm volatile("" : "+v"(own));                                                                            \
+  const int64_t ym = now.m0 + wm * MT * 32, yn = now.n0 + wn * NT * 32;                                    \
+  if (now.m0 + T <= M && now.n0 + T <= N)                                                                  \
+    store_tile<YT, MT, NT, NW, SB, 1, true>(acc, C, C, C, wave, own, ym, yn, M, N, Y, ld_y);               \
+  else                                                                                                     \
+    store_tile<YT, MT, NT, NW, SB, 1>(acc, C, C, C, wave, own, ym, yn, M, N, Y, ld_y);                     \
+  tile += (int)gridDim.x;
+#define AWQ_MX_NEXT(X)                   \
+  kt = 0;                                \
+  now = then;                            \
+  then = tile_at(tile + (int)gridDim.x); \
+  clear();                               \
+  wait_lds();                            \
+  block_barrier();                       \
+  read_scales(c1, X);                    \
+  read_frags(f0, X, 0);
+#define AWQ_MX_START(C, X) \
+  load_stage(C);           \
+  load_stage(X);           \
+  wait_loads<ND>();        \
+  block_barrier();         \
+  read_scales(c1, C);      \
+  read_frags(f0, C, 0);
+
+  // The block's last stage is to be the third of the loop, its only way out: the stages over are done ahead
+  int tile = (int)blockIdx.x;
+  const int over = (int)((int64_t)((tiles - 1 - tile) / (int)gridDim.x + 1) * nk % 3);
+  if (over == 0) {
+    AWQ_MX_START(s0, s1)
+  } else if (over == 1) {
+    AWQ_MX_START(s2, s0)
+    AWQ_MX_STAGE(s2, s0, s1)
+  } else {
+    AWQ_MX_START(s1, s2)
+    AWQ_MX_STAGE(s1, s2, s0)
+    AWQ_MX_STAGE(s2, s0, s1)
+  }
+  for (;;) {
+    AWQ_MX_STAGE(s0, s1, s2)
+    if (kt == nk) {
+      AWQ_MX_STORE(s0)
+      AWQ_MX_NEXT(s1)
+    }
+    AWQ_MX_STAGE(s1, s2, s0)
+    if (kt == nk) {
+      AWQ_MX_STORE(s1)
+      AWQ_MX_NEXT(s2)
+    }
+    AWQ_MX_STAGE(s2, s0, s1)
+    if (kt == nk) {
+      AWQ_MX_STORE(s2)
+      if (tile >= tiles) break;
+      AWQ_MX_NEXT(s0)
+    }
+  }
+#undef AWQ_MX_START
+#undef AWQ_MX_NEXT
+#undef AWQ_MX_STORE
+#undef AWQ_MX_STAGE
+  wait_loads<0>();  // none may land after the block has given its LDS back
+  block_barrier();
+}
+
 constexpr int kMaxRanges = 8;
 
 // Y = sum over z, in order, of part[z] (fp32 [M, ld_p] each): 4 outputs a thread
@@ -802,8 +1020,8 @@ static FewTile few_tile(int64_t M, int64_t N) {
 // The kernel, its tile and the number of K ranges of a product: the ones with the least estimated time.
 // The estimates are fitted to measurements of N, K in {4096, 12288, 24576} x {1024, 4096, 12288} at 1 to 4096
 // tokens.  E.g. (us, 8 bits; few tokens / tiles of 64 / 128 / 256) 16 x 24576 x 4096: 11.9 / 14.4 / - / -;
-// 24 x 4096 x 12288: 10.7 / 11.3 in 8 ranges / - / -; 256 x 4096 x 4096: - / 12 / 15 / 35; 256 x 4096 x 12288:
-// - / 29 / 24 in 4 ranges / 97; 512 x 24576 x 4096: - / 82 / 54 / 46; 2048 x 4096 x 4096: - / 55 / 35 / 41;
+// 24 x 4096 x 12288: 10.7 / 11.3 in 8 ranges / - / -; 256 x 4096 x 4096: - / 12 / 15 / 40; 256 x 4096 x 12288:
+// - / 29 / 23 in 4 ranges / 104; 512 x 24576 x 4096: - / 82 / 54 / 50; 2048 x 4096 x 4096: - / 55 / 34 / 44;
 // (4 bits) 512 x 24576 x 4096: - / - / 46 / 35; 2048 x 4096 x 12288: - / - / 87 / 73.
 struct MxTiling {
   int tile;   // outputs and tokens a tile: 64, 128 or 256; 0: few tokens
@@ -825,17 +1043,19 @@ static double few_time(int a_fmt, int64_t M, int64_t N, int64_t K) {
   return 1.1 + t;
 }
 // us: for each stage, and for a few more that stand for a tile's start and end, `one` + `more` x load while
-// no compute unit has more than one block (load: blocks for each of the 256), else `full` for a load of 1,
-// a third of that by whole rounds
+// no compute unit has more than one block (load: blocks for each of the 256), else `full` for a load of 1, a
+// third of it by whole rounds (half of it for the persistent blocks)
 static double tile_time(int a_fmt, int tile, double blocks, int stages) {
   struct Cost {
-    double base, ends, one, more, full;
+    double base, ends, one, more, full, whole;
   };
-  static const Cost cost[2][3] = {{{3, 0, 0.17, 0.10, 0.20}, {3, 1.5, 0.30, 0.20, 0.50}, {3, 3.5, 0.82, 0.60, 1.45}},
-                                  {{3, 0, 0.15, 0.09, 0.18}, {3, 1.5, 0.26, 0.17, 0.43}, {7, 3.5, 0.50, 0.40, 1.02}}};
+  static const Cost cost[2][3] = {
+      {{3, 0, 0.17, 0.10, 0.20, 1. / 3}, {3, 1.5, 0.30, 0.20, 0.50, 1. / 3}, {6, 2.5, 0.95, 0.45, 1.40, 1. / 2}},
+      {{3, 0, 0.15, 0.09, 0.18, 1. / 3}, {3, 1.5, 0.26, 0.17, 0.43, 1. / 3}, {7, 3.5, 0.50, 0.40, 1.02, 1. / 3}}};
   const Cost& c = cost[a_fmt == kMxFp8 ? 0 : 1][tile == 64 ? 0 : tile == 128 ? 1 : 2];
   const double load = blocks / 256;
-  return c.base + (stages + c.ends) * (load <= 1 ? c.one + c.more * load : c.full * (ceil(load) + 2 * load) / 3);
+  return c.base + (stages + c.ends) * (load <= 1 ? c.one + c.more * load
+                                                 : c.full * (c.whole * ceil(load) + (1 - c.whole) * load));
 }
 static MxTiling mx_tiling(int a_fmt, int64_t M, int64_t N, int64_t K) {
   const int nk = (int)((K + kMxStage - 1) / kMxStage);
@@ -859,13 +1079,14 @@ static MxTiling mx_tiling(int a_fmt, int64_t M, int64_t N, int64_t K) {
 static int64_t part_ld(int64_t N) { return (N + 3) / 4 * 4; }
 
 static int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
-static int64_t big_scale_words(int64_t M, int64_t N, int64_t K) {
-  return (tiles_of(M, kBigTile) + tiles_of(N, kBigTile)) * kBigTile * ((K + kBigStage - 1) / kBigStage * 2);
+static int64_t big_scale_words(int a_fmt, int64_t M, int64_t N, int64_t K) {
+  const int64_t words = a_fmt == kMxFp8 ? (K + kMxStage - 1) / kMxStage : (K + kBigStage - 1) / kBigStage * 2;
+  return (tiles_of(M, kBigTile) + tiles_of(N, kBigTile)) * kBigTile * words;
 }
 
 size_t mx_matmul_workspace(int a_fmt, int64_t M, int64_t N, int64_t K) {
   const MxTiling t = mx_tiling(a_fmt, M, N, K);
-  if (t.tile == kBigTile && a_fmt == kMxFp4) return (size_t)big_scale_words(M, N, K) * sizeof(uint32_t);
+  if (t.tile == kBigTile) return (size_t)big_scale_words(a_fmt, M, N, K) * sizeof(uint32_t);
   return t.ranges > 1 ? (size_t)t.ranges * M * part_ld(N) * sizeof(float) : 0;
 }
 
@@ -901,20 +1122,24 @@ static void tile_launch(const MxTiling& t, const uint8_t* A, const uint8_t* as, 
   mx_tile_kernel<AF, YT, BM, BN, WM, WN, OCC><<<g, WM * WN * kWave, 0, stream>>>(A, as, M, W, ws, N, K, n_mt, n_nt, 4, \
                                                                                t.split, Y, ld_y)
   if (t.tile == 64) AWQ_TILE(64, 64, 2, 2, 4);
-  else if (t.tile == 128) AWQ_TILE(128, 128, 2, 2, 2);
-  else if constexpr (AF == kMxFp8 && YT != 2) AWQ_TILE(256, 256, 4, 2, 2);
+  else AWQ_TILE(128, 128, 2, 2, 2);
 #undef AWQ_TILE
 }
 
-template <int YT>
+template <int AF, int YT>
 static void big_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uint8_t* W, const uint8_t* ws, int64_t N,
                        int64_t K, void* Y, int64_t ld_y, uint32_t* sc, hipStream_t stream) {
   const int n_mt = (int)tiles_of(M, kBigTile), n_nt = (int)tiles_of(N, kBigTile), kb = (int)(K / kMxBlock);
   const int64_t m_pad = (int64_t)n_mt * kBigTile, rows = m_pad + (int64_t)n_nt * kBigTile;
-  stage_scales_kernel<<<dim3((unsigned)(rows / 256), (unsigned)((kb + 15) / 16)), 256, 0, stream>>>(as, M, ws, N, kb,
-                                                                                                   m_pad, rows, sc);
-  mx_big_kernel<YT><<<(unsigned)(n_mt * n_nt), 512, 0, stream>>>(A, M, W, N, K, sc, m_pad, rows, n_mt, n_nt, 4, Y,
-                                                                ld_y);
+  constexpr int SB = (AF == kMxFp8 ? kMxStage : kBigStage) / kMxBlock;
+  stage_scales_kernel<SB><<<dim3((unsigned)(rows / 256), (unsigned)((kb + 15) / 16)), 256, 0, stream>>>(
+      as, M, ws, N, kb, m_pad, rows, sc);
+  if constexpr (AF == kMxFp8)
+    mx_big8_kernel<YT><<<(unsigned)(n_mt * n_nt < 256 ? n_mt * n_nt : 256), 512, 0, stream>>>(
+        A, M, W, N, K, sc, m_pad, rows, n_mt, n_nt, 4, Y, ld_y);
+  else
+    mx_big_kernel<YT><<<(unsigned)(n_mt * n_nt), 512, 0, stream>>>(A, M, W, N, K, sc, m_pad, rows, n_mt, n_nt, 4, Y,
+                                                                   ld_y);
 }
 
 template <int AF, int YT>
@@ -923,8 +1148,8 @@ static void product_launch(const uint8_t* A, const uint8_t* as, int64_t M, const
   const MxTiling t = mx_tiling(AF, M, N, K);
   if (t.tile == 0) {
     few_launch<AF>(A, as, M, W, ws, N, K, Y, ld_y, YT, stream);
-  } else if (AF == kMxFp4 && t.tile == kBigTile) {
-    big_launch<YT>(A, as, M, W, ws, N, K, Y, ld_y, (uint32_t*)part, stream);
+  } else if (t.tile == kBigTile) {
+    if constexpr (AF == kMxFp4 || YT != 2) big_launch<AF, YT>(A, as, M, W, ws, N, K, Y, ld_y, (uint32_t*)part, stream);
   } else if (t.ranges == 1) {
     tile_launch<AF, YT>(t, A, as, M, W, ws, N, K, Y, ld_y, stream);
   } else {

@@ -604,3 +604,33 @@ def test_product_large(A, M, N, K, fmt, dtype):
     """Enough outputs for the largest tiles; lengths that leave 1, 2, 3 blocks and more in the last stage."""
     say(f"mx_matmul large {M}x{N}x{K} {fmt} {dtype}")
     check_product(A, M, N, K, fmt, dtype, ld_y=N + 3)
+
+
+@pytest.mark.parametrize("M,N,K,fmt,dtype", [
+    (4000, 16001, 384, "fp8", "bf16"), (4000, 16001, 416, "fp8", "f16"), (3999, 16001, 544, "fp8", "bf16"),
+    (4000, 16001, 608, "fp8", "f16"), (4096, 16128, 416, "fp8", "bf16"), (4096, 16128, 512, "fp8", "f16"),
+    (4096, 16128, 736, "fp8", "bf16"), (2100, 12250, 1088, "fp8", "bf16"), (1023, 16001, 1056, "fp8", "f16"),
+    (4000, 16001, 384, "fp4", "f32"), (4000, 16001, 416, "fp4", "bf16"), (4096, 16128, 544, "fp4", "f16"),
+    (2100, 12250, 1120, "fp4", "bf16"), (1000, 12250, 1216, "fp4", "f32"),
+])
+def test_product_largest(A, M, N, K, fmt, dtype):
+    """Several of the largest tiles for each compute unit, whole ones and cut ones, over 3 to 9 stages of K, so
+    that a unit's tiles end in each of its buffers.  Compared with the product in 64 bits on the device."""
+    import torch
+    say(f"mx_matmul largest {M}x{N}x{K} {fmt} {dtype}")
+    assert A.mx_matmul_workspace_bytes(fmt, M, N, K) > 0
+    rng = np.random.default_rng(M + 3 * N + 7 * K)
+    (ac, asc), (wc, wsc) = random_mx(rng, M, K, fmt), random_mx(rng, N, K, "fp4")
+    buf = torch.full((M * (N + 3) + 1,), 7.0, dtype=tdt(dtype), device="cuda")
+    out = buf[1:].view(M, N + 3)[:, :N]
+    out.fill_(float("nan"))
+    Y = A.mx_matmul(*dev_mx(ac, asc, fmt), *dev_mx(wc, wsc, "fp4"), out=out)
+    a, w = (torch.from_numpy(O.mx_values(c, sc, f)).double().cuda() for c, sc, f in ((ac, asc, fmt), (wc, wsc, "fp4")))
+    y, tol = a @ w.T, a.abs() @ w.abs().T
+    tol *= (K // 128 + 16) * 2 * U
+    if fmt == "fp8":
+        m8 = lambda v: v.abs().view(v.shape[0], -1, 8).amax(dim=2)
+        tol += 2.0 ** -10 * (m8(a) @ m8(w).T)
+    tol += STEP[dtype] * (y.abs() + tol) + (2.0 ** -25 if dtype == "f16" else 0.0)
+    assert bool(((Y.double() - y).abs() <= tol).all())
+    assert buf[0] == 7 and buf[1:].view(M, N + 3)[:, N:].eq(7).all()
