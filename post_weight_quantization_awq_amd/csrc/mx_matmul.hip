@@ -105,7 +105,7 @@ __device__ __forceinline__ FewScales<ST> few_scales(const uint8_t* row, int c, i
   return s;
 }
 
-// AR: LDS rows of activations (4, or 16 a tile of tokens); with 4 the lanes of the 12 other rows read these
+// AR: LDS rows of activations (4, 16, 24 or 32); the lanes of rows past them read others, unused
 template <int AF, int AR, int NT, int ST, int OCC>
 __global__ __launch_bounds__(kFewWaves * kWave, OCC) void mx_few_kernel(const uint8_t* __restrict__ A,
                                                                        const uint8_t* __restrict__ as, int64_t M,
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(kFewWaves * kWave, OCC) void mx_few_kernel(const ui
       }
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const int m = AR < 16 ? r % AR : 16 * t + r;
+      const int m = 16 * t + (AR - 16 * t < 16 ? r % (AR - 16 * t) : r);
       auto piece = [&](int c) { return *(const uint4*)(buf + m * RB + 16 * (c ^ (CR >= 16 ? m & 15 : swz8(m)))); };
 #pragma unroll
       for (int j = 0; j < ST; ++j) {
@@ -1011,20 +1011,23 @@ __global__ __launch_bounds__(256) void mx_reduce_kernel(const float* __restrict_
 
 // Few tokens: LDS rows of activations, and 16-output tiles a block: two where that still leaves every
 // compute unit a block (16 tokens, us: 24576 x 4096 14.8 -> 11.9, 6144 x 4096 6.5 -> 5.5; but 4096 x 12288,
-// 256 tiles, 8.3 -> 10.5), one for up to 4 tokens (24576 x 4096 11.8, 12.9 with two).
+// 256 tiles, 8.3 -> 10.5), one for up to 4 tokens (24576 x 4096 11.8, 12.9 with two).  24 rows save what the 8
+// others cost with 8-bit activations and one tile (24 tokens, 4096 x 12288: 10.3 -> 9.9; 14.4 both at 24576 x
+// 4096, two tiles; 8.1 -> 8.3 in 4 bits).
 struct FewTile {
   int rows, tiles;
 };
-static FewTile few_tile(int64_t M, int64_t N) {
+static FewTile few_tile(int a_fmt, int64_t M, int64_t N) {
   if (M <= 4) return {4, 1};
   const int rows = M <= 16 ? 16 : 32;
-  return {rows, (N + 15) / 16 * ((M + rows - 1) / rows) > 256 ? 2 : 1};
+  const int tiles = (N + 15) / 16 * ((M + rows - 1) / rows) > 256 ? 2 : 1;
+  return {a_fmt == kMxFp8 && rows == 32 && M <= 24 && tiles == 1 ? 24 : rows, tiles};
 }
 
 // The kernel, its tile and the number of K ranges of a product: the ones with the least estimated time.
 // The estimates are fitted to measurements of N, K in {4096, 12288, 24576} x {1024, 4096, 12288} at 1 to 4096
-// tokens.  E.g. (us, 8 bits; few tokens / tiles of 64 / 128 / 256) 16 x 24576 x 4096: 11.9 / 14.4 / - / -;
-// 24 x 4096 x 12288: 10.7 / 11.3 in 8 ranges / - / -; 256 x 4096 x 4096: - / 12 / 15 / 40; 256 x 4096 x 12288:
+// tokens.  E.g. (us, 8 bits; few tokens / tiles of 64 / 128 / 256) 16 x 24576 x 4096: 11.6 / 14.4 / - / -;
+// 24 x 4096 x 12288: 9.9 / 11.3 in 8 ranges / - / -; 256 x 4096 x 4096: - / 12 / 15 / 40; 256 x 4096 x 12288:
 // - / 29 / 23 in 4 ranges / 104; 512 x 24576 x 4096: - / 82 / 54 / 50; 2048 x 4096 x 4096: - / 55 / 34 / 44;
 // (4 bits) 512 x 24576 x 4096: - / - / 46 / 35; 2048 x 4096 x 12288: - / - / 87 / 73.
 struct MxTiling {
@@ -1033,16 +1036,19 @@ struct MxTiling {
   int ranges;
 };
 // us: the weights at 5 TB/s, for every further block row at 10 TB/s, and the activations that all blocks
-// read at 50 TB/s for 16 rows, 22 TB/s (and 1.3 more) for 32, these in whole rounds of 256 blocks
+// read at 50 TB/s for 16 rows, 20 TB/s (and 0.3 more) above, these in whole rounds of 256 blocks
+// of at least 2.2 us
 static double few_time(int a_fmt, int64_t M, int64_t N, int64_t K) {
-  const FewTile f = few_tile(M, N);
+  const FewTile f = few_tile(a_fmt, M, N);
   const double w_mb = (double)N * (double)K * (17.0 / 32) * 1e-6;
   const double a_mb = (double)M * (double)K * (a_fmt == kMxFp8 ? 1.0 : 0.5) * 1e-6;
   const double cols = (double)((N + 16 * f.tiles - 1) / (16 * f.tiles)), rows = (double)((M + f.rows - 1) / f.rows);
-  double t = w_mb / 5 + (rows - 1) * w_mb / 10 + (f.rows == 4 ? 0.0 : f.rows == 16 ? 0.02 : 0.045) * cols * a_mb;
-  if (f.rows == 32) {
-    t += 1.3;
-    if (cols * rows > 256) t *= ceil(cols * rows / 256) * 256 / (cols * rows);
+  double t = w_mb / 5 + (rows - 1) * w_mb / 10 + (f.rows == 4 ? 0.0 : f.rows == 16 ? 0.02 : 0.05) * cols * a_mb;
+  if (f.rows >= 24) {
+    const double rounds = ceil(cols * rows / 256);
+    t += 0.3;
+    if (rounds > 1) t *= rounds * 256 / (cols * rows);
+    t = t < 2.2 * rounds ? 2.2 * rounds : t;
   }
   return 1.1 + t;
 }
@@ -1097,7 +1103,7 @@ size_t mx_matmul_workspace(int a_fmt, int64_t M, int64_t N, int64_t K) {
 template <int AF>
 static void few_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uint8_t* W, const uint8_t* ws, int64_t N,
                        int64_t K, void* Y, int64_t ld_y, int y_dtype, hipStream_t stream) {
-  const FewTile f = few_tile(M, N);
+  const FewTile f = few_tile(AF, M, N);
   const int64_t a_row = AF == kMxFp8 ? K : K / 2, y_bytes = y_dtype == 2 ? 4 : 2;
   constexpr int64_t kRows = 65535 * 4;  // of a launch: the grid's second dimension holds 65535 blocks
   for (int64_t m = 0; m < M; m += kRows) {
@@ -1111,8 +1117,9 @@ static void few_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uin
     if (f.rows == 4) AWQ_FEW(4, 1, 4, 4);
     else if (f.rows == 16 && f.tiles == 1) AWQ_FEW(16, 1, 2, 4);
     else if (f.rows == 16) AWQ_FEW(16, 2, 2, 4);
-    else if (f.tiles == 1) AWQ_FEW(32, 1, 2, kOcc32);
-    else AWQ_FEW(32, 2, 2, 2);
+    else if (f.tiles == 2) AWQ_FEW(32, 2, 2, 2);
+    else if (f.rows == 32) AWQ_FEW(32, 1, 2, kOcc32);
+    else if constexpr (AF == kMxFp8) AWQ_FEW(24, 1, 2, 2);
   }
 #undef AWQ_FEW
 }

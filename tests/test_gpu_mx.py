@@ -362,8 +362,8 @@ def test_product_sizes(A, M, N, K, fmt, dtype):
 
 
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
-@pytest.mark.parametrize("M", [1, 3, 4, 5, 16, 17, 40])
-@pytest.mark.parametrize("N,K", [(4112, 544), (8208, 1184), (48, 4640), (16, 8192)])
+@pytest.mark.parametrize("M", [1, 3, 4, 5, 16, 17, 24, 25, 40])
+@pytest.mark.parametrize("N,K", [(4112, 544), (8208, 1184), (4099, 2080), (48, 4640), (16, 8192)])
 def test_product_few_rows(A, M, N, K, fmt):
     """Few tokens against few and many outputs: every tile of them, K in one chunk a wave and in several."""
     say(f"mx_matmul few M {M} N {N} K {K} {fmt}")
