@@ -82,9 +82,11 @@ __device__ __forceinline__ void load_lds4(const void* base, uint32_t bytes, uint
 // 24576 x 4096: 14.3 us).  So the weights, used once, are read 64 bytes of a row by
 // 4 lanes and turned by lane permutations (12.5 us), and the activations go through
 // LDS, each wave's through buffers of its own and by direct loads of whole rows,
-// which cost nothing for rows past the last token (16 tokens, 4096 x 12288: 11.7 us
-// loaded by the lanes, 8.3 us so).  For up to 4 tokens 4 LDS rows leave room for
-// more blocks (11.8 us, 4.5 TB/s).
+// which read nothing for rows past the last token (16 tokens, 4096 x 12288: 11.7 us
+// loaded by the lanes, 8.3 us so, 8.1 through registers).  For up to 4 tokens 4 LDS
+// rows leave room for more blocks (11.8 us, 4.5 TB/s).  With more, the path of the
+// activations into LDS bounds it: 24 tokens, 4096 x 12288: 9.7 us, 295 KB a compute
+// unit, its data unit busy 75% of the time.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
 
