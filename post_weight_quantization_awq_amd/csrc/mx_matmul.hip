@@ -120,7 +120,8 @@ __global__ __launch_bounds__(kFewWaves * kWave, OCC) void mx_few_kernel(const ui
   constexpr int CR = RB / 16;                            // 16-byte pieces of it
   constexpr int DI = AR * RB / 1024;                     // direct loads of a chunk, a KiB each
   static_assert(DI >= 1, "whole loads");
-  constexpr int BS = AR * RB > 4 * NT * MT * 16 * 17 ? AR * RB : 4 * NT * MT * 16 * 17;  // a wave's buffer: chunk, later sums
+  // a wave's buffer: chunk, later sums
+  constexpr int BS = AR * RB > 4 * NT * MT * 16 * 17 ? AR * RB : 4 * NT * MT * 16 * 17;
   __shared__ __attribute__((aligned(1024))) uint8_t b0[kFewWaves][(BS + 1023) / 1024 * 1024];
   __shared__ __attribute__((aligned(1024))) uint8_t b1[kFewWaves][AR * RB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -262,12 +263,12 @@ __global__ __launch_bounds__(kFewWaves * kWave, OCC) void mx_few_kernel(const ui
 // ---------------------------------------------------------------------------
 // Many tokens: tiles of BM tokens x BN outputs staged through LDS.
 //
-// K advances in stages of 128 through a ring of three LDS slots, filled by direct
-// loads (16 bytes a lane, no registers) two stages ahead.  A stage is two steps of
-// v_mfma_scale_f32_32x32x64_f8f6f4; the fragments of a step are read from LDS
-// while the matrix cores work on the step before, across the stage boundary too:
-// the block's one barrier a stage stands between the two steps, where the next
-// stage's loads must have landed.
+// K advances in stages of 128 through a ring of NS LDS slots (three or six), filled
+// by direct loads (16 bytes a lane, no registers) NS - 1 stages ahead.  A stage is
+// two steps of v_mfma_scale_f32_32x32x64_f8f6f4; the fragments of a step are read
+// from LDS while the matrix cores work on the step before, across the stage
+// boundary too: the block's one barrier a stage stands between the two steps, where
+// the next stage's loads must have landed.
 // ---------------------------------------------------------------------------
 template <int AF>
 __device__ __forceinline__ f32x16 mfma_mx32(const i32x8 w, const i32x8 a, f32x16 c, int ws, int as, int step) {
@@ -366,7 +367,7 @@ __device__ __forceinline__ void block_tile(int bid, int nblk, int n_mt, int n_nt
 
 // OCC: waves a SIMD that the registers are to leave room for.  blockIdx.y: one of gridDim.y ranges of
 // `split` stages of K; range z's sums go to Y + z M ld_y (YT 2).
-template <int AF, int YT, int BM, int BN, int WM, int WN, int OCC>
+template <int AF, int YT, int BM, int BN, int WM, int WN, int NS, int OCC>
 __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ as, int64_t M, const uint8_t* __restrict__ W,
     const uint8_t* __restrict__ ws, int64_t N, int64_t K, int n_mt, int n_nt, int group_m, int split,
@@ -382,6 +383,9 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
   __shared__ __attribute__((aligned(1024))) uint8_t s0[BM * AB + BN * WB];
   __shared__ __attribute__((aligned(1024))) uint8_t s1[BM * AB + BN * WB];
   __shared__ __attribute__((aligned(1024))) uint8_t s2[BM * AB + BN * WB];
+  __shared__ __attribute__((aligned(1024))) uint8_t s3[NS > 3 ? BM * AB + BN * WB : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t s4[NS > 3 ? BM * AB + BN * WB : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t s5[NS > 3 ? BM * AB + BN * WB : 16];
   __shared__ uint32_t sS[2 * (BM + BN) * 3];     // scale bytes of three stages, a row's side by side
 
   int mt, nt;
@@ -407,7 +411,8 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
 #pragma unroll
   for (int j = 0; j < AI; ++j) {
     const int row = (wave * AI + j) * (1024 / AB) + lane / (AB / 16), slot = lane % (AB / 16);
-    va[j] = row < m_rows ? (uint32_t)row * a_row + 16u * (uint32_t)(slot ^ (AF == kMxFp8 ? swz8(row) : swz4(row))) : kMxOut;
+    va[j] = row < m_rows ? (uint32_t)row * a_row + 16u * (uint32_t)(slot ^ (AF == kMxFp8 ? swz8(row) : swz4(row)))
+                         : kMxOut;
   }
 #pragma unroll
   for (int j = 0; j < WI; ++j) {
@@ -510,50 +515,74 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
       for (int i = 0; i < NT; ++i) acc[i][j] = mfma_mx32<AF>(lo4(f.w[i]), f.a[j], acc[i][j], s.w[i], s.a[j], step);
   };
 
+  load_scales(0);
+  hold_order();
   load_stage(s0, 0);
   load_stage(s1, 1);
-  load_scales(0);
+  if constexpr (NS > 3) {
+    load_stage(s2, 2);
+    load_stage(s3, 3);
+    load_stage(s4, 4);
+  }
+  hold_order();
   write_scales(0);
   load_scales(1);
-  wait_loads<0>();
+  wait_loads<(NS - 2) * ND>();
   block_barrier();
   Frags f0, f1;
   Scales c0, c1;
   read_frags(f0, s0, 0);
   read_scales(c1, 0, 0);
 
-  // Stage kt in slot P = kt % 3 (array C), its step-0 fragments read.  Before the barrier every wave has
-  // read the rest of the stage (lgkmcnt 0), so its slot may be filled again by stage kt + 3; and stage
-  // kt + 1 (array X) has landed: only the loads of stage kt + 2 (array F) are younger.  Loads past the
+  // Stage kt in slot P = kt % NS (array C), its step-0 fragments read.  Before the barrier every wave has
+  // read the rest of the stage (lgkmcnt 0), so its slot may be filled again by stage kt + NS; and stage
+  // kt + 1 (array X) has landed: only the loads of the NS - 2 stages behind it are younger.  Loads past the
   // last stage repeat its last chunks.
-#define AWQ_MX_STAGE(P, C, X, F)                  \
-  {                                               \
-    own_bytes(c0, c1);                            \
-    read_frags(f1, C, 1);                         \
-    load_stage(F, kt + 2);                        \
-    if (P == 2) write_scales(ss + 1);             \
-    products(f0, c0, 0);                          \
-    interleave<NR, ND>();                         \
-    __builtin_amdgcn_sched_barrier(0);            \
-    wait_loads<ND>();                             \
-    block_barrier();                              \
-    __builtin_amdgcn_sched_barrier(0);            \
-    if (P == 2) load_scales(ss + 2);              \
-    read_scales(c1, ss + (P == 2), (P + 1) % 3);  \
-    read_frags(f0, X, 0);                         \
-    products(f1, c0, 1);                          \
-    interleave<NR + (MT + NT) / 2, 0>();          \
-    __builtin_amdgcn_sched_barrier(0);            \
-    ++kt;                                         \
+#define AWQ_MX_STAGE(P, C, X, F)                      \
+  {                                                   \
+    own_bytes(c0, c1);                                \
+    read_frags(f1, C, 1);                             \
+    load_stage(F, kt + NS - 1);                       \
+    if (P % 3 == 2) write_scales(ss + 1);             \
+    products(f0, c0, 0);                              \
+    interleave<NR, ND>();                             \
+    __builtin_amdgcn_sched_barrier(0);                \
+    wait_loads<(NS - 2) * ND>();                      \
+    block_barrier();                                  \
+    __builtin_amdgcn_sched_barrier(0);                \
+    if (P % 3 == 2) load_scales(ss + 2);              \
+    read_scales(c1, ss + (P % 3 == 2), (P + 1) % 3);  \
+    read_frags(f0, X, 0);                             \
+    products(f1, c0, 1);                              \
+    interleave<NR + (MT + NT) / 2, 0>();              \
+    __builtin_amdgcn_sched_barrier(0);                \
+    ++kt;                                             \
+    if (P % 3 == 2) ++ss;                             \
   }
   int kt = 0, ss = 0;  // ss = kt / 3
-  for (; kt + 3 <= nk; ++ss) {
-    AWQ_MX_STAGE(0, s0, s1, s2)
-    AWQ_MX_STAGE(1, s1, s2, s0)
-    AWQ_MX_STAGE(2, s2, s0, s1)
+  if constexpr (NS == 3) {
+    while (kt + 3 <= nk) {
+      AWQ_MX_STAGE(0, s0, s1, s2)
+      AWQ_MX_STAGE(1, s1, s2, s0)
+      AWQ_MX_STAGE(2, s2, s0, s1)
+    }
+    if (kt < nk) AWQ_MX_STAGE(0, s0, s1, s2)
+    if (kt < nk) AWQ_MX_STAGE(1, s1, s2, s0)
+  } else {
+    while (kt + 6 <= nk) {
+      AWQ_MX_STAGE(0, s0, s1, s5)
+      AWQ_MX_STAGE(1, s1, s2, s0)
+      AWQ_MX_STAGE(2, s2, s3, s1)
+      AWQ_MX_STAGE(3, s3, s4, s2)
+      AWQ_MX_STAGE(4, s4, s5, s3)
+      AWQ_MX_STAGE(5, s5, s0, s4)
+    }
+    if (kt < nk) AWQ_MX_STAGE(0, s0, s1, s5)
+    if (kt < nk) AWQ_MX_STAGE(1, s1, s2, s0)
+    if (kt < nk) AWQ_MX_STAGE(2, s2, s3, s1)
+    if (kt < nk) AWQ_MX_STAGE(3, s3, s4, s2)
+    if (kt < nk) AWQ_MX_STAGE(4, s4, s5, s3)
   }
-  if (kt < nk) AWQ_MX_STAGE(0, s0, s1, s2)
-  if (kt < nk) AWQ_MX_STAGE(1, s1, s2, s0)
 #undef AWQ_MX_STAGE
 
   wait_loads<0>();  // none may land after the block has given its LDS back
@@ -849,7 +878,8 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
   };
   auto read_frags = [&](Frags& f, const uint8_t* tile, int step) {
     const int ow = here(w_base + 16 * ((2 * step + h) ^ swz4(r)));
-    const int oa0 = here(a_base + 16 * ((4 * step + h) ^ swz8(r))), oa1 = here(a_base + 16 * ((4 * step + 2 + h) ^ swz8(r)));
+    const int oa0 = here(a_base + 16 * ((4 * step + h) ^ swz8(r)));
+    const int oa1 = here(a_base + 16 * ((4 * step + 2 + h) ^ swz8(r)));
 #pragma unroll
     for (int i = 0; i < NT; ++i)
       f.w[i] = *(const uint4*)(tile + ow + i * 32 * WB);
@@ -1029,7 +1059,7 @@ static FewTile few_tile(int a_fmt, int64_t M, int64_t N) {
 // The kernel, its tile and the number of K ranges of a product: the ones with the least estimated time.
 // The estimates are fitted to measurements of N, K in {4096, 12288, 24576} x {1024, 4096, 12288} at 1 to 4096
 // tokens.  E.g. (us, 8 bits; few tokens / tiles of 64 / 128 / 256) 16 x 24576 x 4096: 11.6 / 14.4 / - / -;
-// 24 x 4096 x 12288: 9.9 / 11.3 in 8 ranges / - / -; 256 x 4096 x 4096: - / 12 / 15 / 40; 256 x 4096 x 12288:
+// 24 x 4096 x 12288: 9.9 / 11.3 in 8 ranges / - / -; 256 x 4096 x 4096: - / 10 / 15 / 40; 256 x 4096 x 12288:
 // - / 29 / 23 in 4 ranges / 104; 512 x 24576 x 4096: - / 82 / 54 / 50; 2048 x 4096 x 4096: - / 55 / 34 / 44;
 // (4 bits) 512 x 24576 x 4096: - / - / 46 / 35; 2048 x 4096 x 12288: - / - / 87 / 73.
 struct MxTiling {
@@ -1037,15 +1067,16 @@ struct MxTiling {
   int split;  // stages a range
   int ranges;
 };
-// us: the weights at 5 TB/s, for every further block row at 10 TB/s, and the activations that all blocks
-// read at 50 TB/s for 16 rows, 20 TB/s (and 0.3 more) above, these in whole rounds of 256 blocks
-// of at least 2.2 us
+// us: the weights at 5 TB/s, for every further block row at 10 TB/s, and the activations that all blocks read
+// at 50 TB/s for 16 rows, 20 or (4 bits) 29 TB/s and 0.3 more above, these in whole rounds of 256 blocks of at
+// least 2.2 us
 static double few_time(int a_fmt, int64_t M, int64_t N, int64_t K) {
   const FewTile f = few_tile(a_fmt, M, N);
   const double w_mb = (double)N * (double)K * (17.0 / 32) * 1e-6;
   const double a_mb = (double)M * (double)K * (a_fmt == kMxFp8 ? 1.0 : 0.5) * 1e-6;
   const double cols = (double)((N + 16 * f.tiles - 1) / (16 * f.tiles)), rows = (double)((M + f.rows - 1) / f.rows);
-  double t = w_mb / 5 + (rows - 1) * w_mb / 10 + (f.rows == 4 ? 0.0 : f.rows == 16 ? 0.02 : 0.05) * cols * a_mb;
+  const double a_cost = f.rows == 4 ? 0.0 : f.rows == 16 ? 0.02 : a_fmt == kMxFp8 ? 0.05 : 0.035;
+  double t = w_mb / 5 + (rows - 1) * w_mb / 10 + a_cost * cols * a_mb;
   if (f.rows >= 24) {
     const double rounds = ceil(cols * rows / 256);
     t += 0.3;
@@ -1062,8 +1093,8 @@ static double tile_time(int a_fmt, int tile, double blocks, int stages) {
     double base, ends, one, more, full, whole;
   };
   static const Cost cost[2][3] = {
-      {{3, 0, 0.17, 0.10, 0.20, 1. / 3}, {3, 1.5, 0.30, 0.20, 0.50, 1. / 3}, {6, 2.5, 0.95, 0.45, 1.40, 1. / 2}},
-      {{3, 0, 0.15, 0.09, 0.18, 1. / 3}, {3, 1.5, 0.26, 0.17, 0.43, 1. / 3}, {7, 3.5, 0.50, 0.40, 1.02, 1. / 3}}};
+      {{3, 0, 0.18, 0.04, 0.20, 1. / 3}, {3, 1.5, 0.30, 0.20, 0.50, 1. / 3}, {6, 2.5, 0.95, 0.45, 1.40, 1. / 2}},
+      {{3.3, 0, 0.125, 0.05, 0.18, 1. / 3}, {3, 1.5, 0.26, 0.17, 0.43, 1. / 3}, {7, 3.5, 0.50, 0.40, 1.02, 1. / 3}}};
   const Cost& c = cost[a_fmt == kMxFp8 ? 0 : 1][tile == 64 ? 0 : tile == 128 ? 1 : 2];
   const double load = blocks / 256;
   return c.base + (stages + c.ends) * (load <= 1 ? c.one + c.more * load
@@ -1126,16 +1157,22 @@ static void few_launch(const uint8_t* A, const uint8_t* as, int64_t M, const uin
 #undef AWQ_FEW
 }
 
+// Slots of the 64 x 64 tiles: six, for loads five stages ahead, where no compute unit has more than one block
+// and there are stages to load ahead (256 x 4096 x 4096, us: 8 bits 11.9 -> 10.1, 4 bits 11.1 -> 8.6); else three,
+// which leave room for more blocks (512 x 4096 x 4096 in 8 bits: 16.4, 17.0 with six; 32 x 12288 x 1024, 8
+// stages: 4.2, 4.6 with six).  Six slots of 128 x 128 tiles gain 0 to 6% there and lose 15 to 30% of larger
+// products.
 template <int AF, int YT>
 static void tile_launch(const MxTiling& t, const uint8_t* A, const uint8_t* as, int64_t M, const uint8_t* W,
                         const uint8_t* ws, int64_t N, int64_t K, void* Y, int64_t ld_y, hipStream_t stream) {
   const int n_mt = (int)tiles_of(M, t.tile), n_nt = (int)tiles_of(N, t.tile);
   const dim3 g((unsigned)(n_mt * n_nt), (unsigned)t.ranges);
-#define AWQ_TILE(BM, BN, WM, WN, OCC)                                                                               \
-  mx_tile_kernel<AF, YT, BM, BN, WM, WN, OCC><<<g, WM * WN * kWave, 0, stream>>>(A, as, M, W, ws, N, K, n_mt, n_nt, 4, \
+#define AWQ_TILE(BM, BN, WM, WN, NS, OCC)                                                                           \
+  mx_tile_kernel<AF, YT, BM, BN, WM, WN, NS, OCC><<<g, WM * WN * kWave, 0, stream>>>(A, as, M, W, ws, N, K, n_mt, n_nt, 4, \
                                                                                t.split, Y, ld_y)
-  if (t.tile == 64) AWQ_TILE(64, 64, 2, 2, 4);
-  else AWQ_TILE(128, 128, 2, 2, 2);
+  if (t.tile == 64 && (int64_t)n_mt * n_nt * t.ranges <= 256 && t.split >= 12) AWQ_TILE(64, 64, 2, 2, 6, 2);
+  else if (t.tile == 64) AWQ_TILE(64, 64, 2, 2, 3, 4);
+  else AWQ_TILE(128, 128, 2, 2, 3, 2);
 #undef AWQ_TILE
 }
 

@@ -370,6 +370,14 @@ def test_product_few_rows(A, M, N, K, fmt):
     check_product(A, M, N, K, fmt, "bf16")
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("K", [1504, 1536, 1568, 1632, 1760, 1888, 2016, 2144, 6176, 12288])
+def test_product_stages(A, K, fmt):
+    """Few tiles for each length of a row's last turn through the buffers, K in one range and in several."""
+    say(f"mx_matmul stages K {K} {fmt}")
+    check_product(A, 130, 333, K, fmt, "f16", ld_y=335)
+
+
 def test_product_many_rows_short(A):
     """More rows than one launch's grid holds, K too short for the tiles."""
     import torch
