@@ -6,6 +6,7 @@
 
 #include "awq_launch.h"
 #include "mx_device.h"
+#include "mx_tiles.h"
 
 namespace awq {
 
@@ -278,8 +279,6 @@ __device__ __forceinline__ f32x16 mfma_mx32(const i32x8 w, const i32x8 a, f32x16
              : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, c, 4, AF == kMxFp8 ? 0 : 4, 2, ws, 2, as);
 }
 
-constexpr int kMxXcds = 8;
-constexpr int kMxStage = 128;   // K per stage
 // Issue order of half a stage: two LDS reads and one or two direct loads behind each MFMA, so that
 // they are under way early and the matrix cores never wait for a burst of them
 template <int READS, int LOADS>
@@ -352,17 +351,6 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[NT][MT], uint8_t*
       }
       __builtin_amdgcn_wave_barrier();
     }
-}
-
-// The tile of a block: each XCD owns a contiguous range of tiles, walked in groups of group_m token tiles
-__device__ __forceinline__ void block_tile(int bid, int nblk, int n_mt, int n_nt, int group_m, int* mt, int* nt) {
-  const int xcd = bid % kMxXcds, pos = bid / kMxXcds, q = nblk / kMxXcds, rr = nblk % kMxXcds;
-  const int id = xcd * q + (xcd < rr ? xcd : rr) + pos;
-  const int per_group = group_m * n_nt;
-  const int first_m = id / per_group * group_m;
-  const int gsz = n_mt - first_m < group_m ? n_mt - first_m : group_m;
-  *mt = first_m + id % per_group % gsz;
-  *nt = id % per_group / gsz;
 }
 
 // OCC: waves a SIMD that the registers are to leave room for.  blockIdx.y: one of gridDim.y ranges of
@@ -601,7 +589,7 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
 // bound them (8192^3 in stages of 128 K: 301 us, of which 252 remain with the loads
 // alone), so every row of a stage is a whole 128-byte line, in two LDS slots.
 // ---------------------------------------------------------------------------
-constexpr int kBigStage = 256, kBigTile = 256;
+constexpr int kBigStage = 256;
 
 // out[w][row] (rows: the A rows, then the W rows, each padded to whole tiles): word w of the row's scale bytes,
 // SB / 4 words a stage.  A last stage that K does not fill holds the row's last SB blocks, 0 in the place of
@@ -830,29 +818,21 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
     const int row = (wave * WI + j) * 16 + lane / 4;
     vw[j] = (uint32_t)row * w_row + 16u * (uint32_t)((lane % 4) ^ swz4(row));
   }
-  struct Tile {
-    int m0, n0;
-  };
-  auto tile_at = [&](int id) {  // past the last one: behind all rows, where nothing is in range
-    int mt, nt;
-    block_tile(id < tiles ? id : 0, tiles, n_mt, n_nt, group_m, &mt, &nt);
-    return Tile{id < tiles ? mt * T : (int)M, id < tiles ? nt * T : (int)N};
-  };
-  Tile now = tile_at((int)blockIdx.x), then = tile_at((int)(blockIdx.x + gridDim.x));  // computed, computed next
-  Tile src = now;  // loaded
+  auto tile_at = [&](int id) { return big_tile_at(id, n_mt, n_nt, group_m, (int)M, (int)N); };
+  TileAt now = tile_at((int)blockIdx.x), then = tile_at((int)(blockIdx.x + gridDim.x));  // computed, computed next
+  TileAt src = now;  // loaded
   int l_k = 0;     // and its stage that is loaded next
   auto load_stage = [&](uint8_t* dst) {
     const int m0 = __builtin_amdgcn_readfirstlane(src.m0), n0 = __builtin_amdgcn_readfirstlane(src.n0);
     const int k = __builtin_amdgcn_readfirstlane(l_k);
     const uint8_t* a_tile = A + (int64_t)m0 * a_row;
     const uint8_t* w_tile = W + (int64_t)n0 * w_row;
-    const uint32_t a_bytes = (uint32_t)min((int)M - m0, T) * a_row, w_bytes = (uint32_t)min((int)N - n0, T) * w_row;
-    const uint32_t ka = min((uint32_t)k * AB, a_row - AB), kw = min((uint32_t)k * WB, w_row - WB);
+    const StageSpan a = stage_span<AB>(m0, (int)M, a_row, k), w = stage_span<WB>(n0, (int)N, w_row, k);
 #pragma unroll
-    for (int j = 0; j < AI; ++j) load_lds16(a_tile, a_bytes, dst + (wave * AI + j) * 1024, va[j], ka);
+    for (int j = 0; j < AI; ++j) load_lds16(a_tile, a.bytes, dst + (wave * AI + j) * 1024, va[j], a.k_off);
 #pragma unroll
-    for (int j = 0; j < WI; ++j) load_lds16(w_tile, w_bytes, dst + oW + (wave * WI + j) * 1024, vw[j], kw);
-    load_lds4(sc + k * rows + (wave < 4 ? m0 + 64 * wave : m_pad + n0 + 64 * (wave - 4)), a_bytes > 0 ? 256 : 0,
+    for (int j = 0; j < WI; ++j) load_lds16(w_tile, w.bytes, dst + oW + (wave * WI + j) * 1024, vw[j], w.k_off);
+    load_lds4(sc + k * rows + (wave < 4 ? m0 + 64 * wave : m_pad + n0 + 64 * (wave - 4)), a.bytes > 0 ? 256 : 0,
               dst + oS + 256 * wave, 4u * (uint32_t)lane);
     const bool wrap = k + 1 == nk;  // without a branch, which would part the stage's products
     l_k = wrap ? 0 : k + 1;
