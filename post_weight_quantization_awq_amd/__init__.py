@@ -612,14 +612,19 @@ _X16 = (torch.float16, torch.bfloat16)
 _FLOATS = {torch.float16: AWQ_F16, torch.bfloat16: AWQ_BF16, torch.float32: AWQ_F32}
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream   # handle of a device's current stream, without a Stream object
+
+
 class _MxPrepared(_Prepared):
-    """A prepared call on the device of `like`: its current stream unless one is given, and that
-    device made current around the launch when it is not.  The arguments are kept as C values for
-    a function without argument types, which spares their conversion in every run."""
+    """A prepared call on the device of `like`, made current around the launch when it is not: on the stream
+    given, or else on the one that is current in every run, so that a plan built anywhere can be run under
+    another stream or captured.  The arguments are kept as C values for a function without argument types,
+    which spares their conversion in every run."""
 
     def _place(self, like: torch.Tensor, stream) -> int:
-        self._device = like.device
+        self._device, self._index = like.device, like.device.index
         self._alone = torch.cuda.device_count() == 1
+        self._follow = stream is None
         if stream is None:
             return torch.cuda.current_stream(like.device).cuda_stream
         if stream.device != like.device:
@@ -632,14 +637,31 @@ class _MxPrepared(_Prepared):
             raise TypeError(f"{self._fn} takes {len(types)} arguments, got {len(args)}")
         self._f = lib()[self._fn]
         self._f.restype = ctypes.c_int32
-        self._args = tuple(t(a) for t, a in zip(types, args))
+        self._bound = args[-1], tuple(t(a) for t, a in zip(types, args))     # the stream, which comes last, and all
+        self._used = {args[-1]}
+
+    def _follow_to(self, stream: int):
+        """The current stream is another one than in the last run.  Memory that the plan allocated goes back to
+        its pool only when that stream is done with it, too."""
+        if stream not in self._used:
+            self._used.add(stream)
+            s = torch.cuda.current_stream(self._device)
+            for t in self._mine:
+                t.record_stream(s)
+        self._bound = stream, (*self._bound[1][:-1], ctypes.c_void_p(stream))
+        return self._bound
 
     def launch(self) -> None:
-        if self._alone or torch.cuda.current_device() == self._device.index:
-            st = self._f(*self._args)
+        at, args = self._bound
+        if self._follow:
+            stream = _raw_stream(self._index)
+            if stream != at:
+                at, args = self._follow_to(stream)
+        if self._alone or torch.cuda.current_device() == self._index:
+            st = self._f(*args)
         else:
             with torch.cuda.device(self._device):
-                st = self._f(*self._args)
+                st = self._f(*args)
         if st != AWQ_OK:
             _check(st)
 
@@ -709,6 +731,7 @@ class MxQuantPlan(_MxPrepared):
         _mx_out(out, rows, cols, fmt, X)
         _dev(X, "X")
         self.out = _mx_empty(out, rows, cols, fmt, X.device, stream)
+        self._mine = self.out if out is None else ()
         self._keep = (X, s)
         self._bind(_ptr(X), _FLOATS[X.dtype], rows, cols, ld, _ptr(s), _mx_fmt(fmt), _ptr(self.out[0]),
                    _ptr(self.out[1]), self._place(X, stream))
@@ -740,6 +763,7 @@ class MxDequantPlan(_MxPrepared):
         with _mx_alloc(stream):
             self.out = torch.empty((rows, cols), dtype=out_dtype, device=codes.device) if out is None else out
         ld = self.out.stride(0) if rows > 1 else max(self.out.stride(0), cols)
+        self._mine = (self.out,) if out is None else ()
         self._keep = (codes, scales, s)
         self._bind(_ptr(codes), _ptr(scales), _MX_FMT[fmt], rows, cols, _ptr(s), _ptr(self.out),
                    _FLOATS[self.out.dtype], ld, self._place(codes, stream))
@@ -772,11 +796,15 @@ class RmsNormMxPlan(_MxPrepared):
         ld_ro = _mx_rows(residual_out, "residual_out", X.dtype, (rows, cols), like=X, optional=True)
         _mx_out(out, rows, cols, fmt, X)
         _dev(X, "X")
+        self._mine = ()
         if residual is not None and residual_out is None:
             with _mx_alloc(stream):
                 residual_out = torch.empty((rows, cols), dtype=X.dtype, device=X.device)
             ld_ro = cols
+            self._mine = (residual_out,)
         self.out = (*_mx_empty(out, rows, cols, fmt, X.device, stream), residual_out)
+        if out is None:
+            self._mine += self.out[:2]
         self._keep = (X, weight, residual)
         self._bind(_ptr(X), _FLOATS[X.dtype], rows, cols, ld_x, _ptr(residual), ld_r, _ptr(weight),
                    _FLOATS[weight.dtype], eps, _ptr(residual_out), ld_ro, _mx_fmt(fmt), _ptr(self.out[0]),
@@ -805,6 +833,7 @@ class SiluMulMxPlan(_MxPrepared):
         _mx_out(out, rows, cols, fmt, gate)
         _dev(gate, "gate")
         self.out = _mx_empty(out, rows, cols, fmt, gate.device, stream)
+        self._mine = self.out if out is None else ()
         self._keep = (gate, up)
         self._bind(_ptr(gate), ld_g, _ptr(up), ld_u, _FLOATS[gate.dtype], rows, cols, _mx_fmt(fmt),
                    _ptr(self.out[0]), _ptr(self.out[1]), self._place(gate, stream))
@@ -849,6 +878,7 @@ class MxMatmulPlan(_MxPrepared):
         with _mx_alloc(stream):
             self.ws = workspace(need, a_codes.device) if (ws is None or ws.numel() < need) else ws
             self.out = torch.empty((M, N), dtype=out_dtype, device=a_codes.device) if out is None else out
+        self._mine = (() if self.ws is ws else (self.ws,)) + (() if out is not None else (self.out,))
         ld = self.out.stride(0) if M > 1 else max(self.out.stride(0), N)
         self._keep = (a_codes, a_scales, w_codes, w_scales)
         self._bind(_ptr(a_codes), _ptr(a_scales), _MX_FMT[fmt], M, _ptr(w_codes), _ptr(w_scales), N, K,
