@@ -166,6 +166,15 @@ __global__ __launch_bounds__(kEwThreads) void silu_mul_mx_kernel(const uint16_t*
   }
 }
 
+// a b, to be converted to output type OT.  The compiler makes one instruction of a product and its conversion to
+// fp16, a b + 0, which loses the sign of a negative zero: there the product stays an operation of its own.
+template <int OT>
+__device__ __forceinline__ float product_for(float a, float b) {
+  float p = a * b;
+  if constexpr (OT == 0) asm("" : "+v"(p));
+  return p;
+}
+
 // ---------------------------------------------------------------------------
 // dequant: out = RN(RN32(code 2^e / s[col])), s optional.  code 2^e is exact in
 // fp32 (unless it overflows); the quotient is rounded to fp32 and then to a
@@ -225,7 +234,7 @@ __global__ __launch_bounds__(kEwThreads) void mx_dequant_kernel(const uint8_t* _
       float v[8];
       decode8<FMT>(c[u], v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= unit;
+      for (int j = 0; j < 8; ++j) v[j] = product_for<OT>(v[j], unit);
       store_values8<OT>(out, p.at(ld), v);
     }
     p.next();
