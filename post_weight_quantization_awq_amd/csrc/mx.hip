@@ -7,6 +7,7 @@
 // 4 neighbouring lanes and its maximum two lane permutations away.
 #include "awq_launch.h"
 #include "mx_device.h"
+#include "mx_quotient.h"
 
 namespace awq {
 
@@ -241,11 +242,9 @@ __global__ __launch_bounds__(kEwThreads) void mx_dequant_kernel(const uint8_t* _
   }
 }
 
-// Divided by the columns' scale.  With y = RN(1 / s), taken once for the lane's
-// rows: q0 = RN(v y), then q0 + RN(v - s q0) y rounded is the IEEE quotient
-// (checked on the host for every mantissa of s and all 8 mantissas of the
-// elements), where nothing leaves the normal range: |s| and 2^e within 2^+-60
-// and 2^+-40.  Elsewhere the division itself.
+// Divided by the columns' scale: mx_quotient (mx_quotient.h) with the reciprocal
+// taken once for the lane's rows, where nothing leaves the normal range: |s| and
+// 2^e within 2^+-60 and 2^+-40.  Elsewhere the division itself.
 __device__ __forceinline__ bool mid_range(float x, uint32_t by) {
   const uint32_t e = __builtin_bit_cast(uint32_t, x) >> 23 & 255;
   return e - (127 - by) <= 2 * by;
@@ -290,10 +289,7 @@ __global__ __launch_bounds__(kEwThreads) void mx_dequant_scaled_kernel(const uin
       for (int j = 0; j < 8; ++j) v[j] *= unit;
       if (usual && mid_range(unit, 40)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float q = v[j] * y[j];
-          v[j] = __builtin_fmaf(__builtin_fmaf(-sv[j], q, v[j]), y[j], q);
-        }
+        for (int j = 0; j < 8; ++j) v[j] = mx_quotient(v[j], sv[j], y[j]);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = v[j] / sv[j];

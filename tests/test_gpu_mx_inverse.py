@@ -38,3 +38,27 @@ def test_dequant_bit_patterns(A, fmt, rows, cols):
     for odt in ("f32", "f16", "bf16"):
         got = A.mx_dequant(*dev_mx(codes, blocks, fmt), out_dtype=tdt(odt))
         assert torch.equal(bits(got), bits(torch.from_numpy(v).to(tdt(odt)))), odt
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("scales", ["usual", "negative", "far"])
+@pytest.mark.parametrize("rows,cols", [(40, 96), (5, 32), (130, 544)])
+def test_scaled_dequant_bit_patterns(A, fmt, scales, rows, cols):
+    """The IEEE quotient: usual scales and block exponents, scales of both signs, and far ones."""
+    import torch
+    say(f"mx_dequant scaled bits {fmt} {scales} {rows}x{cols}")
+    rng = np.random.default_rng(rows + cols)
+    codes = signed_zeros(rng, rows, cols, fmt)
+    blocks = rng.integers(*((0, 256) if scales == "far" else (100, 150)), (rows, cols // 32)).astype(np.uint8)
+    s = np.exp(rng.standard_normal(cols))
+    if scales == "negative":
+        s *= np.where(rng.random(cols) < 0.5, -1, 1)
+    if scales == "far":
+        s *= np.exp2(rng.uniform(-120, 120, cols))
+    s = s.astype(np.float32)
+    with np.errstate(over="ignore"):
+        v = O.mx_values(codes, blocks, fmt).astype(np.float32) / s
+    assert np.signbit(v[v == 0]).any() and not np.signbit(v[v == 0]).all()
+    for odt in ("f32", "f16", "bf16"):
+        got = A.mx_dequant(*dev_mx(codes, blocks, fmt), s=torch.from_numpy(s).cuda(), out_dtype=tdt(odt))
+        assert torch.equal(bits(got), bits(torch.from_numpy(v).to(tdt(odt)))), odt
