@@ -476,7 +476,8 @@ awq_status awq_rms_norm_mx(const void* X, int32_t x_dtype, int64_t rows, int64_t
 
 /* ---------------------------------------------------------------------------
  * awq_silu_mul_mx -- the gated activation between the gate/up and the down
- * linear, quantized: v = gate / (1 + exp(-gate)) * up, in fp32.
+ * linear, quantized: v = gate / (1 + exp(-gate)) * up, within 16 units of 2^-24 of
+ * it and within fp32's range, also where exp(-gate) or gate / (1 + exp(-gate)) is not.
  * gate, up: fp16 or bf16 (x_dtype) [rows, ld_g] and [rows, ld_u]; they may be
  * the two halves of one gate/up result.
  * ------------------------------------------------------------------------- */

@@ -121,17 +121,28 @@ __global__ __launch_bounds__(kEwThreads) void mx_quantize_scaled_kernel(const ui
 
 // g / (1 + e^-g) to a few units of the last place, in 8 operations besides the
 // exponential and the reciprocal: e^-g = 2^t (1 + r ln 2) with t = RN(-g log2 e)
-// and r the rest of the product.  Where 1 + e^-g passes 2^126 (g < -87.3) the
-// result is 0: the exact one is below 1.2e-36.  Gates past 128 (t would overflow
-// for the largest bf16 ones) count as 128 in the exponential, which is 0 there.
+// and r the rest of the product.  For g >= -87 only: below, the reciprocal of
+// 1 + e^-g leaves the normal range.  Gates past 128 (t would overflow for the
+// largest bf16 ones) count as 128 in the exponential, which is 0 there.
+constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.92596298909109e-8f, kLn2 = 0.693147182464599609375f;
 template <int DT>
 __device__ __forceinline__ float silu(float g) {
-  const float kHi = 1.44269502162933349609375f, kLo = 1.92596298909109e-8f, kLn2 = 0.693147182464599609375f;
   const float x = DT == 0 ? -g : __builtin_fmaxf(-g, -128.0f);
-  const float t = x * kHi;
-  const float r = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -t));
+  const float t = x * kLog2eHi;
+  const float r = __builtin_fmaf(x, kLog2eLo, __builtin_fmaf(x, kLog2eHi, -t));
   const float d = __builtin_fmaf(__builtin_amdgcn_exp2f(t), __builtin_fmaf(r, kLn2, 1.0f), 1.0f);
   return g * __builtin_amdgcn_rcpf(d);
+}
+
+constexpr uint32_t kFarGate = 0xC2AE0000u;  // the pattern of -87; those of lesser values are larger
+// g e^g up, which is g / (1 + e^-g) up to 2^-125 of it for g < -87.  e^g is taken as four equal factors, multiplied
+// up so that nothing on the way passes the range, and what vanishes on the way vanishes in the result.
+__device__ __forceinline__ float far_silu_mul(float g, float up) {
+  const float x = __builtin_fmaxf(g, -1024.0f);
+  const float t = x * kLog2eHi;
+  const float r = __builtin_fmaf(x, kLog2eLo, __builtin_fmaf(x, kLog2eHi, -t));
+  const float q = __builtin_amdgcn_exp2f(0.25f * t);
+  return g * q * up * q * q * (q * __builtin_fmaf(r, kLn2, 1.0f));
 }
 
 template <int DT, int FMT>
@@ -158,8 +169,19 @@ __global__ __launch_bounds__(kEwThreads) void silu_mul_mx_kernel(const uint16_t*
       float v[8], b[8];
       unpack8<DT>(g[u], v);
       unpack8<DT>(w[u], b);
+      float gate_j[8];
+      uint32_t far = 0;  // largest pattern: the least gate, if any is negative
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = silu<DT>(v[j]) * b[j];
+      for (int j = 0; j < 8; ++j) {
+        gate_j[j] = v[j];
+        far = max(far, __builtin_bit_cast(uint32_t, v[j]));
+        v[j] = silu<DT>(v[j]) * b[j];
+      }
+      if (far > kFarGate) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (__builtin_bit_cast(uint32_t, gate_j[j]) > kFarGate) v[j] = far_silu_mul(gate_j[j], b[j]);
+      }
       uint32_t codes[2];
       const uint32_t byte = mx_quantize8<FMT>(v, codes);
       mx_store8<FMT>(codes, byte, out, scales, chunk);
