@@ -466,7 +466,8 @@ awq_status awq_mx_dequant(const void* codes, const uint8_t* scales, int32_t fmt,
  * residual_out are both given or both NULL; residual_out may be residual or X
  * itself (same row stride), else the buffers do not overlap.  norm: [cols] of
  * norm_dtype (fp16, bf16 or fp32).  eps >= 0 (with 0 a row of zeros is 0 / 0,
- * NaN).  cols <= 65536 (AWQ_ESHAPE).
+ * NaN).  Rows whose squares pass fp32's range, or vanish in it, are normed in the
+ * middle of the range: v is as exact as for other rows.  cols <= 65536 (AWQ_ESHAPE).
  * A row's result depends on that row alone, not on how many there are.
  * ------------------------------------------------------------------------- */
 awq_status awq_rms_norm_mx(const void* X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld_x,

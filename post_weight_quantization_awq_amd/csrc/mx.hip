@@ -362,7 +362,32 @@ __device__ __forceinline__ void load_weight8(const void* w, int dt, int64_t col,
   }
 }
 
-// GL = 0: the block holds one row (blockDim.x lanes); else GL lanes of a wave do
+// A row's lanes: with GL = 0 the block (blockDim.x of them), else GL lanes of a wave.  Their values, none of
+// them below 0, joined by `f`; the same result in each of them.
+template <int GL, class F>
+__device__ __forceinline__ float row_total(float v, float* part, F f) {
+  if constexpr (GL != 0) {
+#pragma unroll
+    for (int m = GL / 2; m >= 1; m >>= 1) v = f(v, __shfl_xor(v, m, kWave));
+    return v;
+  } else {
+#pragma unroll
+    for (int m = kWave / 2; m >= 1; m >>= 1) v = f(v, __shfl_xor(v, m, kWave));
+    const int wave = (int)threadIdx.x >> 6, nw = (int)blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) part[wave] = v;
+    __syncthreads();
+    v = 0.0f;
+    for (int i = 0; i < nw; ++i) v = f(v, part[i]);
+    return v;
+  }
+}
+
+// Rows whose squares leave fp32's range: the mean is infinite, or so small that squares lost below the range count
+// (those are off by at most 2^-150 each, 2^-134 for the longest row, 2^-34 of the least sum or eps taken).  They are
+// brought to the middle of the range first, by the power of two of their largest value or, where that is less,
+// of eps's root.  Rows that hold an infinity or a NaN stay as they are: 1 / sqrt(inf) = 0 times an infinity is NaN.
+constexpr float kNormLeast = 0x1p-100f;
+
 template <int DT, int FMT, int GL, int CH>
 __global__ __launch_bounds__(GL ? 256 : 1024) void rms_norm_mx_kernel(const NormArgs a) {
   const int lanes = GL ? GL : (int)blockDim.x;
@@ -389,19 +414,39 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void rms_norm_mx_kernel(const Norm
       for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(h[c][j], h[c][j], sum);
     }
   }
-  if constexpr (GL != 0) {
+  __shared__ float part[GL ? 1 : 16];
+  sum = row_total<GL>(sum, part, [](float x, float y) { return x + y; });
+  float mean = sum / (float)a.cols + a.eps;
+  // the same for the whole row
+  if (__builtin_expect(!(mean < HUGE_VALF) || (sum < kNormLeast && a.eps < kNormLeast), false)) {
+    uint32_t top = 0;
+    if constexpr (GL == 0) __syncthreads();  // the sum has been read
 #pragma unroll
-    for (int m = GL / 2; m >= 1; m >>= 1) sum += __shfl_xor(sum, m, kWave);
-  } else {
-    __shared__ float part[16];
-    sum = wave_sum(sum);
-    const int wave = (int)threadIdx.x >> 6, nw = (int)blockDim.x >> 6;
-    if ((threadIdx.x & 63) == 0) part[wave] = sum;
-    __syncthreads();
-    sum = 0.0f;
-    for (int i = 0; i < nw; ++i) sum += part[i];
+    for (int c = 0; c < CH; ++c)
+      if (live && lane + c * lanes < cpr)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, __builtin_bit_cast(uint32_t, h[c][j]) & 0x7FFFFFFFu);
+    top = __builtin_bit_cast(uint32_t, row_total<GL>(__builtin_bit_cast(float, top), part, [](float x, float y) {
+      return __builtin_bit_cast(float, max(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)));
+    }));
+    if (top < 0x7F800000u) {
+      int k2 = (int)(top >> 23) - 127;
+      if (a.eps > 0.0f) k2 = max(k2, ((int)(__builtin_bit_cast(uint32_t, a.eps) >> 23) - 127) / 2);
+      sum = 0.0f;
+      if constexpr (GL == 0) __syncthreads();
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if (live && lane + c * lanes < cpr)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            h[c][j] = __builtin_ldexpf(h[c][j], -k2);
+            sum = __builtin_fmaf(h[c][j], h[c][j], sum);
+          }
+      sum = row_total<GL>(sum, part, [](float x, float y) { return x + y; });
+      mean = sum / (float)a.cols + __builtin_ldexpf(a.eps, -2 * k2);
+    }
   }
-  const float r = 1.0f / sqrtf(sum / (float)a.cols + a.eps);
+  const float r = 1.0f / sqrtf(mean);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int k = lane + c * lanes;
