@@ -12,12 +12,9 @@
 #pragma once
 
 #include "awq_device.h"
+#include "mx_format.h"
 
 namespace awq {
-
-constexpr int kMxBlock = 32;
-constexpr int kMxFp8 = 0, kMxFp4 = 1;  // element formats (AWQ_MX_FP8, AWQ_MX_FP4)
-constexpr uint32_t kMxNan = 255;
 
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2v __attribute__((ext_vector_type(2)));

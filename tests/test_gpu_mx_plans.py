@@ -11,9 +11,9 @@ from tests.test_gpu_mx import A, dev_mx, random_mx, to_dev, values  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 
-def plans(A, T, D=416, N=1024):
-    """A prepared call of each operator (the product with K ranges, so that it has a workspace and two launches) on
-    X, and a function that computes the same by functional calls."""
+def plans(A, T, D=4640, N=520):
+    """A prepared call of each operator on X (200 rows: the product in K ranges, with a workspace and two launches),
+    and a function that computes the same by functional calls."""
     import torch
     rng = np.random.default_rng(T)
     X = torch.zeros((T, D), dtype=torch.bfloat16, device="cuda")
@@ -47,6 +47,7 @@ def test_plans_built_before_the_capture(A, T):
     import torch
     say(f"mx plans captured T {T}")
     X, p, eager = plans(A, T)
+    assert T < 200 or A.mx_matmul_workspace_bytes("fp8", T, 520, 4640) > 0
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
