@@ -1,7 +1,5 @@
 """Prepared calls of the microscaled operators: on the stream that is current when they
 run, in captured graphs, and on a stream of their own."""
-import gc
-
 import numpy as np
 import pytest
 
@@ -83,27 +81,28 @@ def test_plans_run_on_the_current_stream(A):
     assert same(outs, eager())
 
 
-def test_plan_keeps_its_memory_for_the_stream_that_used_it(A):
+@pytest.mark.parametrize("which", ["ws", "out"])
+def test_plan_keeps_its_memory_for_the_stream_that_used_it(A, which):
     """A plan dropped while another stream still runs it: its memory is not handed out before that stream is done."""
     import torch
-    say("mx plan dropped while its stream runs")
+    say(f"mx plan dropped while its stream runs, {which}")
     rng = np.random.default_rng(3)
     a, w = dev_mx(*random_mx(rng, 200, 4096, "fp8"), "fp8"), dev_mx(*random_mx(rng, 520, 4096, "fp4"), "fp4")
-    torch.cuda.synchronize()
     plan = A.MxMatmulPlan(*a, *w)
     assert plan.ws.numel() > 256
-    held = [(t.data_ptr(), t.numel() * t.element_size()) for t in (plan.ws, plan.out)]
+    plan.run()
+    t = getattr(plan, which)
+    at, n = t.data_ptr(), t.numel() * t.element_size()
+    del t
     s = torch.cuda.Stream()
+    torch.cuda.synchronize()
     with torch.cuda.stream(s):
-        torch.cuda._sleep(200_000_000)
+        torch.cuda._sleep(400_000_000)
         plan.run()
     del plan
-    gc.collect()
-    for _, n in held:
-        q = torch.empty(n, dtype=torch.uint8, device="cuda")
-        busy = not s.query()
-        assert busy, "the wait was too short"
-        assert all(q.data_ptr() + n <= at or at + m <= q.data_ptr() for at, m in held)
+    assert not s.query(), "the wait was too short"
+    q = torch.empty(n, dtype=torch.uint8, device="cuda").data_ptr()
+    assert q + n <= at or at + n <= q
     s.synchronize()
 
 
