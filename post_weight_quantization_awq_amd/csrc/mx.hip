@@ -18,7 +18,7 @@ namespace awq {
 // the arithmetic, nontemporal.  Measured: quantize 16384 x 4096 35.8 us, 5.7 TB/s
 // (40.4 with ordinary loads, 37.3 at two chunks); gating 8192 x 12288 91 us,
 // 5.6 TB/s (96 at four chunks, 121 with expf and a division: 34 VALU operations
-// a value then bound it, 21 now).
+// a value then bound it, 22 now).
 // ---------------------------------------------------------------------------
 constexpr int kEwThreads = 256, kEwUnroll = 4, kGateUnroll = 2;
 
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(kEwThreads) void mx_quantize_kernel(const uint16_t*
 // the scale is loaded (and, in the inverse, its reciprocal taken) once for them.
 // A block is 2^tx chunks of columns (as many as a row has, rounded up to a power of
 // two, from 4 to 64) by 256 / 2^tx x kColRows rows.  Measured at 4096 x 12288 to 4
-// bits: 25.7 us, the inverse 23.9 us, 5 TB/s; on 48 million values (us, 16 / 64
+// bits: 26.0 us, the inverse 24.3 us, 5 TB/s; on 48 million values (us, 16 / 64
 // chunks a block, quantized): 128 columns 23.5 / 48, 480 columns 32.6 / 24.1, 4096
 // columns 28.4 / 24.0.
 constexpr int kColRows = 4;
@@ -326,7 +326,7 @@ __global__ __launch_bounds__(kEwThreads) void mx_dequant_scaled_kernel(const uin
 // y = h / sqrt(mean h^2 + eps) * weight -> codes, scales.  The mean is taken
 // over the unrounded fp32 h.  A row stays in registers between its sum of
 // squares and its scaling, so the inputs are read once: 6001 x 4096 fp16 with a
-// residual takes 30.4 us, 5.7 TB/s.  Lanes of a row: the GL lanes of a wave that
+// residual takes 30.6 us, 5.7 TB/s.  Lanes of a row: the GL lanes of a wave that
 // its chunks of 8 need (several rows a wave) up to 256 columns, 32 lanes with two
 // chunks each up to 512, else a whole block with one exchange of wave sums through
 // LDS.  Measured on 24 million values in bf16 with a residual, us: 128 columns 30

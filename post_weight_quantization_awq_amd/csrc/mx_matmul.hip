@@ -74,9 +74,12 @@ __device__ __forceinline__ void load_lds4(const void* base, uint32_t bytes, uint
 
 // ---------------------------------------------------------------------------
 // Few tokens, bound by reading the weights: a block holds 16 NT outputs and AR
-// tokens.  Its 8 waves take chunks of ST MFMA steps of 128 K in turn, the next
-// chunk's loads on their way while one is multiplied, and their sums are added in
-// wave order through LDS.  The matrix cores want 16 lanes side by side in 16 rows;
+// tokens.  Its 8 waves take chunks of ST MFMA steps of 128 K in turn, and their
+// sums are added in wave order through LDS.  A wave issues the next chunk's loads
+// ahead of the products of the one at hand.  They are on their way meanwhile for
+// every second chunk only: the loads of a row's ragged end stand under branches,
+// where the compiler loses count of what is in flight, so in the first half of the
+// loop it waits for all of it.  The matrix cores want 16 lanes side by side in 16 rows;
 // loaded like that, every lane is an access of its own (measured at one token,
 // 24576 x 4096: 14.3 us).  So the weights, used once, are read 64 bytes of a row by
 // 4 lanes and turned by lane permutations (12.5 us), and the activations go through

@@ -116,7 +116,10 @@ inline double tile_time(int a_fmt, int tile, double blocks, int stages) {
 inline MxTiling mx_tiling(int a_fmt, int64_t M, int64_t N, int64_t K) {
   const int nk = (int)((K + kMxStage - 1) / kMxStage);
   MxTiling best = {0, nk, 1};
-  if (K < 3 * kMxStage) return best;  // a tile's scales are taken three stages at a time
+  // A tile's scales are taken three stages at a time, so shorter rows go to the few-token kernel however many tokens
+  // there are.  A row is one or two chunks then, for one or two of a block's 8 waves: 4096 x 4096 x 256 takes 131 us
+  // in 8 bits and 121 in 4, 4096 x 4096 x 384 on the tiles 16 and 13.
+  if (K < 3 * kMxStage) return best;
   double least = M <= 64 ? few_time(a_fmt, M, N, K) : HUGE_VAL;
   for (int tile = 64; tile <= 256; tile *= 2) {
     const double blocks = (double)((M + tile - 1) / tile) * (double)((N + tile - 1) / tile);
