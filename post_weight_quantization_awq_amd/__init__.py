@@ -605,7 +605,9 @@ def norm_group_fold(s_members: Sequence[torch.Tensor], norm: Optional[torch.Tens
 # ---------------------------------------------------------------------------
 # Microscaled (MX) operators.  codes: float8_e4m3fn [rows, cols] ("fp8") or uint8
 # [rows, cols / 2] with two 4-bit codes a byte ("fp4"); scales: float8_e8m0fnu
-# [rows, cols / 32].  The plans run on the device that holds their tensors.
+# [rows, cols / 32].  The plans run on the device that holds their tensors, and
+# on the stream that is current in each run unless one is given.  A captured graph
+# works on its plan's buffers: the plan stays as long as the graph.
 # ---------------------------------------------------------------------------
 _MX_FMT = {"fp8": AWQ_MX_FP8, "fp4": AWQ_MX_FP4}
 _X16 = (torch.float16, torch.bfloat16)
