@@ -515,6 +515,113 @@ awq_status awq_mx_matmul(const void* a_codes, const uint8_t* a_scales, int32_t a
                          void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * awq_mx_linear -- awq_mx_matmul with bias, activation and residual in its epilogue:
+ *
+ *   v = act(sum + bias[n]) + residual[m, n]     in fp32, the sum as in awq_mx_matmul
+ *
+ * rounded once to y_dtype (fp16, bf16, or fp32 with a_fmt = AWQ_MX_FP4), or, where
+ * y_fmt is AWQ_MX_FP8 or AWQ_MX_FP4, quantized to codes and scales [M, N] (N % 32 ==
+ * 0), the operand of the next product.  y_fmt = -1: Y [M, ld_y] is written, else
+ * codes and scales are; the other pointers are ignored.
+ * act: AWQ_ACT_NONE; AWQ_ACT_RELU, max(x, 0); AWQ_ACT_SILU, x / (1 + exp(-x));
+ * AWQ_ACT_GELU, x (1 + erf(x / sqrt 2)) / 2; AWQ_ACT_GELU_TANH, x (1 + tanh(sqrt(2 / pi)
+ * (x + 0.044715 x^3))) / 2.  Each is within 2^-18 of its value (GELU 2^-16, GELU_TANH 2^-15)
+ * down to fp32's smallest normal number, for any argument; NaN stays NaN.
+ * bias: [N] of bias_dtype (fp16, bf16 or fp32), or NULL.  residual: [M, ld_r] of
+ * r_dtype (fp16, bf16 or fp32), ld_r >= N, or NULL; it may be Y itself (same dtype and
+ * row stride), else the buffers do not overlap.  Operands, sizes, alignment,
+ * workspace and errors as awq_mx_matmul; K = 0 is AWQ_ESHAPE.
+ * ------------------------------------------------------------------------- */
+#define AWQ_ACT_NONE 0
+#define AWQ_ACT_RELU 1
+#define AWQ_ACT_SILU 2
+#define AWQ_ACT_GELU 3
+#define AWQ_ACT_GELU_TANH 4
+awq_status awq_mx_linear_workspace(int32_t a_fmt, int64_t M, int64_t N, int64_t K, size_t* bytes /* [host] */);
+awq_status awq_mx_linear(const void* a_codes, const uint8_t* a_scales, int32_t a_fmt, int64_t M, const void* w_codes,
+                         const uint8_t* w_scales, int64_t N, int64_t K, const void* bias, int32_t bias_dtype,
+                         int32_t act, const void* residual, int32_t r_dtype, int64_t ld_r, void* Y, int64_t ld_y,
+                         int32_t y_dtype, int32_t y_fmt, void* codes, uint8_t* scales, void* ws, size_t ws_bytes,
+                         hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * awq_moe_route -- the experts of each token, and the (token, expert) pairs in
+ * expert order, as awq_mx_matmul_grouped and awq_block_norm_mx take them.
+ *   experts[t, j]  the expert with the j-th largest logit (equal ones: the lower
+ *                  index first; NaN counts as the largest, -inf is never taken),
+ *                  -1 where no more are left
+ *   weights[t, j]  scale * exp(l[t, j] - max l[t]) / sum, in fp32, 0 where experts is
+ *                  -1; the sum is over the token's chosen experts (renormalize != 0)
+ *                  or over all n_experts
+ *   offsets[e]     pairs of the experts before e; offsets[n_experts]: all pairs
+ *   rows[p]        token of the p-th pair, in the order of the experts and, among an
+ *                  expert's, of the tokens; -1 behind the last pair
+ *   places[t, j]   the pair's p, -1 where experts is -1
+ * So a token whose logits are all -inf (a padded one) takes no place.  Weights of a
+ * token with a NaN or +inf logit are NaN.
+ * logits: fp16, bf16 or fp32 [T, ld], ld >= n_experts, aligned to its elements.
+ * experts, places: int32 [T, top]; weights: fp32 [T, top]; rows: int32 [T top]; offsets:
+ * int32 [n_experts + 1].  1 <= top <= min(n_experts, 32), n_experts <= 1024, T <= 2^24,
+ * T top < 2^31 (AWQ_ESHAPE).  T = 0 writes offsets alone (zeros).  ws:
+ * awq_moe_route_workspace bytes (0 up to 64 tokens; ws may then be NULL), 256-byte
+ * aligned, for this call alone while it runs.  Deterministic.
+ * ------------------------------------------------------------------------- */
+awq_status awq_moe_route_workspace(int64_t T, int32_t n_experts, size_t* bytes /* [host] */);
+awq_status awq_moe_route(const void* logits, int32_t dtype, int64_t T, int32_t n_experts, int64_t ld, int32_t top,
+                         int32_t renormalize, float scale, int32_t* experts, float* weights, int32_t* rows,
+                         int32_t* places, int32_t* offsets, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * awq_mx_matmul_grouped -- awq_mx_matmul with a matrix for each group of rows:
+ *
+ *   Y[m] = a[rows ? rows[m] : m] W[e]^T,   offsets[e] <= m < offsets[e + 1]
+ *
+ * a_codes [a_rows, K] of a_fmt; w_codes [n_groups, N, K] of AWQ_MX_FP4, contiguous, with
+ * w_scales [n_groups, N, K / 32].  offsets: int32 [n_groups + 1] on the device, not
+ * descending, as awq_moe_route writes them; it is read when the call runs, so a
+ * captured graph takes what stands there in each replay.  M: rows that Y has room for;
+ * rows of Y outside [offsets[0], offsets[n_groups]) are left as they were.  rows: int32 [M],
+ * or NULL, when a_rows must be M.  Offsets outside [0, M] count as the nearest of them;
+ * a row number outside [0, a_rows) stands for a row of zeros.  Where offsets descend, rows
+ * that two groups name hold the result of either.
+ * The weights of groups without rows are not read.  Y, its types, the sums and their
+ * accuracy as awq_mx_matmul.  1 <= n_groups <= 1024, M <= 2^26, N <= 2^20, M N <= 2^37, K <=
+ * 2^22, K % 32 == 0, a_rows <= 2^26, and with rows the codes of A below 2^31 bytes (AWQ_ESHAPE).
+ * M = 0 or N = 0 returns AWQ_OK at once.  ws: awq_mx_matmul_grouped_workspace bytes (possibly
+ * 0), 256-byte aligned, for this call alone while it runs.  Deterministic.
+ * ------------------------------------------------------------------------- */
+awq_status awq_mx_matmul_grouped_workspace(int32_t a_fmt, int64_t M, int64_t N, int64_t K, int32_t n_groups,
+                                           size_t* bytes /* [host] */);
+awq_status awq_mx_matmul_grouped(const void* a_codes, const uint8_t* a_scales, int32_t a_fmt, int64_t a_rows,
+                                 const int32_t* rows, int64_t M, const void* w_codes, const uint8_t* w_scales,
+                                 int32_t n_groups, int64_t N, int64_t K, const int32_t* offsets, void* Y, int64_t ld_y,
+                                 int32_t y_dtype, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * awq_block_norm_mx -- between two blocks: the norm after the first with its gate,
+ * the residual's addition, and the norm before the second, quantized.
+ *   y = X[t], or with places: sum_j shares[t, j] X[places[t, j]], in order of j, fp32
+ *   z = y / sqrt(mean_col y^2 + eps) * post         (y where post is NULL)
+ *   h = residual_scale * residual + gate * z        (z where gate is NULL)
+ *   residual_out = RN(h)                            in x_dtype
+ *   v = h / sqrt(mean_col h^2 + eps) * norm         fp32 -> codes, scales
+ * all of it in fp32, unrounded between the steps.  places, shares [rows, top]: both or
+ * neither, as awq_moe_route writes them (top <= 32; places outside [0, x_rows) add nothing).
+ * X: fp16 or bf16 (x_dtype) [x_rows, ld_x]; without places x_rows must be rows.
+ * residual, residual_out: [rows, ld_*] of x_dtype; residual_out may be residual or, without
+ * places, X itself (same row stride), else the buffers do not overlap.  post, norm: [cols];
+ * gate: [cols] with ld_g = 0, or [rows, ld_g]; each fp16, bf16 or fp32.  eps, rows whose
+ * squares leave fp32's range, and the limit of 65536 cols as in awq_rms_norm_mx.  A row's result
+ * depends on that row alone, not on how many there are.
+ * ------------------------------------------------------------------------- */
+awq_status awq_block_norm_mx(const void* X, int32_t x_dtype, int64_t x_rows, int64_t ld_x, const int32_t* places,
+                             const float* shares, int32_t top, int64_t rows, int64_t cols, const void* post,
+                             int32_t post_dtype, const void* gate, int32_t gate_dtype, int64_t ld_g,
+                             const void* residual, int64_t ld_r, float residual_scale, const void* norm,
+                             int32_t norm_dtype, float eps, void* residual_out, int64_t ld_ro, int32_t fmt, void* codes,
+                             uint8_t* scales, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * awq_set_timing_events -- benchmark hook.  While set, every later call on
  * this host thread records `before` and `after` (hipEvent_t handles passed as
  * void*, created by the caller) on the call's stream immediately around its

@@ -648,3 +648,72 @@ def silu_mul(gate: np.ndarray, up: np.ndarray) -> np.ndarray:
     g = gate.astype(np.float64)
     with np.errstate(over="ignore"):
         return g / (1.0 + np.exp(-g)) * up.astype(np.float64)
+
+
+# ---------------------------------------------------------------------------
+# A block with experts, and the linears and norms around it (fp64)
+# ---------------------------------------------------------------------------
+def activation(v: np.ndarray, name) -> np.ndarray:
+    """fp64 activation: None, "relu", "silu", "gelu" (erf) or "gelu_tanh"."""
+    from scipy.special import log_ndtr
+    with np.errstate(over="ignore", invalid="ignore"):
+        if name is None:
+            return v
+        if name == "relu":
+            return np.where(v < 0, 0.0, v)
+        if name == "silu":
+            return v / (1.0 + np.exp(-v))
+        if name == "gelu":
+            return v * np.exp(log_ndtr(v))
+        assert name == "gelu_tanh"
+        return v / (1.0 + np.exp(-2.0 * np.sqrt(2.0 / np.pi) * (v + 0.044715 * v ** 3)))
+
+
+def moe_route(logits: np.ndarray, top: int, renormalize: bool = True, scale: float = 1.0):
+    """(experts, weights fp64, rows, places, offsets) of logits [T, E]: one token and one expert at a time."""
+    T, E = logits.shape
+    experts = np.full((T, top), -1, np.int64)
+    weights = np.zeros((T, top))
+    for t in range(T):
+        l = logits[t].astype(np.float64)
+        # NaN first, then descending; equal logits by index; -inf not at all
+        order = sorted((e for e in range(E) if l[e] != -np.inf), key=lambda e: (not np.isnan(l[e]),
+                                                                                0.0 if np.isnan(l[e]) else -l[e], e))
+        got = order[:top]
+        experts[t, :len(got)] = got
+        if got:
+            with np.errstate(invalid="ignore"):
+                most = l[got[0]]
+                p = np.exp(l - most)
+                total = p[got].sum() if renormalize else p[[e for e in range(E) if l[e] != -np.inf]].sum()
+                weights[t, :len(got)] = p[got] / total * scale
+    rows = np.full(T * top, -1, np.int64)
+    places = np.full((T, top), -1, np.int64)
+    offsets = np.zeros(E + 1, np.int64)
+    at = 0
+    for e in range(E):
+        offsets[e] = at
+        for t, j in np.argwhere(experts == e):
+            rows[at], places[t, j] = t, at
+            at += 1
+    offsets[E] = at
+    return experts, weights, rows, places, offsets
+
+
+def block_norm(x, residual, norm, eps, post=None, gate=None, residual_scale=1.0, places=None, shares=None):
+    """(h, v) in fp64: y = x or sum_j shares[:, j] x[places[:, j]] (places outside x add nothing), z = y / rms(y) *
+    post, h = residual_scale residual + gate z, v = h / rms(h) * norm."""
+    x = x.astype(np.float64)
+    y = x
+    if places is not None:
+        y = np.zeros((places.shape[0], x.shape[1]))
+        for t in range(places.shape[0]):
+            for p, s in zip(places[t], shares[t]):
+                if 0 <= p < x.shape[0]:
+                    y[t] += float(s) * x[p]
+    if post is not None:
+        y = rms_norm(y, post, eps)[1]
+    if gate is not None:
+        y = gate.astype(np.float64) * y
+    h = residual_scale * residual.astype(np.float64) + y
+    return h, rms_norm(h, norm, eps)[1]

@@ -20,6 +20,10 @@ Entry points (same names as the C ABI):
 * ``rms_norm_mx``         RMS norm with the residual's addition, microscaled result
 * ``silu_mul_mx``         SiLU gating, microscaled result
 * ``mx_matmul``           product of microscaled activations with 4-bit microscaled weights
+* ``mx_linear``           the same with bias, activation and residual in its epilogue, also with a microscaled result
+* ``moe_route``           each token's experts and shares, and the (token, expert) pairs in expert order
+* ``mx_matmul_grouped``   products grouped by expert with ragged sizes
+* ``block_norm_mx``       the experts' sum, the norm after a block, gate, residual, and the norm before the next one
 """
 from __future__ import annotations
 
@@ -27,7 +31,7 @@ import contextlib
 import ctypes
 import dataclasses
 import os
-from typing import List, Optional, Sequence
+from typing import List, NamedTuple, Optional, Sequence
 
 import torch
 
@@ -52,7 +56,8 @@ EXPORTED = ("awq_act_stats_workspace", "awq_act_stats", "awq_candidate_scales_wo
             "awq_weight_channel_mean", "awq_candidate_scales_duo_workspace", "awq_candidate_scales_duo",
             "awq_w4a16_workspace", "awq_w4a16_matmul", "awq_search_scales_noalloc",
             "awq_mx_quantize", "awq_mx_dequant", "awq_rms_norm_mx", "awq_silu_mul_mx", "awq_mx_matmul_workspace",
-            "awq_mx_matmul",
+            "awq_mx_matmul", "awq_mx_linear_workspace", "awq_mx_linear", "awq_moe_route_workspace", "awq_moe_route",
+            "awq_mx_matmul_grouped_workspace", "awq_mx_matmul_grouped", "awq_block_norm_mx",
             "awq_last_error", "awq_abi_version", "awq_set_timing_events")
 
 
@@ -106,6 +111,14 @@ def _load() -> ctypes.CDLL:
         "awq_silu_mul_mx": [P, I64, P, I64, I32, I64, I64, I32, P, P, P],
         "awq_mx_matmul_workspace": [I32, I64, I64, I64, PSZ],
         "awq_mx_matmul": [P, P, I32, I64, P, P, I64, I64, P, I64, I32, P, SZ, P],
+        "awq_mx_linear_workspace": [I32, I64, I64, I64, PSZ],
+        "awq_mx_linear": [P, P, I32, I64, P, P, I64, I64, P, I32, I32, P, I32, I64, P, I64, I32, I32, P, P, P, SZ, P],
+        "awq_moe_route_workspace": [I64, I32, PSZ],
+        "awq_moe_route": [P, I32, I64, I32, I64, I32, I32, F32, P, P, P, P, P, P, SZ, P],
+        "awq_mx_matmul_grouped_workspace": [I32, I64, I64, I64, I32, PSZ],
+        "awq_mx_matmul_grouped": [P, P, I32, I64, P, I64, P, P, I32, I64, I64, P, P, I64, I32, P, SZ, P],
+        "awq_block_norm_mx": [P, I32, I64, I64, P, P, I32, I64, I64, P, I32, P, I32, I64, P, I64, F32, P, I32, F32,
+                              P, I64, I32, P, P, P],
         "awq_set_timing_events": [P, P],
         "awq_search_scales_noalloc": [ctypes.POINTER(SearchCfg), ctypes.POINTER(WGroup), I64, P, P, P, P, P],
     }
@@ -899,6 +912,254 @@ def mx_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tens
     return MxMatmulPlan(a_codes, a_scales, w_codes, w_scales, out_dtype, out, stream=stream).run()
 
 
+# ---------------------------------------------------------------------------
+# A block with experts, and the linears and norms around it
+# ---------------------------------------------------------------------------
+_ACT = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def mx_linear_workspace_bytes(fmt: str, M: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().awq_mx_linear_workspace(_mx_fmt(fmt), M, N, K, ctypes.byref(n)))
+    return n.value
+
+
+class MxLinearPlan(_MxPrepared):
+    """act(A W^T + bias) + residual from quantized operands (as MxMatmulPlan takes them), rounded once to out_dtype,
+    or with fmt quantized to (codes, scales)."""
+    _fn = "awq_mx_linear"
+
+    def __init__(self, a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                 bias: Optional[torch.Tensor] = None, activation: Optional[str] = None,
+                 residual: Optional[torch.Tensor] = None, out_dtype=torch.float16, fmt: Optional[str] = None, out=None,
+                 ws: Optional[torch.Tensor] = None, stream=None):
+        a_fmt, M, K = _mx_operand(a_codes, a_scales, "a_")
+        w_fmt, N, Kw = _mx_operand(w_codes, w_scales, "w_", like=a_codes)
+        if w_fmt != "fp4":
+            raise ValueError("w_codes must hold 4-bit codes (uint8)")
+        if Kw != K:
+            raise ValueError(f"a_codes have {K} columns, w_codes {Kw}")
+        if activation not in _ACT:
+            raise ValueError(f"activation {activation!r} not in {list(_ACT)}")
+        _tensor(bias, "bias", tuple(_FLOATS), (N,), like=a_codes, optional=True)
+        ld_r = _mx_rows(residual, "residual", tuple(_FLOATS), (M, N), like=a_codes, optional=True)
+        if fmt is not None:
+            _mx_out(out, M, N, fmt, a_codes)
+        elif out is not None:
+            _mx_rows(out, "out", tuple(_FLOATS), (M, N), like=a_codes)
+            out_dtype = out.dtype
+        if out_dtype not in _FLOATS:
+            raise ValueError(f"out_dtype must be one of {list(_FLOATS)}, got {out_dtype}")
+        _tensor(ws, "ws", torch.uint8, (None,), like=a_codes, optional=True)
+        _dev(a_codes, "a_codes")
+        need = mx_linear_workspace_bytes(a_fmt, M, N, K)
+        y = codes = scales = None
+        ld = N
+        with _mx_alloc(stream):
+            self.ws = workspace(need, a_codes.device) if (ws is None or ws.numel() < need) else ws
+            if fmt is not None:
+                self.out = codes, scales = _mx_empty(out, M, N, fmt, a_codes.device, stream)
+            else:
+                self.out = y = torch.empty((M, N), dtype=out_dtype, device=a_codes.device) if out is None else out
+                ld = y.stride(0) if M > 1 else max(y.stride(0), N)
+        self._mine = (() if self.ws is ws else (self.ws,))
+        if out is None:
+            self._mine += (y,) if fmt is None else (codes, scales)
+        self._keep = (a_codes, a_scales, w_codes, w_scales, bias, residual)
+        self._bind(_ptr(a_codes), _ptr(a_scales), _MX_FMT[a_fmt], M, _ptr(w_codes), _ptr(w_scales), N, K, _ptr(bias),
+                   0 if bias is None else _FLOATS[bias.dtype], _ACT[activation], _ptr(residual),
+                   0 if residual is None else _FLOATS[residual.dtype], ld_r, _ptr(y), ld, _FLOATS[out_dtype],
+                   -1 if fmt is None else _mx_fmt(fmt), _ptr(codes), _ptr(scales), _ptr(self.ws), self.ws.numel(),
+                   self._place(a_codes, stream))
+
+    def run(self):
+        self.launch()
+        return self.out
+
+
+def mx_linear(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+              bias: Optional[torch.Tensor] = None, activation: Optional[str] = None,
+              residual: Optional[torch.Tensor] = None, out_dtype=torch.float16, fmt: Optional[str] = None, out=None,
+              stream=None):
+    """act(A W^T + bias) + residual of quantized A and W: activation None, "relu", "silu", "gelu" or "gelu_tanh"; bias
+    [N]; residual [M, N] (which may be `out`).  Rounded once to out_dtype, or with fmt "fp8" / "fp4" returned
+    as (codes, scales), the operand of the next product."""
+    return MxLinearPlan(a_codes, a_scales, w_codes, w_scales, bias, activation, residual, out_dtype, fmt, out,
+                        stream=stream).run()
+
+
+class MoeRouting(NamedTuple):
+    experts: torch.Tensor   # int32 [T, top]: descending by logit, -1 where none is left
+    weights: torch.Tensor   # fp32 [T, top]
+    rows: torch.Tensor      # int32 [T * top]: the token of each place, -1 behind the last
+    places: torch.Tensor    # int32 [T, top]: the place of each pair, -1 where experts is -1
+    offsets: torch.Tensor   # int32 [n_experts + 1]: each expert's first place
+
+
+class MoeRoutePlan(_MxPrepared):
+    """The `top` experts of each token by its logits [T, n_experts] and their shares, and the (token, expert) pairs
+    in expert order."""
+    _fn = "awq_moe_route"
+
+    def __init__(self, logits: torch.Tensor, top: int, renormalize: bool = True, scale: float = 1.0,
+                 out: Optional[MoeRouting] = None, ws: Optional[torch.Tensor] = None, stream=None):
+        ld = _mx_rows(logits, "logits", tuple(_FLOATS))
+        T, n = logits.shape
+        shapes = {"experts": (T, top), "weights": (T, top), "rows": (T * top,), "places": (T, top), "offsets": (n + 1,)}
+        types = {k: torch.float32 if k == "weights" else torch.int32 for k in shapes}
+        if not 1 <= top <= min(n, 32):
+            raise ValueError(f"top must be in [1, min({n}, 32)], got {top}")
+        if out is not None:
+            for k, shape in shapes.items():
+                _tensor(getattr(out, k), k, types[k], shape, like=logits)
+        _tensor(ws, "ws", torch.uint8, (None,), like=logits, optional=True)
+        _dev(logits, "logits")
+        need = ctypes.c_size_t()
+        _check(lib().awq_moe_route_workspace(T, n, ctypes.byref(need)))
+        need = need.value
+        with _mx_alloc(stream):
+            self.ws = workspace(need, logits.device) if (ws is None or ws.numel() < need) else ws
+            self.out = MoeRouting(**{k: torch.empty(shape, dtype=types[k], device=logits.device)
+                                     for k, shape in shapes.items()}) if out is None else MoeRouting(*out)
+        self._mine = (() if self.ws is ws else (self.ws,)) + (() if out is not None else tuple(self.out))
+        self._keep = (logits,)
+        self._bind(_ptr(logits), _FLOATS[logits.dtype], T, n, ld, top, int(renormalize), scale,
+                   *(_ptr(t) for t in self.out), _ptr(self.ws), self.ws.numel(), self._place(logits, stream))
+
+    def run(self) -> MoeRouting:
+        self.launch()
+        return self.out
+
+
+def moe_route(logits: torch.Tensor, top: int, renormalize: bool = True, scale: float = 1.0,
+              out: Optional[MoeRouting] = None, stream=None) -> MoeRouting:
+    """(experts, weights, rows, places, offsets) of logits [T, n_experts]: each token's `top` largest (ties to the
+    lower index, -inf never), the shares exp(l - max) / sum (over the chosen, or over all without renormalize)
+    times scale, and the pairs in expert order for mx_matmul_grouped and block_norm_mx."""
+    return MoeRoutePlan(logits, top, renormalize, scale, out, stream=stream).run()
+
+
+def mx_matmul_grouped_workspace_bytes(fmt: str, M: int, N: int, K: int, n_groups: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().awq_mx_matmul_grouped_workspace(_mx_fmt(fmt), M, N, K, n_groups, ctypes.byref(n)))
+    return n.value
+
+
+class MxMatmulGroupedPlan(_MxPrepared):
+    """Y [M, N]: rows [offsets[e], offsets[e + 1]) are A's rows (or those that `rows` names) times W[e]^T.  offsets
+    and rows are read in each run."""
+    _fn = "awq_mx_matmul_grouped"
+
+    def __init__(self, a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                 offsets: torch.Tensor, rows: Optional[torch.Tensor] = None, out_dtype=torch.float16,
+                 out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
+        fmt, a_rows, K = _mx_operand(a_codes, a_scales, "a_")
+        _tensor(w_codes, "w_codes", torch.uint8, (None, None, K // 2), like=a_codes)
+        n_groups, N = w_codes.shape[:2]
+        _tensor(w_scales, "w_scales", torch.float8_e8m0fnu, (n_groups, N, K // 32), like=a_codes)
+        _tensor(offsets, "offsets", torch.int32, (n_groups + 1,), like=a_codes)
+        _tensor(rows, "rows", torch.int32, (None,), like=a_codes, optional=True)
+        M = a_rows if rows is None else rows.shape[0]
+        if out is not None:
+            _mx_rows(out, "out", tuple(_FLOATS), (M, N), like=a_codes)
+            out_dtype = out.dtype
+        if out_dtype not in _FLOATS:
+            raise ValueError(f"out_dtype must be one of {list(_FLOATS)}, got {out_dtype}")
+        _tensor(ws, "ws", torch.uint8, (None,), like=a_codes, optional=True)
+        _dev(a_codes, "a_codes")
+        need = mx_matmul_grouped_workspace_bytes(fmt, M, N, K, n_groups)
+        with _mx_alloc(stream):
+            self.ws = workspace(need, a_codes.device) if (ws is None or ws.numel() < need) else ws
+            self.out = torch.empty((M, N), dtype=out_dtype, device=a_codes.device) if out is None else out
+        self._mine = (() if self.ws is ws else (self.ws,)) + (() if out is not None else (self.out,))
+        ld = self.out.stride(0) if M > 1 else max(self.out.stride(0), N)
+        self._keep = (a_codes, a_scales, w_codes, w_scales, offsets, rows)
+        self._bind(_ptr(a_codes), _ptr(a_scales), _MX_FMT[fmt], a_rows, _ptr(rows), M, _ptr(w_codes), _ptr(w_scales),
+                   n_groups, N, K, _ptr(offsets), _ptr(self.out), ld, _FLOATS[self.out.dtype], _ptr(self.ws),
+                   self.ws.numel(), self._place(a_codes, stream))
+
+    def run(self) -> torch.Tensor:
+        self.launch()
+        return self.out
+
+
+def mx_matmul_grouped(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                      offsets: torch.Tensor, rows: Optional[torch.Tensor] = None, out_dtype=torch.float16,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y[m] = A[rows[m]] W[e]^T (A[m] without rows) for offsets[e] <= m < offsets[e + 1]: quantized A [*, K], W
+    [n_groups, N, K] (mx_quantize of each matrix, stacked), offsets and rows as of moe_route.  Rows of `out` outside
+    the groups are left as they were."""
+    return MxMatmulGroupedPlan(a_codes, a_scales, w_codes, w_scales, offsets, rows, out_dtype, out,
+                               stream=stream).run()
+
+
+class BlockNormMxPlan(_MxPrepared):
+    """y = X, or the sum of its rows places[t] weighted by shares[t]; h = residual_scale residual + gate norm(y) (the
+    norm with post_weight, if given); codes, scales of h / sqrt(mean h^2 + eps) * weight; residual_out = h in X's
+    dtype, which may be residual, or X itself without places."""
+    _fn = "awq_block_norm_mx"
+
+    def __init__(self, X: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                 post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                 residual_scale: float = 1.0, places: Optional[torch.Tensor] = None,
+                 shares: Optional[torch.Tensor] = None, fmt: str = "fp8",
+                 residual_out: Optional[torch.Tensor] = None, out=None, stream=None):
+        ld_x = _mx_rows(X, "X")
+        ld_r = _mx_rows(residual, "residual", X.dtype, (None, X.shape[1]), like=X)
+        rows, cols = residual.shape
+        if (places is None) != (shares is None):
+            raise ValueError("places and shares go together")
+        if places is None:
+            _mx_rows(X, "X", X.dtype, (rows, cols))
+        else:
+            _tensor(places, "places", torch.int32, (rows, None), like=X)
+            _tensor(shares, "shares", torch.float32, tuple(places.shape), like=X)
+        _tensor(weight, "weight", tuple(_FLOATS), (cols,), like=X)
+        _tensor(post_weight, "post_weight", tuple(_FLOATS), (cols,), like=X, optional=True)
+        ld_g = 0
+        if gate is not None and gate.dim() == 2 and not (rows > 0 and gate.stride(0) == 0 and gate.shape[0] == rows):
+            ld_g = _mx_rows(gate, "gate", tuple(_FLOATS), (rows, cols), like=X)
+        elif gate is not None and gate.dim() == 2:
+            _tensor(gate[0], "gate", tuple(_FLOATS), (cols,), like=X)
+        else:
+            _tensor(gate, "gate", tuple(_FLOATS), (cols,), like=X, optional=True)
+        ld_ro = _mx_rows(residual_out, "residual_out", X.dtype, (rows, cols), like=X, optional=True)
+        _mx_out(out, rows, cols, fmt, X)
+        _dev(X, "X")
+        self._mine = ()
+        if residual_out is None:
+            with _mx_alloc(stream):
+                residual_out = torch.empty((rows, cols), dtype=X.dtype, device=X.device)
+            ld_ro = cols
+            self._mine = (residual_out,)
+        self.out = (*_mx_empty(out, rows, cols, fmt, X.device, stream), residual_out)
+        if out is None:
+            self._mine += self.out[:2]
+        self._keep = (X, residual, weight, post_weight, gate, places, shares)
+        dt = lambda t: 0 if t is None else _FLOATS[t.dtype]  # noqa: E731
+        self._bind(_ptr(X), _FLOATS[X.dtype], X.shape[0], ld_x, _ptr(places), _ptr(shares),
+                   0 if places is None else places.shape[1], rows, cols, _ptr(post_weight), dt(post_weight), _ptr(gate),
+                   dt(gate), ld_g, _ptr(residual), ld_r, residual_scale, _ptr(weight), dt(weight), eps,
+                   _ptr(residual_out), ld_ro, _mx_fmt(fmt), _ptr(self.out[0]), _ptr(self.out[1]),
+                   self._place(X, stream))
+
+    def run(self):
+        self.launch()
+        return self.out
+
+
+def block_norm_mx(X: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                  post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  residual_scale: float = 1.0, places: Optional[torch.Tensor] = None,
+                  shares: Optional[torch.Tensor] = None, fmt: str = "fp8", residual_out: Optional[torch.Tensor] = None,
+                  out=None, stream=None):
+    """Returns (codes, scales, residual_out): h = residual_scale * residual + gate * norm(y), with y = X or the sum of
+    its rows places[t] weighted by shares[t] (places and weights of moe_route), the norm by post_weight (none
+    without), gate [cols] or [rows, cols]; the RMS norm of h by weight, quantized; and h in X's dtype."""
+    return BlockNormMxPlan(X, residual, weight, eps, post_weight, gate, residual_scale, places, shares, fmt,
+                           residual_out, out, stream).run()
+
+
 def set_timing_events(before: Optional[int], after: Optional[int]) -> None:
     """Record raw hipEvent_t handles around the main kernel of every later call (None clears)."""
     _check(lib().awq_set_timing_events(before, after))
@@ -908,4 +1169,7 @@ __all__ = ["set_timing_events", "ActStatsPlan", "SearchPlan", "search_scales_noa
            "weight_channel_mean", "candidate_scales_duo", "W4A16Plan", "w4a16_matmul", "AwqError", "act_stats", "candidate_scales", "search_scales", "quantize_pack", "unpack_dequant",
            "search_workspace_bytes", "act_stats_workspace_bytes", "SearchResult", "lib", "LIB_PATH",
            "MxQuantPlan", "mx_quantize", "MxDequantPlan", "mx_dequant", "RmsNormMxPlan", "rms_norm_mx",
-           "SiluMulMxPlan", "silu_mul_mx", "MxMatmulPlan", "mx_matmul", "mx_matmul_workspace_bytes"]
+           "SiluMulMxPlan", "silu_mul_mx", "MxMatmulPlan", "mx_matmul", "mx_matmul_workspace_bytes",
+           "MxLinearPlan", "mx_linear", "mx_linear_workspace_bytes", "MoeRouting", "MoeRoutePlan", "moe_route",
+           "MxMatmulGroupedPlan", "mx_matmul_grouped", "mx_matmul_grouped_workspace_bytes", "BlockNormMxPlan",
+           "block_norm_mx"]

@@ -887,4 +887,189 @@ awq_status awq_mx_matmul(const void* a_codes, const uint8_t* a_scales, int32_t a
   return hip_status(e, "awq_mx_matmul");
 }
 
+// ---------------------------------------------------------------------------
+static awq_status workspace_fits(const void* ws, size_t ws_bytes, size_t need) {
+  if (need == 0) return AWQ_OK;
+  if (!ws || ws_bytes < need) return fail(AWQ_EWORKSPACE, "workspace %zu bytes < %zu", ws_bytes, need);
+  if ((uintptr_t)ws & 255u) return fail(AWQ_EALIGN, "ws not 256-byte aligned");
+  return AWQ_OK;
+}
+
+awq_status awq_mx_linear_workspace(int32_t a_fmt, int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  if (!bytes) return fail(AWQ_EINVAL, "bytes is NULL");
+  if (awq_status st = mx_matmul_shape(a_fmt, M, N, K)) return st;
+  *bytes = (M == 0 || N == 0 || K == 0) ? 0 : align256(mx_linear_workspace(a_fmt, M, N, K));
+  return ok();
+}
+
+awq_status awq_mx_linear(const void* a_codes, const uint8_t* a_scales, int32_t a_fmt, int64_t M, const void* w_codes,
+                         const uint8_t* w_scales, int64_t N, int64_t K, const void* bias, int32_t bias_dtype,
+                         int32_t act, const void* residual, int32_t r_dtype, int64_t ld_r, void* Y, int64_t ld_y,
+                         int32_t y_dtype, int32_t y_fmt, void* codes, uint8_t* scales, void* ws, size_t ws_bytes,
+                         hipStream_t stream) {
+  if (awq_status st = mx_matmul_shape(a_fmt, M, N, K)) return st;
+  if (y_fmt != -1 && y_fmt != AWQ_MX_FP8 && y_fmt != AWQ_MX_FP4)
+    return fail(AWQ_EDTYPE, "y_fmt %d: need -1, AWQ_MX_FP8 or AWQ_MX_FP4", y_fmt);
+  if (act < AWQ_ACT_NONE || act > AWQ_ACT_GELU_TANH) return fail(AWQ_EINVAL, "act %d is no AWQ_ACT_*", act);
+  const bool quantized = y_fmt != -1;
+  if (!quantized) {
+    if (!any_float(y_dtype)) return fail(AWQ_EDTYPE, "y_dtype %d: need AWQ_F16, AWQ_BF16 or AWQ_F32", y_dtype);
+    if (y_dtype == AWQ_F32 && a_fmt == AWQ_MX_FP8)
+      return fail(AWQ_EDTYPE, "an fp32 result needs AWQ_MX_FP4 activations: sums of 8-bit products are not fp32-exact");
+  } else if (N % 32) {
+    return fail(AWQ_ESHAPE, "N %lld not a multiple of 32, and the result is quantized", (long long)N);
+  }
+  if (bias && !any_float(bias_dtype)) return fail(AWQ_EDTYPE, "bias_dtype %d: need AWQ_F16, AWQ_BF16 or AWQ_F32", bias_dtype);
+  if (residual && !any_float(r_dtype)) return fail(AWQ_EDTYPE, "r_dtype %d: need AWQ_F16, AWQ_BF16 or AWQ_F32", r_dtype);
+  if (M == 0 || N == 0) return ok();
+  if (K == 0) return fail(AWQ_ESHAPE, "K is 0 with M, N > 0");
+  if (quantized && M >= ((int64_t)1 << 33) / N)
+    return fail(AWQ_ESHAPE, "%lld x %lld: 2^33 quantized values or more", (long long)M, (long long)N);
+  if (!quantized && ld_y < N) return fail(AWQ_ESHAPE, "ld_y %lld < N %lld", (long long)ld_y, (long long)N);
+  if (residual && ld_r < N) return fail(AWQ_ESHAPE, "ld_r %lld < N %lld", (long long)ld_r, (long long)N);
+  if (!a_codes || !a_scales || !w_codes || !w_scales) return fail(AWQ_EINVAL, "a_codes / a_scales / w_codes / w_scales is NULL");
+  if (quantized ? !codes || !scales : !Y) return fail(AWQ_EINVAL, quantized ? "codes / scales is NULL" : "Y is NULL");
+  if (!quantized && residual == Y && (r_dtype != y_dtype || ld_r != ld_y))
+    return fail(AWQ_EINVAL, "residual is Y, of another dtype or row stride");
+  if (!aligned16(a_codes) || !aligned16(w_codes) || (quantized && !aligned16(codes)))
+    return fail(AWQ_EALIGN, "codes not 16-byte aligned");
+  if ((!quantized && misaligned(Y, y_dtype)) || (bias && misaligned(bias, bias_dtype)) ||
+      (residual && misaligned(residual, r_dtype)))
+    return fail(AWQ_EALIGN, "Y / bias / residual misaligned");
+  if (awq_status st = workspace_fits(ws, ws_bytes, align256(mx_linear_workspace(a_fmt, M, N, K)))) return st;
+  mark(true, stream);
+  hipError_t e = launch_mx_linear(a_codes, a_scales, a_fmt, M, w_codes, w_scales, N, K, bias, bias_dtype, act,
+                                  residual, r_dtype, ld_r, Y, ld_y,
+                                  quantized ? (y_fmt == AWQ_MX_FP8 ? 3 : 4) : y_dtype, codes, scales, ws,
+                                  stream);
+  mark(false, stream);
+  return hip_status(e, "awq_mx_linear");
+}
+
+// ---------------------------------------------------------------------------
+constexpr int kMostExperts = 1024, kMostTop = 32;
+
+static awq_status route_shape(int64_t T, int32_t n_experts) {
+  if (T < 0 || n_experts < 0) return fail(AWQ_EINVAL, "negative size");
+  if (n_experts < 1 || n_experts > kMostExperts)
+    return fail(AWQ_ESHAPE, "n_experts %d not in [1, %d]", n_experts, kMostExperts);
+  if (T > (int64_t)1 << 24) return fail(AWQ_ESHAPE, "T %lld > 2^24", (long long)T);
+  return ok();
+}
+
+awq_status awq_moe_route_workspace(int64_t T, int32_t n_experts, size_t* bytes) {
+  if (!bytes) return fail(AWQ_EINVAL, "bytes is NULL");
+  if (awq_status st = route_shape(T, n_experts)) return st;
+  *bytes = align256(moe_route_workspace(T, n_experts));
+  return ok();
+}
+
+awq_status awq_moe_route(const void* logits, int32_t dtype, int64_t T, int32_t n_experts, int64_t ld, int32_t top,
+                         int32_t renormalize, float scale, int32_t* experts, float* weights, int32_t* rows,
+                         int32_t* places, int32_t* offsets, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!any_float(dtype)) return fail(AWQ_EDTYPE, "dtype %d: need AWQ_F16, AWQ_BF16 or AWQ_F32", dtype);
+  if (awq_status st = route_shape(T, n_experts)) return st;
+  if (top < 1 || top > n_experts || top > kMostTop)
+    return fail(AWQ_ESHAPE, "top %d not in [1, min(%d, %d)]", top, n_experts, kMostTop);
+  if (T * top >= (int64_t)1 << 31) return fail(AWQ_ESHAPE, "T top = %lld >= 2^31", (long long)(T * top));
+  if (ld < n_experts) return fail(AWQ_ESHAPE, "ld %lld < n_experts %d", (long long)ld, n_experts);
+  if (!offsets || (T > 0 && (!logits || !experts || !weights || !rows || !places)))
+    return fail(AWQ_EINVAL, "logits / experts / weights / rows / places / offsets is NULL");
+  if (misaligned(logits, dtype) || misaligned(experts, AWQ_F32) || misaligned(weights, AWQ_F32) ||
+      misaligned(rows, AWQ_F32) || misaligned(places, AWQ_F32) || misaligned(offsets, AWQ_F32))
+    return fail(AWQ_EALIGN, "logits / experts / weights / rows / places / offsets misaligned");
+  if (awq_status st = workspace_fits(ws, ws_bytes, align256(moe_route_workspace(T, n_experts)))) return st;
+  mark(true, stream);
+  hipError_t e = launch_moe_route(logits, dtype, T, n_experts, ld, top, renormalize != 0, scale, experts,
+                                  weights, rows, places, offsets, ws, stream);
+  mark(false, stream);
+  return hip_status(e, "awq_moe_route");
+}
+
+static awq_status grouped_shape(int32_t a_fmt, int64_t M, int64_t N, int64_t K, int32_t n_groups) {
+  if (awq_status st = mx_matmul_shape(a_fmt, M, N, K)) return st;
+  if (n_groups < 1 || n_groups > kMostExperts)
+    return fail(AWQ_ESHAPE, "n_groups %d not in [1, %d]", n_groups, kMostExperts);
+  if (N > (int64_t)1 << 20) return fail(AWQ_ESHAPE, "N %lld > 2^20", (long long)N);
+  return ok();
+}
+
+awq_status awq_mx_matmul_grouped_workspace(int32_t a_fmt, int64_t M, int64_t N, int64_t K, int32_t n_groups,
+                                           size_t* bytes) {
+  if (!bytes) return fail(AWQ_EINVAL, "bytes is NULL");
+  if (awq_status st = grouped_shape(a_fmt, M, N, K, n_groups)) return st;
+  *bytes = (M == 0 || N == 0 || K == 0) ? 0 : align256(mx_grouped_workspace(a_fmt, M, N, K, n_groups));
+  return ok();
+}
+
+awq_status awq_mx_matmul_grouped(const void* a_codes, const uint8_t* a_scales, int32_t a_fmt, int64_t a_rows,
+                                 const int32_t* rows, int64_t M, const void* w_codes, const uint8_t* w_scales,
+                                 int32_t n_groups, int64_t N, int64_t K, const int32_t* offsets, void* Y, int64_t ld_y,
+                                 int32_t y_dtype, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (awq_status st = grouped_shape(a_fmt, M, N, K, n_groups)) return st;
+  if (!any_float(y_dtype)) return fail(AWQ_EDTYPE, "y_dtype %d: need AWQ_F16, AWQ_BF16 or AWQ_F32", y_dtype);
+  if (y_dtype == AWQ_F32 && a_fmt == AWQ_MX_FP8)
+    return fail(AWQ_EDTYPE, "an fp32 result needs AWQ_MX_FP4 activations: sums of 8-bit products are not fp32-exact");
+  if (a_rows < 0) return fail(AWQ_EINVAL, "negative size");
+  if (M == 0 || N == 0) return ok();
+  if (K == 0) return fail(AWQ_ESHAPE, "K is 0 with M, N > 0");
+  if (!rows && a_rows != M) return fail(AWQ_ESHAPE, "a_rows %lld is not M %lld, and rows is NULL", (long long)a_rows, (long long)M);
+  if (a_rows < 1 || a_rows > kMxMaxRows) return fail(AWQ_ESHAPE, "a_rows %lld not in [1, 2^26]", (long long)a_rows);
+  if (rows && a_rows * (a_fmt == AWQ_MX_FP8 ? K : K / 2) >= (int64_t)1 << 31)
+    return fail(AWQ_ESHAPE, "a_codes have 2^31 bytes or more, and rows is given");
+  if (ld_y < N) return fail(AWQ_ESHAPE, "ld_y %lld < N %lld", (long long)ld_y, (long long)N);
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !offsets || !Y)
+    return fail(AWQ_EINVAL, "a_codes / a_scales / w_codes / w_scales / offsets / Y is NULL");
+  if (!aligned16(a_codes) || !aligned16(w_codes)) return fail(AWQ_EALIGN, "codes not 16-byte aligned");
+  if (misaligned(Y, y_dtype) || misaligned(rows, AWQ_F32) || misaligned(offsets, AWQ_F32))
+    return fail(AWQ_EALIGN, "Y / rows / offsets misaligned");
+  if (awq_status st = workspace_fits(ws, ws_bytes, align256(mx_grouped_workspace(a_fmt, M, N, K, n_groups)))) return st;
+  mark(true, stream);
+  hipError_t e = launch_mx_matmul_grouped(a_codes, a_scales, a_fmt, a_rows, rows, M, w_codes, w_scales, n_groups, N, K,
+                                          offsets, Y, ld_y, y_dtype, ws, stream);
+  mark(false, stream);
+  return hip_status(e, "awq_mx_matmul_grouped");
+}
+
+awq_status awq_block_norm_mx(const void* X, int32_t x_dtype, int64_t x_rows, int64_t ld_x, const int32_t* places,
+                             const float* shares, int32_t top, int64_t rows, int64_t cols, const void* post,
+                             int32_t post_dtype, const void* gate, int32_t gate_dtype, int64_t ld_g,
+                             const void* residual, int64_t ld_r, float residual_scale, const void* norm,
+                             int32_t norm_dtype, float eps, void* residual_out, int64_t ld_ro, int32_t fmt, void* codes,
+                             uint8_t* scales, hipStream_t stream) {
+  if (!x16(x_dtype)) return fail(AWQ_EDTYPE, "x_dtype %d: need AWQ_F16 or AWQ_BF16", x_dtype);
+  if (!any_float(norm_dtype) || (post && !any_float(post_dtype)) || (gate && !any_float(gate_dtype)))
+    return fail(AWQ_EDTYPE, "norm_dtype, post_dtype or gate_dtype: need AWQ_F16, AWQ_BF16 or AWQ_F32");
+  if (awq_status st = mx_shape(fmt, rows, cols)) return st;
+  if (!(eps >= 0.0f)) return fail(AWQ_EINVAL, "eps %g is negative or NaN", (double)eps);
+  if ((places == nullptr) != (shares == nullptr)) return fail(AWQ_EINVAL, "places and shares go together");
+  if (x_rows < 0 || x_rows > (int64_t)1 << 31) return fail(AWQ_ESHAPE, "x_rows %lld not in [0, 2^31]", (long long)x_rows);
+  if (places && (top < 1 || top > kMostTop)) return fail(AWQ_ESHAPE, "top %d not in [1, %d]", top, kMostTop);
+  if (!places && x_rows != rows)
+    return fail(AWQ_ESHAPE, "x_rows %lld is not rows %lld, and places is NULL", (long long)x_rows, (long long)rows);
+  if (rows == 0 || cols == 0) return ok();
+  if (cols > rms_norm_mx_max_cols())
+    return fail(AWQ_ESHAPE, "cols %lld > %lld", (long long)cols, (long long)rms_norm_mx_max_cols());
+  if (ld_x < cols || ld_r < cols || ld_ro < cols)
+    return fail(AWQ_ESHAPE, "ld_x %lld, ld_r %lld or ld_ro %lld < cols %lld", (long long)ld_x, (long long)ld_r,
+                (long long)ld_ro, (long long)cols);
+  if (gate && ld_g != 0 && ld_g < cols) return fail(AWQ_ESHAPE, "ld_g %lld is not 0 and < cols %lld", (long long)ld_g, (long long)cols);
+  if ((!X && x_rows > 0) || !residual || !norm || !residual_out || !codes || !scales)
+    return fail(AWQ_EINVAL, "X / residual / norm / residual_out / codes / scales is NULL");
+  if (places && residual_out == X) return fail(AWQ_EINVAL, "residual_out is X, whose rows other tokens read");
+  if (misaligned(X, x_dtype) || misaligned(residual, x_dtype) || misaligned(residual_out, x_dtype) ||
+      misaligned(norm, norm_dtype) || (post && misaligned(post, post_dtype)) || (gate && misaligned(gate, gate_dtype)) ||
+      misaligned(places, AWQ_F32) || misaligned(shares, AWQ_F32))
+    return fail(AWQ_EALIGN, "X / residual / residual_out / norm / post / gate / places / shares misaligned");
+  if (!aligned16(codes)) return fail(AWQ_EALIGN, "codes not 16-byte aligned");
+  const BlockNormArgs a = {(const uint16_t*)X, x_rows, ld_x, places, shares, top, post, post_dtype, gate,
+                           gate_dtype, ld_g, (const uint16_t*)residual, ld_r, residual_scale, norm,
+                           norm_dtype, eps, (uint16_t*)residual_out, ld_ro, rows, cols, (uint8_t*)codes,
+                           scales};
+  mark(true, stream);
+  hipError_t e = launch_block_norm_mx(a, x_dtype, fmt, stream);
+  mark(false, stream);
+  return hip_status(e, "awq_block_norm_mx");
+}
+
 }  // extern "C"

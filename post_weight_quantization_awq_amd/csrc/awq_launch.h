@@ -164,4 +164,49 @@ size_t mx_matmul_workspace(int a_fmt, int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx_matmul(const void* A, const uint8_t* as, int a_fmt, int64_t M, const void* W, const uint8_t* ws,
                             int64_t N, int64_t K, void* Y, int64_t ld_y, int y_dtype, void* work, hipStream_t stream);
 
+// bias_dtype, r_dtype: 0 fp16, 1 bf16, 2 fp32; act: kAct* (mx_act.h); out: 0, 1, 2 as y_dtype, 3 / 4 fp8 / fp4 codes
+size_t mx_linear_workspace(int a_fmt, int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx_linear(const void* A, const uint8_t* as, int a_fmt, int64_t M, const void* W, const uint8_t* ws,
+                            int64_t N, int64_t K, const void* bias, int bias_dtype, int act, const void* residual,
+                            int r_dtype, int64_t ld_r, void* Y, int64_t ld_y, int out, void* codes, uint8_t* scales,
+                            void* work, hipStream_t stream);
+
+// a_rows: rows of A; rows: null or M of them
+size_t mx_grouped_workspace(int a_fmt, int64_t M, int64_t N, int64_t K, int n_groups);
+hipError_t launch_mx_matmul_grouped(const void* A, const uint8_t* as, int a_fmt, int64_t a_rows, const int32_t* rows,
+                                    int64_t M, const void* W, const uint8_t* ws, int n_groups, int64_t N, int64_t K,
+                                    const int32_t* offsets, void* Y, int64_t ld_y, int y_dtype, void* work,
+                                    hipStream_t stream);
+
+// dtype: 0 fp16, 1 bf16, 2 fp32
+size_t moe_route_workspace(int64_t rows, int n_experts);
+hipError_t launch_moe_route(const void* logits, int dtype, int64_t rows, int n_experts, int64_t ld, int top,
+                            bool renorm, float scale, int32_t* experts, float* weights, int32_t* rows_out,
+                            int32_t* places, int32_t* offsets, void* ws, hipStream_t stream);
+
+struct BlockNormArgs {
+  const uint16_t* X;
+  int64_t x_rows, ld_x;
+  const int32_t* places;  // may be null
+  const float* shares;
+  int top;
+  const void* post;       // may be null
+  int post_dtype;         // 0 fp16, 1 bf16, 2 fp32
+  const void* gate;       // may be null
+  int gate_dtype;
+  int64_t ld_g;           // 0: one gate for all rows
+  const uint16_t* R;
+  int64_t ld_r;
+  float residual_scale;
+  const void* norm;
+  int norm_dtype;
+  float eps;
+  uint16_t* RO;
+  int64_t ld_ro;
+  int64_t rows, cols;
+  uint8_t* codes;
+  uint8_t* scales;
+};
+hipError_t launch_block_norm_mx(const BlockNormArgs& a, int dt, int fmt, hipStream_t stream);
+
 }  // namespace awq

@@ -6,7 +6,9 @@
 // A lane holds 8 consecutive values (16 bytes of input), so a block of 32 is
 // 4 neighbouring lanes and its maximum two lane permutations away.
 #include "awq_launch.h"
+#include "mx_act.h"
 #include "mx_device.h"
+#include "mx_norm.h"
 #include "mx_quotient.h"
 
 namespace awq {
@@ -117,32 +119,6 @@ __global__ __launch_bounds__(kEwThreads) void mx_quantize_scaled_kernel(const ui
       mx_store8<FMT>(codes, byte, out, scales, (row + p.step * u) * cpr + col);
     }
   }
-}
-
-// g / (1 + e^-g) to a few units of the last place, in 8 operations besides the
-// exponential and the reciprocal: e^-g = 2^t (1 + r ln 2) with t = RN(-g log2 e)
-// and r the rest of the product.  For g >= -87 only: below, the reciprocal of
-// 1 + e^-g leaves the normal range.  Gates past 128 (t would overflow for the
-// largest bf16 ones) count as 128 in the exponential, which is 0 there.
-constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.92596298909109e-8f, kLn2 = 0.693147182464599609375f;
-template <int DT>
-__device__ __forceinline__ float silu(float g) {
-  const float x = DT == 0 ? -g : __builtin_fmaxf(-g, -128.0f);
-  const float t = x * kLog2eHi;
-  const float r = __builtin_fmaf(x, kLog2eLo, __builtin_fmaf(x, kLog2eHi, -t));
-  const float d = __builtin_fmaf(__builtin_amdgcn_exp2f(t), __builtin_fmaf(r, kLn2, 1.0f), 1.0f);
-  return g * __builtin_amdgcn_rcpf(d);
-}
-
-constexpr uint32_t kFarGate = 0xC2AE0000u;  // the pattern of -87; those of lesser values are larger
-// g e^g up, which is g / (1 + e^-g) up to 2^-125 of it for g < -87.  e^g is taken as four equal factors, multiplied
-// up so that nothing on the way passes the range, and what vanishes on the way vanishes in the result.
-__device__ __forceinline__ float far_silu_mul(float g, float up) {
-  const float x = __builtin_fmaxf(g, -1024.0f);
-  const float t = x * kLog2eHi;
-  const float r = __builtin_fmaf(x, kLog2eLo, __builtin_fmaf(x, kLog2eHi, -t));
-  const float q = __builtin_amdgcn_exp2f(0.25f * t);
-  return g * q * up * q * q * (q * __builtin_fmaf(r, kLn2, 1.0f));
 }
 
 template <int DT, int FMT>
@@ -351,43 +327,6 @@ struct NormArgs {
   uint8_t* scales;
 };
 
-__device__ __forceinline__ void load_weight8(const void* w, int dt, int64_t col, float (&f)[8]) {
-  if (dt == 2) {
-    *(float4*)&f[0] = ld_any<float4>((const float*)w + col);
-    *(float4*)&f[4] = ld_any<float4>((const float*)w + col + 4);
-  } else {
-    const uint4 u = ld_any<uint4>((const uint16_t*)w + col);
-    if (dt == 0) unpack8<0>(u, f);
-    else unpack8<1>(u, f);
-  }
-}
-
-// A row's lanes: with GL = 0 the block (blockDim.x of them), else GL lanes of a wave.  Their values, none of
-// them below 0, joined by `f`; the same result in each of them.
-template <int GL, class F>
-__device__ __forceinline__ float row_total(float v, float* part, F f) {
-  if constexpr (GL != 0) {
-#pragma unroll
-    for (int m = GL / 2; m >= 1; m >>= 1) v = f(v, __shfl_xor(v, m, kWave));
-    return v;
-  } else {
-#pragma unroll
-    for (int m = kWave / 2; m >= 1; m >>= 1) v = f(v, __shfl_xor(v, m, kWave));
-    const int wave = (int)threadIdx.x >> 6, nw = (int)blockDim.x >> 6;
-    if ((threadIdx.x & 63) == 0) part[wave] = v;
-    __syncthreads();
-    v = 0.0f;
-    for (int i = 0; i < nw; ++i) v = f(v, part[i]);
-    return v;
-  }
-}
-
-// Rows whose squares leave fp32's range: the mean is infinite, or so small that squares lost below the range count
-// (those are off by at most 2^-150 each, 2^-134 for the longest row, 2^-34 of the least sum or eps taken).  They are
-// brought to the middle of the range first, by the power of two of their largest value or, where that is less,
-// of eps's root.  Rows that hold an infinity or a NaN stay as they are: 1 / sqrt(inf) = 0 times an infinity is NaN.
-constexpr float kNormLeast = 0x1p-100f;
-
 template <int DT, int FMT, int GL, int CH>
 __global__ __launch_bounds__(GL ? 256 : 1024) void rms_norm_mx_kernel(const NormArgs a) {
   const int lanes = GL ? GL : (int)blockDim.x;
@@ -415,38 +354,7 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void rms_norm_mx_kernel(const Norm
     }
   }
   __shared__ float part[GL ? 1 : 16];
-  sum = row_total<GL>(sum, part, [](float x, float y) { return x + y; });
-  float mean = sum / (float)a.cols + a.eps;
-  // the same for the whole row
-  if (__builtin_expect(!(mean < HUGE_VALF) || (sum < kNormLeast && a.eps < kNormLeast), false)) {
-    uint32_t top = 0;
-    if constexpr (GL == 0) __syncthreads();  // the sum has been read
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-      if (live && lane + c * lanes < cpr)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __builtin_bit_cast(uint32_t, h[c][j]) & 0x7FFFFFFFu);
-    top = __builtin_bit_cast(uint32_t, row_total<GL>(__builtin_bit_cast(float, top), part, [](float x, float y) {
-      return __builtin_bit_cast(float, max(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)));
-    }));
-    if (top < 0x7F800000u) {
-      int k2 = (int)(top >> 23) - 127;
-      if (a.eps > 0.0f) k2 = max(k2, ((int)(__builtin_bit_cast(uint32_t, a.eps) >> 23) - 127) / 2);
-      sum = 0.0f;
-      if constexpr (GL == 0) __syncthreads();
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-        if (live && lane + c * lanes < cpr)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            h[c][j] = __builtin_ldexpf(h[c][j], -k2);
-            sum = __builtin_fmaf(h[c][j], h[c][j], sum);
-          }
-      sum = row_total<GL>(sum, part, [](float x, float y) { return x + y; });
-      mean = sum / (float)a.cols + __builtin_ldexpf(a.eps, -2 * k2);
-    }
-  }
-  const float r = 1.0f / sqrtf(mean);
+  const float r = row_scale<GL, CH>(h, sum, live, lane, lanes, cpr, a.cols, a.eps, part);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int k = lane + c * lanes;

@@ -1,0 +1,122 @@
+// Product of microscaled operands grouped by expert: rows [offsets[e],
+// offsets[e + 1]) of Y are rows of A (their own, or those that `rows` names) times
+// matrix e of W.  The kernels are the product's (mx_product.h); a block finds its
+// tile of rows by itself, from the offsets on the device, so that the host waits
+// for nothing and a captured graph takes whatever offsets there are.
+#include <algorithm>
+
+#include "awq_launch.h"
+#include "mx_product.h"
+
+namespace awq {
+
+struct GroupedWork {
+  int n_mt, n_nt;
+  int64_t m_pad, n_pad, rows;        // scale rows: of A, of one group's weight, of all
+  size_t scales, tab, offsets, all;  // bytes up to the tiles' table, the row offsets, the end
+};
+static GroupedWork grouped_work(int a_fmt, int64_t M, int64_t N, int64_t K, int n_groups) {
+  GroupedWork w;
+  w.n_mt = (int)group_tiles_most(M, n_groups, kBigTile);
+  w.n_nt = (int)tiles_of(N, kBigTile);
+  w.m_pad = (int64_t)w.n_mt * kBigTile;
+  w.n_pad = (int64_t)w.n_nt * kBigTile;
+  w.rows = w.m_pad + n_groups * w.n_pad;
+  const int64_t words = a_fmt == kMxFp8 ? (K + kMxStage - 1) / kMxStage : (K + kBigStage - 1) / kBigStage * 2;
+  w.scales = (size_t)(w.rows * words) * 4;
+  w.tab = w.scales;  // a multiple of 1024
+  w.offsets = w.tab + ((size_t)w.n_mt + 1) * sizeof(int4);
+  w.all = w.offsets + (size_t)w.m_pad * 4;
+  return w;
+}
+
+size_t mx_grouped_workspace(int a_fmt, int64_t M, int64_t N, int64_t K, int n_groups) {
+  if (group_tiling(a_fmt, M, N, K, n_groups).tile != kBigTile) return 0;
+  return grouped_work(a_fmt, M, N, K, n_groups).all;
+}
+
+struct GroupedArgs {
+  const uint8_t *A, *as, *W, *ws;
+  int64_t M, N, K;
+  void* Y;
+  int64_t ld_y;
+  Groups g;
+};
+
+template <int AF>
+static void grouped_few(const GroupedArgs& p, const GroupTiling& t, int y_dtype, hipStream_t stream) {
+  const int64_t most = group_tiles_most(p.M, p.g.n, t.few_rows), cols = tiles_of(p.N, 16 * t.few_tiles);
+  // of a launch: the grid's second dimension, and fewer than 2^32 lanes
+  const int64_t step = std::min<int64_t>(65535, std::max<int64_t>(1, ((int64_t)1 << 22) / cols));
+  Groups g = p.g;
+  for (int64_t m = 0; m < most; m += step) {
+    g.first_tile = (int)m;
+    const dim3 grid((unsigned)cols, (unsigned)std::min(step, most - m));
+#define AWQ_FEW(AR, NT, ST, OCC)                                                                               \
+  mx_few_kernel<AF, AR, NT, ST, OCC, Groups><<<grid, kFewWaves * kWave, 0, stream>>>(p.A, p.as, p.M, p.W, p.ws, p.N, \
+                                                                                     p.K, p.Y, p.ld_y, y_dtype, g)
+    if (t.few_rows == 4) AWQ_FEW(4, 1, 4, 4);
+    else if (t.few_rows == 16 && t.few_tiles == 1) AWQ_FEW(16, 1, 2, 4);
+    else if (t.few_rows == 16) AWQ_FEW(16, 2, 2, 4);
+    else AWQ_FEW(32, 2, 2, 2);
+#undef AWQ_FEW
+  }
+}
+
+template <int AF, int YT>
+static void grouped_launch(const GroupedArgs& p, uint8_t* work, hipStream_t stream) {
+  const GroupTiling t = group_tiling(AF, p.M, p.N, p.K, p.g.n);
+  if (t.tile == 0) {
+    grouped_few<AF>(p, t, YT, stream);
+  } else if (t.tile < kBigTile) {
+    const int n_mt = (int)group_tiles_most(p.M, p.g.n, t.tile), n_nt = (int)tiles_of(p.N, t.tile);
+    const int nk = (int)((p.K + kMxStage - 1) / kMxStage);
+#define AWQ_TILE(BM, NS, OCC)                                                                              \
+  mx_tile_kernel<AF, YT, BM, BM, 2, 2, NS, OCC, Groups><<<(unsigned)(n_mt * n_nt), 4 * kWave, 0, stream>>>( \
+      p.A, p.as, p.M, p.W, p.ws, p.N, p.K, n_mt, n_nt, 4, nk, p.Y, p.ld_y, p.g)
+    if (t.tile == 64) AWQ_TILE(64, 3, 4);
+    else AWQ_TILE(128, 3, 2);
+#undef AWQ_TILE
+  } else if constexpr (AF == kMxFp4 || YT != 2) {
+    const GroupedWork w = grouped_work(AF, p.M, p.N, p.K, p.g.n);
+    constexpr int SB = (AF == kMxFp8 ? kMxStage : kBigStage) / kMxBlock;
+    const int kb = (int)(p.K / kMxBlock);
+    uint32_t* sc = (uint32_t*)work;
+    const StagedGroups sg = {(const int4*)(work + w.tab), (const uint32_t*)(work + w.offsets)};
+    stage_groups_kernel<SB><<<dim3((unsigned)(w.rows / 256), (unsigned)((kb + 15) / 16)), 256, 0, stream>>>(
+        p.g, p.as, (int)p.M, (uint32_t)(AF == kMxFp8 ? p.K : p.K / 2), p.ws, p.N, w.n_pad, kb, w.n_mt, w.rows, sc,
+        (int4*)(work + w.tab), (uint32_t*)(work + w.offsets));
+    const int tiles = w.n_mt * w.n_nt;
+    if constexpr (AF == kMxFp8) {
+      const unsigned blocks = (unsigned)std::min(tiles, 256);
+      if (p.g.rows != nullptr)
+        mx_big8_kernel<YT, Groups, true><<<blocks, 512, 0, stream>>>(p.A, p.M, p.W, p.N, p.K, sc, w.m_pad, w.rows, w.n_mt,
+                                                                     w.n_nt, 4, p.Y, p.ld_y, p.g, sg);
+      else
+        mx_big8_kernel<YT, Groups, false><<<blocks, 512, 0, stream>>>(p.A, p.M, p.W, p.N, p.K, sc, w.m_pad, w.rows, w.n_mt,
+                                                                      w.n_nt, 4, p.Y, p.ld_y, p.g, sg);
+    } else {
+      mx_big_kernel<YT, Groups><<<(unsigned)tiles, 512, 0, stream>>>(p.A, p.M, p.W, p.N, p.K, sc, w.m_pad, w.rows, w.n_mt,
+                                                                     w.n_nt, 4, p.Y, p.ld_y, p.g, sg);
+    }
+  }
+}
+
+hipError_t launch_mx_matmul_grouped(const void* A, const uint8_t* as, int a_fmt, int64_t a_rows, const int32_t* rows,
+                                    int64_t M, const void* W, const uint8_t* ws, int n_groups, int64_t N, int64_t K,
+                                    const int32_t* offsets, void* Y, int64_t ld_y, int y_dtype, void* work,
+                                    hipStream_t stream) {
+  const GroupedArgs p = {(const uint8_t*)A, as, (const uint8_t*)W, ws, M, N, K, Y, ld_y,
+                         {offsets, n_groups, rows, a_rows, 0}};
+  if (a_fmt == kMxFp8) {
+    if (y_dtype == 0) grouped_launch<kMxFp8, 0>(p, (uint8_t*)work, stream);
+    else grouped_launch<kMxFp8, 1>(p, (uint8_t*)work, stream);
+  } else {
+    if (y_dtype == 0) grouped_launch<kMxFp4, 0>(p, (uint8_t*)work, stream);
+    else if (y_dtype == 1) grouped_launch<kMxFp4, 1>(p, (uint8_t*)work, stream);
+    else grouped_launch<kMxFp4, 2>(p, (uint8_t*)work, stream);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace awq

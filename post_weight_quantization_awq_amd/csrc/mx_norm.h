@@ -1,0 +1,84 @@
+// The RMS norm of a row that stays in registers.
+#pragma once
+
+#include "mx_device.h"
+
+namespace awq {
+
+__device__ __forceinline__ void load_weight8(const void* w, int dt, int64_t col, float (&f)[8]) {
+  if (dt == 2) {
+    *(float4*)&f[0] = ld_any<float4>((const float*)w + col);
+    *(float4*)&f[4] = ld_any<float4>((const float*)w + col + 4);
+  } else {
+    const uint4 u = ld_any<uint4>((const uint16_t*)w + col);
+    if (dt == 0) unpack8<0>(u, f);
+    else unpack8<1>(u, f);
+  }
+}
+
+// A row's lanes: with GL = 0 the block (blockDim.x of them), else GL lanes of a wave.  Their values, none of
+// them below 0, joined by `f`; the same result in each of them.
+template <int GL, class F>
+__device__ __forceinline__ float row_total(float v, float* part, F f) {
+  if constexpr (GL != 0) {
+#pragma unroll
+    for (int m = GL / 2; m >= 1; m >>= 1) v = f(v, __shfl_xor(v, m, kWave));
+    return v;
+  } else {
+#pragma unroll
+    for (int m = kWave / 2; m >= 1; m >>= 1) v = f(v, __shfl_xor(v, m, kWave));
+    const int wave = (int)threadIdx.x >> 6, nw = (int)blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) part[wave] = v;
+    __syncthreads();
+    v = 0.0f;
+    for (int i = 0; i < nw; ++i) v = f(v, part[i]);
+    return v;
+  }
+}
+
+// Rows whose squares leave fp32's range: the mean is infinite, or so small that squares lost below the range count
+// (those are off by at most 2^-150 each, 2^-134 for the longest row, 2^-34 of the least sum or eps taken).  They are
+// brought to the middle of the range first, by the power of two of their largest value or, where that is less,
+// of eps's root.  Rows that hold an infinity or a NaN stay as they are: 1 / sqrt(inf) = 0 times an infinity is NaN.
+constexpr float kNormLeast = 0x1p-100f;
+
+// 1 / sqrt(mean h^2 + eps) of a row whose lanes hold h and their sums of squares.  Where those leave fp32's range h
+// is scaled, and what is returned goes with the scaled h.  part: 16 floats of LDS with GL = 0.
+template <int GL, int CH>
+__device__ __forceinline__ float row_scale(float (&h)[CH][8], float sum, bool live, int lane, int lanes, int cpr,
+                                           int64_t cols, float eps, float* part) {
+  sum = row_total<GL>(sum, part, [](float x, float y) { return x + y; });
+  float mean = sum / (float)cols + eps;
+  // the same for the whole row
+  if (__builtin_expect(!(mean < HUGE_VALF) || (sum < kNormLeast && eps < kNormLeast), false)) {
+    uint32_t top = 0;
+    if constexpr (GL == 0) __syncthreads();  // the sum has been read
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (live && lane + c * lanes < cpr)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, __builtin_bit_cast(uint32_t, h[c][j]) & 0x7FFFFFFFu);
+    top = __builtin_bit_cast(uint32_t, row_total<GL>(__builtin_bit_cast(float, top), part, [](float x, float y) {
+      return __builtin_bit_cast(float, max(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)));
+    }));
+    if (top < 0x7F800000u) {
+      int k2 = (int)(top >> 23) - 127;
+      if (eps > 0.0f) k2 = max(k2, ((int)(__builtin_bit_cast(uint32_t, eps) >> 23) - 127) / 2);
+      sum = 0.0f;
+      if constexpr (GL == 0) __syncthreads();
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if (live && lane + c * lanes < cpr)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            h[c][j] = __builtin_ldexpf(h[c][j], -k2);
+            sum = __builtin_fmaf(h[c][j], h[c][j], sum);
+          }
+      sum = row_total<GL>(sum, part, [](float x, float y) { return x + y; });
+      mean = sum / (float)cols + __builtin_ldexpf(eps, -2 * k2);
+    }
+  }
+  return 1.0f / sqrtf(mean);
+}
+
+}  // namespace awq

@@ -145,4 +145,41 @@ inline int tile_slots(const MxTiling& t, int64_t M, int64_t N) {
   return t.tile == 64 && tiles_of(M, 64) * tiles_of(N, 64) * t.ranges <= 256 && t.split >= 12 ? 6 : 3;
 }
 
+// ---------------------------------------------------------------------------
+// Products grouped by expert
+// ---------------------------------------------------------------------------
+// Tiles of rows that M rows in n_groups groups can have: one that is not full for every group that has rows
+inline int64_t group_tiles_most(int64_t M, int n_groups, int tile) {
+  const int64_t used = M < n_groups ? M : n_groups;
+  return (M + used * (tile - 1)) / tile;
+}
+
+// The kernel and its tile, for even shares of the rows: the ones with the least estimated time.
+struct GroupTiling {
+  int tile;                  // 64, 128 or 256; 0: few rows a group,
+  int few_rows, few_tiles;   // then the LDS rows and 16-output tiles of a block
+};
+inline GroupTiling group_tiling(int a_fmt, int64_t M, int64_t N, int64_t K, int n_groups) {
+  const double used = (double)(M < n_groups ? M : n_groups), each = (double)M / used;
+  const int rows = each <= 3 ? 4 : each <= 20 ? 16 : 32;
+  const double w_mb = used * (double)N * (double)K * (17.0 / 32) * 1e-6;
+  const double a_mb = (double)M * (double)K * (a_fmt == kMxFp8 ? 1.0 : 0.5) * 1e-6;
+  const double few_mt = used * ceil(each / rows);
+  GroupTiling best = {0, rows, rows == 4 || (N + 15) / 16 * few_mt <= 256 ? 1 : 2};
+  if (rows == 32) best.few_tiles = 2;
+  if (K < 3 * kMxStage) return best;
+  const double a_cost = rows == 4 ? 0.0 : rows == 16 ? 0.02 : a_fmt == kMxFp8 ? 0.05 : 0.035;
+  double least = each <= 64 ? 2 + w_mb / 5 + (ceil(each / rows) - 1) * w_mb / 10 +
+                                  a_cost * (double)N / (16 * best.few_tiles) * a_mb
+                            : HUGE_VAL;
+  const int nk = (int)((K + kMxStage - 1) / kMxStage);
+  for (int tile = 64; tile <= 256; tile *= 2) {
+    const double n_nt = (double)((N + tile - 1) / tile);
+    if ((double)group_tiles_most(M, n_groups, tile) * n_nt > (1 << 22)) continue;  // a launch holds fewer than 2^32 lanes
+    const double t = tile_time(a_fmt, tile, used * ceil(each / tile) * n_nt, nk);
+    if (t < least) least = t, best.tile = tile;
+  }
+  return best;
+}
+
 }  // namespace awq
