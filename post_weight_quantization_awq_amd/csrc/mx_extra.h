@@ -16,7 +16,7 @@ struct NoExtra {
 // quantized.
 // ---------------------------------------------------------------------------
 struct Epilogue {
-  static constexpr bool kGroups = false, kEpi = true;
+  static constexpr bool kGroups = false, kEpi = true, kRes = true;
   const void* bias;  // may be null
   int bias_dtype;    // 0 fp16, 1 bf16, 2 fp32
   int act;           // kAct*
@@ -27,6 +27,9 @@ struct Epilogue {
   uint8_t* codes;
   uint8_t* scales;
 };
+struct EpilogueAlone : Epilogue {  // without a residual
+  static constexpr bool kRes = false;
+};
 constexpr int kOutFp8 = 3, kOutFp4 = 4;
 
 __device__ __forceinline__ float load_float(const void* p, int64_t i, int dt) {
@@ -34,21 +37,44 @@ __device__ __forceinline__ float load_float(const void* p, int64_t i, int dt) {
   const uint32_t v = ((const uint16_t*)p)[i];
   return dt == 0 ? x2f<0>(v) : x2f<1>(v);
 }
-// 8 values from i on, the last `left` of them or all
-__device__ __forceinline__ void load_floats8(const void* p, int64_t i, int dt, int64_t left, float (&f)[8]) {
+// 8 values from i on as they lie in memory, the last `left` of them or all
+struct Raw8 {
+  uint4 lo, hi;  // hi: of 32-bit values
+};
+__device__ __forceinline__ Raw8 load_raw8(const void* p, int64_t i, int dt, int64_t left) {
+  Raw8 r = {};
   if (left >= 8) {
     if (dt == 2) {
-      *(float4*)&f[0] = ld_any<float4>((const float*)p + i);
-      *(float4*)&f[4] = ld_any<float4>((const float*)p + i + 4);
+      r.lo = ld_any<uint4>((const float*)p + i);
+      r.hi = ld_any<uint4>((const float*)p + i + 4);
     } else {
-      const uint4 u = ld_any<uint4>((const uint16_t*)p + i);
-      if (dt == 0) unpack8<0>(u, f);
-      else unpack8<1>(u, f);
+      r.lo = ld_any<uint4>((const uint16_t*)p + i);
     }
   } else {
+    uint32_t w[8] = {};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = j < left ? load_float(p, i + j, dt) : 0.0f;
+    for (int j = 0; j < 8; ++j)
+      if (j < left) {
+        if (dt == 2) w[j] = ((const uint32_t*)p)[i + j];
+        else w[j / 2] |= (uint32_t)((const uint16_t*)p)[i + j] << (16 * (j % 2));
+      }
+    r.lo = make_uint4(w[0], w[1], w[2], w[3]);
+    r.hi = make_uint4(w[4], w[5], w[6], w[7]);
   }
+  return r;
+}
+__device__ __forceinline__ void add_raw8(float (&v)[8], const Raw8& r, int dt) {
+  float f[8];
+  if (dt == 0) {
+    unpack8<0>(r.lo, f);
+  } else if (dt == 1) {
+    unpack8<1>(r.lo, f);
+  } else {
+    *(uint4*)&f[0] = r.lo;
+    *(uint4*)&f[4] = r.hi;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] += f[j];
 }
 __device__ __forceinline__ void store_floats8(void* p, int64_t i, int dt, int64_t left, const float (&f)[8]) {
   if (left >= 8) {
@@ -68,30 +94,52 @@ __device__ __forceinline__ void store_floats8(void* p, int64_t i, int dt, int64_
   }
 }
 
-// 8 consecutive outputs n.. of row m: activation, residual, store.  Quantized results: the block of 32 is 4
-// neighbouring lanes, all active; `in`: the row is there.
-__device__ __forceinline__ void finish8(const Epilogue& x, float (&v)[8], const float (&bias)[8], int64_t m, int64_t n,
-                                        int64_t N, bool in, void* Y, int64_t ld_y) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] += bias[j];
-  activate(v, x.act);
-  if (x.R != nullptr && in) {
-    float r[8];
-    load_floats8(x.R, m * x.ld_r + n, x.r_dtype, N - n, r);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += r[j];
-  }
+// Where a lane's 8 outputs of a row go, and their residual; `on` rows further
+struct OutRow {
+  uint8_t* y;       // Y, or the codes
+  uint8_t* scale;
+  const uint8_t* r;
+};
+__device__ __forceinline__ OutRow out_row(const Epilogue& x, void* Y, int64_t ld_y, int64_t m, int64_t n, int64_t N) {
+  OutRow o = {nullptr, nullptr, nullptr};
   if (x.out <= 2) {
-    if (in) store_floats8(Y, m * ld_y + n, x.out, N - n, v);
+    o.y = (uint8_t*)Y + (m * ld_y + n) * (x.out == 2 ? 4 : 2);
+  } else {
+    const int64_t at = m * N + n;
+    o.y = x.codes + (x.out == kOutFp8 ? at : at / 2);
+    o.scale = x.scales + at / 32;
+  }
+  if (x.R != nullptr) o.r = (const uint8_t*)x.R + (m * x.ld_r + n) * (x.r_dtype == 2 ? 4 : 2);
+  return o;
+}
+__device__ __forceinline__ OutRow row_step(const Epilogue& x, int64_t ld_y, int on, int64_t N) {  // as offsets
+  return {(uint8_t*)(on * (x.out == kOutFp8 ? N : x.out == kOutFp4 ? N / 2 : ld_y * (x.out == 2 ? 4 : 2))),
+          (uint8_t*)(on * (N / 32)), (const uint8_t*)(on * x.ld_r * (x.r_dtype == 2 ? 4 : 2))};
+}
+__device__ __forceinline__ void go_on(OutRow& o, const OutRow& step) {
+  o.y += (intptr_t)step.y, o.scale += (intptr_t)step.scale, o.r += (intptr_t)step.r;
+}
+
+// 8 outputs with their bias: activation, residual (`r` for 16-bit ones), store of the last `left` of them or all.
+// Quantized results: the block of 32 is 4 neighbouring lanes, all active; `in`: the row is there.
+template <bool RES>
+__device__ __forceinline__ void finish8(const Epilogue& x, float (&v)[8], const uint4 r, const OutRow& o, int64_t left,
+                                        bool in) {
+  activate(v, x.act);
+  if (RES && in) add_raw8(v, x.r_dtype == 2 ? load_raw8(o.r, 0, 2, left) : Raw8{r, r}, x.r_dtype);
+  if (x.out <= 2) {
+    if (in) store_floats8(o.y, 0, x.out, left, v);
   } else {
     uint32_t codes[2];
+    uint32_t byte;
     if (x.out == kOutFp8) {
-      const uint32_t byte = mx_quantize8<kMxFp8>(v, codes);
-      if (in) mx_store8<kMxFp8>(codes, byte, x.codes, x.scales, (m * N + n) / 8);
+      byte = mx_quantize8<kMxFp8>(v, codes);
+      if (in) *(uint2*)o.y = make_uint2(codes[0], codes[1]);
     } else {
-      const uint32_t byte = mx_quantize8<kMxFp4>(v, codes);
-      if (in) mx_store8<kMxFp4>(codes, byte, x.codes, x.scales, (m * N + n) / 8);
+      byte = mx_quantize8<kMxFp4>(v, codes);
+      if (in) *(uint32_t*)o.y = codes[0];
     }
+    if (in && threadIdx.x % 4 == 0) *o.scale = (uint8_t)byte;
   }
 }
 

@@ -16,6 +16,10 @@ __global__ __launch_bounds__(256) void mx_reduce_epi_kernel(const float* __restr
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t m = i / (ld_p / 8), n = 8 * (i % (ld_p / 8));
   if (m >= M) return;  // whole blocks of 32 together: ld_p = N where the result is quantized
+  Raw8 bias = {};
+  if (x.bias != nullptr) bias = load_raw8(x.bias, n, x.bias_dtype, N - n);
+  uint4 r = make_uint4(0, 0, 0, 0);
+  if (x.R != nullptr && x.r_dtype != 2) r = load_raw8(x.R, m * x.ld_r + n, x.r_dtype, N - n).lo;
   float4 p[kMaxRanges][2];
 #pragma unroll
   for (int z = 0; z < kMaxRanges; ++z)
@@ -31,9 +35,10 @@ __global__ __launch_bounds__(256) void mx_reduce_epi_kernel(const float* __restr
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += f[j];
     }
-  float bias[8] = {};
-  if (x.bias != nullptr) load_floats8(x.bias, n, x.bias_dtype, N - n, bias);
-  finish8(x, v, bias, m, n, N, n < N, Y, ld_y);
+  if (x.bias != nullptr) add_raw8(v, bias, x.bias_dtype);
+  const OutRow o = out_row(x, Y, ld_y, m, n, N);
+  if (x.R != nullptr) finish8<true>(x, v, r, o, N - n, n < N);
+  else finish8<false>(x, v, r, o, N - n, n < N);
 }
 
 static int64_t part_ld8(int64_t N) { return (N + 7) / 8 * 8; }
@@ -95,6 +100,17 @@ static void linear_tiles(const MxTiling& t, const LinearArgs& p, void* Y, int64_
 #undef AWQ_TILE
 }
 
+template <int AF, class X>
+static void linear_big(const LinearArgs& p, const uint32_t* sc, int n_mt, int n_nt, const X& x, hipStream_t stream) {
+  const int64_t m_pad = (int64_t)n_mt * kBigTile, rows = m_pad + (int64_t)n_nt * kBigTile;
+  if constexpr (AF == kMxFp8)
+    mx_big8_kernel<0, X><<<(unsigned)std::min(n_mt * n_nt, 256), 512, 0, stream>>>(
+        p.A, p.M, p.W, p.N, p.K, sc, m_pad, rows, n_mt, n_nt, 4, p.Y, p.ld_y, x);
+  else
+    mx_big_kernel<0, X><<<(unsigned)(n_mt * n_nt), 512, 0, stream>>>(p.A, p.M, p.W, p.N, p.K, sc, m_pad, rows, n_mt, n_nt,
+                                                                     4, p.Y, p.ld_y, x);
+}
+
 template <int AF>
 static void linear_launch(const LinearArgs& p, void* work, hipStream_t stream) {
   const MxTiling t = mx_tiling(AF, p.M, p.N, p.K);
@@ -107,14 +123,11 @@ static void linear_launch(const LinearArgs& p, void* work, hipStream_t stream) {
     uint32_t* sc = (uint32_t*)work;
     stage_scales_kernel<SB><<<dim3((unsigned)(rows / 256), (unsigned)((kb + 15) / 16)), 256, 0, stream>>>(
         p.as, p.M, p.ws, p.N, kb, m_pad, rows, sc);
-    if constexpr (AF == kMxFp8)
-      mx_big8_kernel<0, Epilogue><<<(unsigned)std::min(n_mt * n_nt, 256), 512, 0, stream>>>(
-          p.A, p.M, p.W, p.N, p.K, sc, m_pad, rows, n_mt, n_nt, 4, p.Y, p.ld_y, p.x);
-    else
-      mx_big_kernel<0, Epilogue><<<(unsigned)(n_mt * n_nt), 512, 0, stream>>>(p.A, p.M, p.W, p.N, p.K, sc, m_pad, rows,
-                                                                              n_mt, n_nt, 4, p.Y, p.ld_y, p.x);
+    if (p.x.R != nullptr) linear_big<AF, Epilogue>(p, sc, n_mt, n_nt, {p.x}, stream);
+    else linear_big<AF, EpilogueAlone>(p, sc, n_mt, n_nt, {p.x}, stream);
   } else if (t.ranges == 1) {
-    linear_tiles<AF, Epilogue>(t, p, p.Y, p.ld_y, p.x, stream);
+    if (p.x.R != nullptr) linear_tiles<AF, Epilogue>(t, p, p.Y, p.ld_y, {p.x}, stream);
+    else linear_tiles<AF, EpilogueAlone>(t, p, p.Y, p.ld_y, {p.x}, stream);
   } else {
     const int64_t ld_p = part_ld8(p.N);
     linear_tiles<AF, NoExtra>(t, p, work, ld_p, NoExtra(), stream);

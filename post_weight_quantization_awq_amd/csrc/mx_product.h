@@ -2,6 +2,8 @@
 // grouped by expert share.
 #pragma once
 
+#include <stddef.h>
+
 #include "mx_device.h"
 #include "mx_extra.h"
 #include "mx_tiles.h"
@@ -388,41 +390,102 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[NT][MT], uint8_t*
     }
 }
 
-// The same with an epilogue: the sums go through LDS in fp32, 32 tokens x 32 outputs at a time, and come back 8
-// outputs a lane.  The residual of the next 16 rows is on its way meanwhile.
-template <int MT, int NT, int NW, int SB, int NA>
+// The same with an epilogue: the sums go through LDS in fp32, 16 tokens x 64 outputs at a time (32 x 32 where a wave
+// has no more), and come back 8 outputs a lane, so that 128 bytes of a row go to memory together.
+// The turns are a loop, of which only the choice of the registers is unrolled: with all of it unrolled (60 KB of code,
+// run once a tile) the blocks waited for instructions (8192 x 4096 x 4096 in 4 bits: 130 us, 72 without an
+// epilogue).  A wait for a load is one for all earlier stores, too, so the bias lies in LDS, and with AHEAD, where the
+// registers suffice, 16-bit residuals are loaded for all turns at first.
+template <int MT, int NT, int NW, int SB, int NA, bool AHEAD, class X>
 __device__ __forceinline__ void store_tile_epi(const f32x16 (&acc)[NT][MT], uint8_t* s0, uint8_t* s1, uint8_t* s2,
                                                int wave, int lane, int64_t m0, int64_t n0, int64_t M, int64_t N,
-                                               void* Y, int64_t ld_y, const Epilogue& x) {
+                                               void* Y, int64_t ld_y, const X& x) {
+  constexpr int CG = NT > 1 ? 2 : 1;                              // 32-output tiles a turn
+  constexpr int TR = 32 / CG, NS = MT * CG, LR = 4 * CG;          // tokens a turn, turns, lanes of a row
   constexpr int WS = (NW + NA - 1) / NA;                          // waves an array
-  constexpr int RS = WS * 32 * 144 <= SB ? 144 : 128;             // stride of a row: padded where there is room
-  static_assert(WS * 32 * RS <= SB, "an array holds the rows of its waves");
-  uint8_t* part = (wave < WS ? s0 : wave < 2 * WS ? s1 : s2) + wave % WS * (32 * RS);
-  const int r = lane & 31, h = lane >> 5, row = lane / 4, c = 8 * (lane % 4);
+  constexpr int RS = WS * TR * (CG * 128 + 16) <= SB ? CG * 128 + 16 : CG * 128;  // padded where there is room
+  constexpr bool RES = X::kRes;
+  static_assert(WS * TR * RS <= SB, "an array holds the rows of its waves");
+  __shared__ __attribute__((aligned(16))) float biases[NW][32 * NT];
+  uint8_t* part = (wave < WS ? s0 : wave < 2 * WS ? s1 : s2) + wave % WS * (TR * RS);
+  const int r = lane & 31, h = lane >> 5, row = lane / LR, c = 8 * (lane % LR);
+  const int rows = (int)(M - m0 < 32 * MT ? M - m0 : 32 * MT);  // of the wave's
+  uint4 res[NT / CG][NS][2];  // with AHEAD
+  const OutRow step = row_step(x, ld_y, TR / 2, N);
+  auto load_res = [&](int ip, uint4 (&v)[NS][2]) {
+    if (x.r_dtype == 2) return;
+    const int64_t n = n0 + 32 * CG * ip + c;
+    OutRow o = out_row(x, Y, ld_y, m0 + row, n, N);
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int64_t n = n0 + 32 * i + c;
-    float bias[8] = {};
-    if (x.bias != nullptr) load_floats8(x.bias, n, x.bias_dtype, N - n, bias);
+    for (int t = 0; t < 2 * NS; ++t) {
+      v[t / 2][t % 2] = make_uint4(0, 0, 0, 0);
+      if (row + TR / 2 * t < rows && n < N) v[t / 2][t % 2] = load_raw8(o.r, 0, x.r_dtype, N - n).lo;
+      o.r += (intptr_t)step.r;
+    }
+  };
+  if constexpr (RES && AHEAD) {
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
+    for (int ip = 0; ip < NT / CG; ++ip) load_res(ip, res[ip]);
+  }
+  if (x.bias != nullptr) {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x16& v = acc[i][j];
-        *(float4*)(part + r * RS + (8 * g + 4 * h) * 4) =
-            make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+    for (int i = 0; i < (NT + 1) / 2; ++i) {
+      const int64_t n = n0 + 64 * i + lane;
+      if ((NT > 1 || lane < 32) && n < N) biases[wave][64 * i + lane] = load_float(x.bias, n, x.bias_dtype);
+    }
+  }
+#pragma unroll
+  for (int ip = 0; ip < NT / CG; ++ip) {
+    if (ip == 0) wait_loads<0>();
+    const int64_t n = n0 + 32 * CG * ip + c;
+    OutRow o = out_row(x, Y, ld_y, m0 + row, n, N);
+    int at_row = row;
+#pragma unroll 1
+    for (int s = 0; s < NS; ++s) {
+      uint4 now[2] = {};
+      if constexpr (RES && !AHEAD) {
+        if (x.r_dtype != 2) {
+#pragma unroll
+          for (int it = 0; it < 2; ++it)
+            if (at_row + TR / 2 * it < rows && n < N)
+              now[it] = load_raw8(o.r + it * (intptr_t)step.r, 0, x.r_dtype, N - n).lo;
+        }
       }
+#pragma unroll
+      for (int k = 0; k < NS; ++k)
+        if (s == k) {
+          if (CG == 1 || r / 16 == k % 2) {
+#pragma unroll
+            for (int i = 0; i < CG; ++i)
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const f32x16& v = acc[CG * ip + i][k / CG];
+                *(float4*)(part + (CG == 1 ? r : r % 16) * RS + (32 * i + 8 * g + 4 * h) * 4) =
+                    make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+              }
+          }
+          if constexpr (RES && AHEAD) {
+            now[0] = res[ip][k][0];
+            now[1] = res[ip][k][1];
+          }
+        }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
+#pragma unroll 1
       for (int it = 0; it < 2; ++it) {
-        const uint8_t* at = part + (16 * it + row) * RS + 4 * c;
+        const uint8_t* at = part + (TR / 2 * it + row) * RS + 4 * c;
         float v[8];
         *(float4*)&v[0] = *(const float4*)at;
         *(float4*)&v[4] = *(const float4*)(at + 16);
-        const int64_t m = m0 + 32 * j + 16 * it + row;
-        finish8(x, v, bias, m, n, N, m < M && n < N, Y, ld_y);
+        if (x.bias != nullptr) {
+          const float* b = &biases[wave][32 * CG * ip + c];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] += b[j];
+        }
+        finish8<RES>(x, v, it == 0 ? now[0] : now[1], o, N - n, at_row < rows && n < N);
+        go_on(o, step);
+        at_row += TR / 2;
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -686,7 +749,7 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
   block_barrier();
 
   if constexpr (X::kEpi)
-    store_tile_epi<MT, NT, NW, BM * AB + BN * WB, 3>(acc, s0, s1, s2, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M,
+    store_tile_epi<MT, NT, NW, BM * AB + BN * WB, 3, true>(acc, s0, s1, s2, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M,
                                                      N, Y, ld_y, x);
   else
     store_tile<YT, MT, NT, NW, BM * AB + BN * WB>(acc, s0, s1, s2, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M, N,
@@ -777,7 +840,9 @@ __global__ __launch_bounds__(256) void stage_groups_kernel(const Groups g, const
     p = as + (live ? of : 0) * kb;
     if (blockIdx.y == 0) {
       if (threadIdx.x == 0) tab[blockIdx.x] = make_int4(t.group, t.first, t.end, 0);
-      if (g.rows != nullptr) a_at[row] = live ? (uint32_t)of * a_row : kMxOut;
+      // the rows of each 32 in the order in which 8 lanes take every 8th of them
+      const int i = (int)threadIdx.x, place = (i & ~31) | (i & 7) << 2 | (i >> 3 & 3);
+      if (g.rows != nullptr) a_at[row - (int)threadIdx.x + place] = live ? (uint32_t)of * a_row : kMxOut;
     }
   } else {
     const int64_t r = row - (int64_t)n_mt * kBigTile;
@@ -855,7 +920,8 @@ __global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restric
     va[j] = row < m_rows ? at : kMxOut;
     vw[j] = row < n_rows ? at : kMxOut;
     if constexpr (X::kGroups) {
-      if (x.rows != nullptr) va[j] = sg.a_at[sc_m + row] + 16u * (uint32_t)(lane % 8 ^ swz8(row));
+      if (x.rows != nullptr)
+        va[j] = sg.a_at[sc_m + 32 * wave + 4 * (lane / 8) + j] + 16u * (uint32_t)(lane % 8 ^ swz8(row));
     }
   }
   // scales: the wave's 64 of the tile's 256 + 256 rows; words past the last stage's are not read
@@ -968,10 +1034,41 @@ __global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restric
   wait_loads<0>();  // none may land after the block has given its LDS back
   block_barrier();
   if constexpr (X::kEpi)
-    store_tile_epi<MT, NT, NW, SB, 2>(acc, s0, s1, s1, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M, N, Y, ld_y, x);
+    store_tile_epi<MT, NT, NW, SB, 2, true>(acc, s0, s1, s1, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M, N, Y, ld_y, x);
   else
     store_tile<YT, MT, NT, NW, SB / 2>(acc, s0, s1, s1 + SB / 2, wave, lane, m0 + wm * MT * 32, n0 + wn * NT * 32, M, N,
                                        Y, ld_y);
+}
+
+// The arguments of mx_big8_kernel as they lie in its argument block.  The epilogue reads its own ones there, behind a
+// pointer that the compiler cannot see through: kept in scalar registers meanwhile they would push addresses of the
+// stages into scratch memory, and each of those reloads waits for all loads in flight (4096 x 12288 x 4096: 1064 us).
+template <class X>
+struct Big8Args {
+  const uint8_t* A;
+  int64_t M;
+  const uint8_t* W;
+  int64_t N, K;
+  const uint32_t* sc;
+  int64_t m_pad, rows;
+  int n_mt, n_nt, group_m;
+  void* Y;
+  int64_t ld_y;
+  X x;
+  StagedGroups sg;
+};
+template <class X>
+__device__ __forceinline__ X own_extra() {
+  typedef __attribute__((address_space(4))) const uint64_t* words;
+  static_assert(sizeof(X) % 8 == 0 && offsetof(Big8Args<X>, x) % 8 == 0, "whole words");
+  words p = (words)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  uint64_t w[sizeof(X) / 8];
+#pragma unroll
+  for (size_t i = 0; i < sizeof(X) / 8; ++i) w[i] = p[offsetof(Big8Args<X>, x) / 8 + i];
+  X x;
+  __builtin_memcpy(&x, w, sizeof(X));
+  return x;
 }
 
 // 8-bit activations, stages of 128 K in three LDS slots as in mx_tile_kernel, each with its scale words.  At
@@ -990,9 +1087,9 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
   constexpr int WM = 4, WN = 2, NW = 8, MT = T / WM / 32, NT = T / WN / 32;
   constexpr int AB = 128, WB = 64;                                    // bytes of a row's stage
   constexpr int AI = T * AB / 1024 / NW, WI = T * WB / 1024 / NW;     // direct loads of codes a wave and stage
-  constexpr int ND = AI + WI + 1;                                     // and one of scales
+  constexpr int ND = AI + WI + 1 + (GATHER ? 1 : 0);                  // one of scales, and one of row offsets
   constexpr int NR = NT + 2 * MT;                                     // LDS reads of a step's fragments
-  constexpr int oW = T * AB, oS = oW + T * WB, SB = oS + 2 * T * 4;
+  constexpr int oW = T * AB, oS = oW + T * WB, oO = oS + 2 * T * 4, SB = oO + (GATHER ? NW * 256 : 0);
   __shared__ __attribute__((aligned(1024))) uint8_t s0[SB];
   __shared__ __attribute__((aligned(1024))) uint8_t s1[SB];
   __shared__ __attribute__((aligned(1024))) uint8_t s2[SB];
@@ -1038,20 +1135,15 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
   };
   Place now = tile_at((int)blockIdx.x), then = tile_at((int)(blockIdx.x + gridDim.x));  // computed, computed next
   Place src = now;  // loaded
-  uint32_t vn[AI];  // offsets of the next tile's rows
-  auto row_offsets = [&](const Place& t, uint32_t (&v)[AI]) {
-#pragma unroll
-    for (int j = 0; j < AI; ++j) {
-      const int row = (wave * AI + j) * (1024 / AB) + lane / (AB / 16);
-      v[j] = sg.a_at[t.sc + row] + 16u * (uint32_t)(lane % (AB / 16) ^ swz8(row));
-    }
-  };
-  if constexpr (GATHER) {
-    row_offsets(now, va);
-    row_offsets(then, vn);
-  }
   int l_k = 0;     // and its stage that is loaded next
-  auto load_stage = [&](uint8_t* dst) {
+  // GATHER: the offsets of a tile's rows, 32 of each wave, come with the stage that is computed when they are needed,
+  // two stages ahead of the one that they are for (a tile has at least four).  at: where the first ones come from
+  auto load_stage = [&](uint8_t* dst, const void* at) {
+    if constexpr (GATHER) {
+      const uint4 v = *(const uint4*)at;
+      const uint32_t piece = 16u * (uint32_t)(lane % 8 ^ lane / 8);
+      va[0] = v.x + piece, va[1] = v.y + (piece ^ 16), va[2] = v.z + piece, va[3] = v.w + (piece ^ 16);
+    }
     const int m0 = __builtin_amdgcn_readfirstlane(src.m0), n0 = __builtin_amdgcn_readfirstlane(src.n0);
     const int k = __builtin_amdgcn_readfirstlane(l_k);
     const int end = X::kGroups ? __builtin_amdgcn_readfirstlane(src.end) : (int)M;
@@ -1069,6 +1161,9 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
     for (int j = 0; j < WI; ++j) load_lds16(w_tile, w.bytes, dst + oW + (wave * WI + j) * 1024, vw[j], w.k_off);
     load_lds4(sc + k * rows + (wave < 4 ? sc_m + 64 * wave : sc_n + 64 * (wave - 4)), a.bytes > 0 ? 256 : 0,
               dst + oS + 256 * wave, 4u * (uint32_t)lane);
+    if constexpr (GATHER)
+      load_lds4(sg.a_at + (k + 2 >= nk ? __builtin_amdgcn_readfirstlane(then.sc) : sc_m) + 32 * wave, a.bytes > 0 ? 128 : 0,
+                dst + oO + 256 * wave, 4u * (uint32_t)(lane % 32));
     const bool wrap = k + 1 == nk;  // without a branch, which would part the stage's products
     l_k = wrap ? 0 : k + 1;
     src.m0 = wrap ? then.m0 : m0;
@@ -1077,10 +1172,6 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
       src.end = wrap ? then.end : end;
       src.group = wrap ? then.group : group;
       src.sc = wrap ? then.sc : sc_m;
-    }
-    if constexpr (GATHER) {
-#pragma unroll
-      for (int j = 0; j < AI; ++j) va[j] = wrap ? vn[j] : va[j];
     }
   };
 
@@ -1143,6 +1234,8 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
         acc[i][j] = mfma_mx32<kMxFp8>(lo4(f.w[i]), f.a[j], acc[i][j], (int)s.w[i], (int)s.a[j], step);
   };
 
+  auto offsets = [&](const uint8_t* slot) { return (const void*)(slot + oO + 256 * wave + 16 * (lane / 8)); };
+  const void* first = GATHER ? (const void*)(sg.a_at + now.sc + 32 * wave + 4 * (lane / 8)) : nullptr;
   Frags f0, f1;
   Scales c0, c1;
   clear();
@@ -1154,7 +1247,7 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
   {                                      \
     own_bytes(c0, c1);                   \
     read_frags(f1, C, 1);                \
-    load_stage(F);                       \
+    load_stage(F, offsets(C));           \
     products(f0, c0, 0);                 \
     interleave<NR, ND>();                \
     __builtin_amdgcn_sched_barrier(0);   \
@@ -1175,7 +1268,7 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
   const int64_t ym = now.m0 + wm * MT * 32, yn = now.n0 + wn * NT * 32;                                    \
   const int64_t ye = X::kGroups ? now.end : M;                                                             \
   if constexpr (X::kEpi)                                                                                   \
-    store_tile_epi<MT, NT, NW, SB, 1>(acc, C, C, C, wave, own, ym, yn, M, N, Y, ld_y, x);                  \
+    store_tile_epi<MT, NT, NW, SB, 1, false>(acc, C, C, C, wave, own, ym, yn, M, N, Y, ld_y, own_extra<X>());     \
   else if (now.m0 + T <= ye && now.n0 + T <= N)                                                            \
     store_tile<YT, MT, NT, NW, SB, 1, true>(acc, C, C, C, wave, own, ym, yn, ye, N, Y, ld_y);              \
   else                                                                                                     \
@@ -1185,15 +1278,14 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
   kt = 0;                                \
   now = then;                            \
   then = tile_at(tile + (int)gridDim.x); \
-  if constexpr (GATHER) row_offsets(then, vn); \
   clear();                               \
   wait_lds();                            \
   block_barrier();                       \
   read_scales(c1, X);                    \
   read_frags(f0, X, 0);
 #define AWQ_MX_START(C, X) \
-  load_stage(C);           \
-  load_stage(X);           \
+  load_stage(C, first);    \
+  load_stage(X, first);    \
   wait_loads<ND>();        \
   block_barrier();         \
   read_scales(c1, C);      \
@@ -1212,24 +1304,27 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
     AWQ_MX_STAGE(s1, s2, s0)
     AWQ_MX_STAGE(s2, s0, s1)
   }
+  // the epilogue's loops are not to look hotter to the register allocation than the stages
+#define AWQ_MX_IF_ENDED if (X::kEpi ? __builtin_expect(kt == nk, false) : kt == nk)
   for (;;) {
     AWQ_MX_STAGE(s0, s1, s2)
-    if (kt == nk) {
+    AWQ_MX_IF_ENDED {
       AWQ_MX_STORE(s0)
       AWQ_MX_NEXT(s1)
     }
     AWQ_MX_STAGE(s1, s2, s0)
-    if (kt == nk) {
+    AWQ_MX_IF_ENDED {
       AWQ_MX_STORE(s1)
       AWQ_MX_NEXT(s2)
     }
     AWQ_MX_STAGE(s2, s0, s1)
-    if (kt == nk) {
+    AWQ_MX_IF_ENDED {
       AWQ_MX_STORE(s2)
       if (tile >= tiles) break;
       AWQ_MX_NEXT(s0)
     }
   }
+#undef AWQ_MX_IF_ENDED
 #undef AWQ_MX_START
 #undef AWQ_MX_NEXT
 #undef AWQ_MX_STORE

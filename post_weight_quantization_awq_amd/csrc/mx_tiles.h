@@ -175,6 +175,7 @@ inline GroupTiling group_tiling(int a_fmt, int64_t M, int64_t N, int64_t K, int 
   const int nk = (int)((K + kMxStage - 1) / kMxStage);
   for (int tile = 64; tile <= 256; tile *= 2) {
     const double n_nt = (double)((N + tile - 1) / tile);
+    if (tile == kBigTile && K <= 3 * kMxStage) continue;  // the persistent blocks look two stages ahead within a tile
     if ((double)group_tiles_most(M, n_groups, tile) * n_nt > (1 << 22)) continue;  // a launch holds fewer than 2^32 lanes
     const double t = tile_time(a_fmt, tile, used * ceil(each / tile) * n_nt, nk);
     if (t < least) least = t, best.tile = tile;
