@@ -16,7 +16,7 @@ namespace awq {
 
 // A row of X, or the weighted sum of its rows that a token's places name; places outside X name none.  Rows are
 // loaded four at a time, ahead of their sums (one at a time from 16385 columns on, for want of registers).
-template <int DT, int CH>
+template <int DT, int CH, bool FULL>
 __device__ __forceinline__ void load_sum(const BlockNormArgs& a, int64_t row, int lane, int lanes, int cpr,
                                          float (&y)[CH][8]) {
 #pragma unroll
@@ -26,7 +26,7 @@ __device__ __forceinline__ void load_sum(const BlockNormArgs& a, int64_t row, in
   if (a.places == nullptr) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      if (lane + c * lanes < cpr) unpack8<DT>(ld_stream(a.X + row * a.ld_x + 8 * (lane + c * lanes)), y[c]);
+      if (FULL || lane + c * lanes < cpr) unpack8<DT>(ld_stream(a.X + row * a.ld_x + 8 * (lane + c * lanes)), y[c]);
     return;
   }
   constexpr int NP = CH >= 4 ? 1 : 4;
@@ -44,13 +44,13 @@ __device__ __forceinline__ void load_sum(const BlockNormArgs& a, int64_t row, in
     for (int j = 0; j < NP; ++j)
 #pragma unroll
       for (int c = 0; c < CH; ++c)
-        if ((int64_t)place[j] < a.x_rows && lane + c * lanes < cpr)
+        if ((int64_t)place[j] < a.x_rows && (FULL || lane + c * lanes < cpr))
           x[j][c] = ld_stream(a.X + (int64_t)place[j] * a.ld_x + 8 * (lane + c * lanes));
 #pragma unroll
     for (int j = 0; j < NP; ++j)
 #pragma unroll
       for (int c = 0; c < CH; ++c)
-        if ((int64_t)place[j] < a.x_rows && lane + c * lanes < cpr) {
+        if ((int64_t)place[j] < a.x_rows && (FULL || lane + c * lanes < cpr)) {
           float f[8];
           unpack8<DT>(x[j][c], f);
 #pragma unroll
@@ -59,52 +59,91 @@ __device__ __forceinline__ void load_sum(const BlockNormArgs& a, int64_t row, in
   }
 }
 
-template <int CH>
+// 8 weights as they lie in memory
+struct Ahead8 {
+  uint4 lo, hi;  // hi: of 32-bit ones
+};
+__device__ __forceinline__ Ahead8 load_ahead(const void* w, int dt, int64_t col) {
+  Ahead8 r;
+  if (dt == 2) {
+    r.lo = ld_any<uint4>((const float*)w + col);
+    r.hi = ld_any<uint4>((const float*)w + col + 4);
+  } else {
+    r.lo = ld_any<uint4>((const uint16_t*)w + col);
+  }
+  return r;
+}
+__device__ __forceinline__ void ahead_values(const Ahead8& r, int dt, float (&f)[8]) {
+  if (dt == 2) {
+    *(uint4*)&f[0] = r.lo;
+    *(uint4*)&f[4] = r.hi;
+  } else if (dt == 0) {
+    unpack8<0>(r.lo, f);
+  } else {
+    unpack8<1>(r.lo, f);
+  }
+}
+
+template <int CH, bool FULL>
 __device__ __forceinline__ float squares(const float (&h)[CH][8], int lane, int lanes, int cpr) {
   float sum = 0.0f;
 #pragma unroll
   for (int c = 0; c < CH; ++c)
-    if (lane + c * lanes < cpr)
+    if (FULL || lane + c * lanes < cpr)
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(h[c][j], h[c][j], sum);
   return sum;
 }
 
-template <int DT, int FMT, int GL, int CH>
+// FULL: every lane has CH chunks
+template <int DT, int FMT, int GL, int CH, bool FULL>
 __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const BlockNormArgs a) {
   const int lanes = GL ? GL : (int)blockDim.x;
   const int lane = GL ? (int)threadIdx.x % (GL ? GL : 1) : (int)threadIdx.x;
   const int64_t row = GL ? (int64_t)blockIdx.x * (256 / (GL ? GL : 1)) + (int)threadIdx.x / (GL ? GL : 1)
                          : (int64_t)blockIdx.x;
-  const bool live = row < a.rows;
-  const int cpr = live ? (int)(a.cols / 8) : 0;  // chunks of the row that there are
+  const bool live = FULL || row < a.rows;
+  const int cpr = FULL ? CH * lanes : live ? (int)(a.cols / 8) : 0;  // chunks of the row that there are
   __shared__ float part[2][GL ? 1 : 16];
-  constexpr bool kEarly = CH < 8;  // the residual ahead of the sums, but for the longest rows, for want of registers
+  constexpr bool kEarly = CH < 4;  // what is added ahead of the sums, but for the longest rows, for want of registers
   uint4 res[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c)
-    if (kEarly && lane + c * lanes < cpr) res[c] = ld_stream(a.R + row * a.ld_r + 8 * (lane + c * lanes));
+    if (kEarly && (FULL || lane + c * lanes < cpr)) res[c] = ld_stream(a.R + row * a.ld_r + 8 * (lane + c * lanes));
   float h[CH][8];
-  load_sum<DT, CH>(a, row, lane, lanes, cpr, h);
-  if (a.post != nullptr) {
-    const float r = row_scale<GL, CH>(h, squares<CH>(h, lane, lanes, cpr), live, lane, lanes, cpr, a.cols, a.eps,
-                                      part[0]);
+  load_sum<DT, CH, FULL>(a, row, lane, lanes, cpr, h);
+  Ahead8 post[CH], gate[CH], norm[CH];
+  auto each = [&](auto f) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      if (lane + c * lanes < cpr) {
+      if (kEarly && (FULL || lane + c * lanes < cpr)) f(c, 8 * (int64_t)(lane + c * lanes));
+  };
+  auto get_post = [&]() { if (a.post != nullptr) each([&](int c, int64_t col) { post[c] = load_ahead(a.post, a.post_dtype, col); }); };
+  auto get_gate = [&]() { if (a.gate != nullptr) each([&](int c, int64_t col) { gate[c] = load_ahead(a.gate, a.gate_dtype, row * a.ld_g + col); }); };
+  auto get_norm = [&]() { each([&](int c, int64_t col) { norm[c] = load_ahead(a.norm, a.norm_dtype, col); }); };
+  if (a.post != nullptr) {
+    const float r = row_scale<GL, CH>(h, squares<CH, FULL>(h, lane, lanes, cpr), live, lane, lanes, cpr, a.cols, a.eps,
+                                      part[0]);
+    get_post();
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (FULL || lane + c * lanes < cpr) {
         float w[8];
-        load_weight8(a.post, a.post_dtype, 8 * (int64_t)(lane + c * lanes), w);
+        if constexpr (kEarly) ahead_values(post[c], a.post_dtype, w);
+        else load_weight8(a.post, a.post_dtype, 8 * (int64_t)(lane + c * lanes), w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[c][j] = h[c][j] * r * w[j];
       }
   }
+  get_gate();
 #pragma unroll
   for (int c = 0; c < CH; ++c)
-    if (lane + c * lanes < cpr) {
+    if (FULL || lane + c * lanes < cpr) {
       const int64_t col = 8 * (int64_t)(lane + c * lanes);
       if (a.gate != nullptr) {
         float g[8];
-        load_weight8(a.gate, a.gate_dtype, row * a.ld_g + col, g);
+        if constexpr (kEarly) ahead_values(gate[c], a.gate_dtype, g);
+        else load_weight8(a.gate, a.gate_dtype, row * a.ld_g + col, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[c][j] *= g[j];
       }
@@ -116,13 +155,15 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const Bl
       st_any(a.RO + row * a.ld_ro + col, pack8<DT>(h[c]));
     }
   const float r =
-      row_scale<GL, CH>(h, squares<CH>(h, lane, lanes, cpr), live, lane, lanes, cpr, a.cols, a.eps, part[1]);
+      row_scale<GL, CH>(h, squares<CH, FULL>(h, lane, lanes, cpr), live, lane, lanes, cpr, a.cols, a.eps, part[1]);
+  get_norm();
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int k = lane + c * lanes;
-    if (k < cpr) {
+    if (FULL || k < cpr) {
       float w[8];
-      load_weight8(a.norm, a.norm_dtype, 8 * (int64_t)k, w);
+      if constexpr (kEarly) ahead_values(norm[c], a.norm_dtype, w);
+      else load_weight8(a.norm, a.norm_dtype, 8 * (int64_t)k, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[c][j] = h[c][j] * r * w[j];
       uint32_t codes[2];
@@ -136,20 +177,23 @@ template <int DT, int FMT>
 static void block_norm_launch(const BlockNormArgs& a, hipStream_t stream) {
   const int64_t cpr = a.cols / 8;
 #define AWQ_NORM_W(GL, CH) \
-  block_norm_mx_kernel<DT, FMT, GL, CH><<<(unsigned)((a.rows + 256 / GL - 1) / (256 / GL)), 256, 0, stream>>>(a)
-#define AWQ_NORM_B(CH)                                                                                               \
-  block_norm_mx_kernel<DT, FMT, 0, CH><<<(unsigned)a.rows, (unsigned)(((cpr + CH - 1) / CH + 63) / 64 * 64), 0, stream>>>( \
-      a)
+  block_norm_mx_kernel<DT, FMT, GL, CH, false><<<(unsigned)((a.rows + 256 / GL - 1) / (256 / GL)), 256, 0, stream>>>(a)
+#define AWQ_NORM_B(CH, FULL)                                                                                         \
+  block_norm_mx_kernel<DT, FMT, 0, CH, FULL><<<(unsigned)a.rows, (unsigned)(((cpr + CH - 1) / CH + 63) / 64 * 64), 0, \
+                                               stream>>>(a)
   if (cpr <= 4) AWQ_NORM_W(4, 1);
   else if (cpr <= 8) AWQ_NORM_W(8, 1);
   else if (cpr <= 16) AWQ_NORM_W(16, 1);
   else if (cpr <= 32) AWQ_NORM_W(32, 1);
   else if (cpr <= 64) AWQ_NORM_W(32, 2);
-  else if (cpr <= 512) AWQ_NORM_B(2);
-  else if (cpr <= 1024) AWQ_NORM_B(1);
-  else if (cpr <= 2048) AWQ_NORM_B(2);
-  else if (cpr <= 4096) AWQ_NORM_B(4);
-  else AWQ_NORM_B(8);
+  else if (cpr <= 512 && cpr % 128 == 0) AWQ_NORM_B(2, true);
+  else if (cpr <= 512) AWQ_NORM_B(2, false);
+  else if (cpr <= 1024 && cpr % 64 == 0) AWQ_NORM_B(1, true);
+  else if (cpr <= 1024) AWQ_NORM_B(1, false);
+  else if (cpr <= 2048 && cpr % 128 == 0) AWQ_NORM_B(2, true);
+  else if (cpr <= 2048) AWQ_NORM_B(2, false);
+  else if (cpr <= 4096) AWQ_NORM_B(4, false);
+  else AWQ_NORM_B(8, false);
 #undef AWQ_NORM_W
 #undef AWQ_NORM_B
 }

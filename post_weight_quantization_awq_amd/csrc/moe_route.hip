@@ -11,6 +11,7 @@
 //
 // Bound by latency, not by the logits' bytes.
 #include "awq_launch.h"
+#include "mx_device.h"
 
 namespace awq {
 
@@ -192,6 +193,131 @@ __global__ __launch_bounds__(kRouteThreads) void route_select_kernel(const Route
   }
 }
 
+// More tokens: 4 lanes take a token, each a fourth of its logits, and keep the best K of them in order by insertion
+// (a maximum and a minimum for each place); two merges across the lanes join them.  A logit and its expert are one
+// positive double that orders as they do: 32 bits of key, then the experts from the last to the first.  62 operations
+// a token of 128 experts and 8 places, where a wave for each token takes 300.
+constexpr int kLaneThreads = 4 * kRouteChunk, kLaneExperts = 256;
+__device__ __forceinline__ double route_pack(uint32_t key, uint32_t e) {
+  return __builtin_bit_cast(double, (uint64_t)key << 30 | (0x3FFFFFFFu - e));
+}
+__device__ __forceinline__ uint32_t packed_key(double d) { return (uint32_t)(__builtin_bit_cast(uint64_t, d) >> 30); }
+__device__ __forceinline__ int packed_expert(double d) {
+  return (int)(0x3FFFFFFFu - ((uint32_t)__builtin_bit_cast(uint64_t, d) & 0x3FFFFFFFu));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double d) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, d);
+  return __builtin_bit_cast(double, (uint64_t)dpp_u<CTRL>((uint32_t)(u >> 32)) << 32 | dpp_u<CTRL>((uint32_t)u));
+}
+__device__ __forceinline__ void order(double& a, double& b) {  // a the larger
+  const double m = __builtin_fmax(a, b);
+  b = __builtin_fmin(a, b);
+  a = m;
+}
+// The best K of the lane's and another lane's lists, in order
+template <int K, int CTRL>
+__device__ __forceinline__ void merge_lists(double (&v)[K]) {
+  double o[K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) o[i] = dpp_d<CTRL>(v[K - 1 - i]);
+#pragma unroll
+  for (int i = 0; i < K; ++i) v[i] = __builtin_fmax(v[i], o[i]);  // falls, then rises, or the other way round
+#pragma unroll
+  for (int d = K / 2; d >= 1; d /= 2)
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if ((i & d) == 0) order(v[i], v[i + d]);
+}
+
+// The lane's 4 logits of 16 from e on; -inf for those that are not there
+template <int DT>
+__device__ __forceinline__ void load_logits4(const RouteArgs& a, int64_t at, int e, float (&f)[4]) {
+  if (e + 4 <= a.n_experts) {
+    if constexpr (DT == 2) {
+      *(float4*)f = ld_any<float4>((const float*)a.logits + at + e);
+    } else {
+      const uint2 u = ld_any<uint2>((const uint16_t*)a.logits + at + e);
+      f[0] = x2f<DT>(u.x & 0xFFFFu), f[1] = x2f<DT>(u.x >> 16), f[2] = x2f<DT>(u.y & 0xFFFFu), f[3] = x2f<DT>(u.y >> 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = e + i < a.n_experts ? route_logit(a.logits, DT, at + e + i) : -INFINITY;
+  }
+}
+
+template <int K, int DT>
+__global__ __launch_bounds__(kLaneThreads) void route_lanes_kernel(const RouteArgs a) {
+  __shared__ unsigned long long mask[kLaneExperts];
+  const int tid = threadIdx.x, q = tid % 4, tt = tid / 4;
+  const int64_t t0 = (int64_t)blockIdx.x * a.per;
+  uint32_t count = 0;  // of expert `tid`
+  for (int c = 0; c < a.per && t0 + c < a.rows; c += kRouteChunk) {
+    mask[tid] = 0;
+    __syncthreads();
+    const int64_t t = t0 + c + tt;
+    const bool live = t < a.rows;
+    const int64_t at = (live ? t : a.rows - 1) * a.ld;
+    double v[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = 0.0;
+#pragma unroll 2
+    for (int e = 4 * q; e < a.n_experts; e += 16) {
+      float f[4];
+      load_logits4<DT>(a, at, e, f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t key = route_key(f[i]);
+        double x = key != 0 ? route_pack(key, (uint32_t)(e + i)) : 0.0;
+#pragma unroll
+        for (int s = 0; s < K; ++s) order(v[s], x);
+      }
+    }
+    merge_lists<K, 0xB1>(v);
+    merge_lists<K, 0x4E>(v);
+    const float most = route_value(packed_key(v[0]));
+    float sum = 0.0f;
+    if (!a.renorm && v[0] != 0.0) {
+#pragma unroll 2
+      for (int e = 4 * q; e < a.n_experts; e += 16) {
+        float f[4];
+        load_logits4<DT>(a, at, e, f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (route_key(f[i]) != 0) sum += expf(f[i] - most);
+      }
+    }
+    // the lane's places: q, q + 4
+    constexpr int PL = (K + 3) / 4;
+    int id[PL];
+    float p[PL];
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      double d = 0.0;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        if (4 * i + s < K) d = q == s ? v[4 * i + s] : d;
+      const bool some = d != 0.0 && 4 * i + q < a.top;
+      id[i] = some ? packed_expert(d) : -1;
+      p[i] = some ? expf(route_value(packed_key(d)) - most) : 0.0f;
+      if (a.renorm) sum += p[i];
+    }
+    sum += dpp_m<0xB1>(sum);
+    sum += dpp_m<0x4E>(sum);
+#pragma unroll
+    for (int i = 0; i < PL; ++i)
+      if (live && 4 * i + q < a.top) {
+        a.experts[t * a.top + 4 * i + q] = id[i];
+        a.weights[t * a.top + 4 * i + q] = id[i] >= 0 ? p[i] / sum * a.scale : 0.0f;
+        if (id[i] >= 0) atomicOr(&mask[id[i]], 1ull << tt);
+      }
+    __syncthreads();
+    count += __popcll(mask[tid]);
+    __syncthreads();  // the masks are cleared for the next chunk
+  }
+  if (tid < a.ld_counts) a.counts[(int64_t)blockIdx.x * a.ld_counts + tid] = (uint16_t)count;
+}
+
 // Places of a block's pairs: the experts' totals and what lies in the blocks before, from the counts of all blocks,
 // 8 experts a thread.
 __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(const RouteArgs a) {
@@ -276,14 +402,24 @@ size_t moe_route_workspace(int64_t rows, int n_experts) {
   return rows <= kRouteChunk ? 0 : (size_t)route_blocks(rows) * ((n_experts + 7) / 8 * 8) * sizeof(uint16_t);
 }
 
+template <int K>
+static void route_lanes_launch(const RouteArgs& a, hipStream_t stream) {
+  if (a.dtype == 0) route_lanes_kernel<K, 0><<<(unsigned)a.blocks, kLaneThreads, 0, stream>>>(a);
+  else if (a.dtype == 1) route_lanes_kernel<K, 1><<<(unsigned)a.blocks, kLaneThreads, 0, stream>>>(a);
+  else route_lanes_kernel<K, 2><<<(unsigned)a.blocks, kLaneThreads, 0, stream>>>(a);
+}
+
 template <int EL>
 static void route_launch(const RouteArgs& a, hipStream_t stream) {
   if (a.blocks == 1) {
     route_select_kernel<EL, true><<<1, kRouteThreads, 0, stream>>>(a);
-  } else {
-    route_select_kernel<EL, false><<<(unsigned)a.blocks, kRouteThreads, 0, stream>>>(a);
-    route_place_kernel<<<(unsigned)a.blocks, kRouteThreads, 0, stream>>>(a);
+    return;
   }
+  if (a.n_experts > kLaneExperts || a.top > 8) route_select_kernel<EL, false><<<(unsigned)a.blocks, kRouteThreads, 0, stream>>>(a);
+  else if (a.top > 4) route_lanes_launch<8>(a, stream);
+  else if (a.top > 2) route_lanes_launch<4>(a, stream);
+  else route_lanes_launch<2>(a, stream);
+  route_place_kernel<<<(unsigned)a.blocks, kRouteThreads, 0, stream>>>(a);
 }
 
 hipError_t launch_moe_route(const void* logits, int dtype, int64_t rows, int n_experts, int64_t ld, int top,

@@ -44,22 +44,16 @@ struct GroupedArgs {
 };
 
 template <int AF>
-static void grouped_few(const GroupedArgs& p, const GroupTiling& t, int y_dtype, hipStream_t stream) {
-  const int64_t most = group_tiles_most(p.M, p.g.n, t.few_rows), cols = tiles_of(p.N, 16 * t.few_tiles);
+static void grouped_few(const GroupedArgs& p, int y_dtype, hipStream_t stream) {
+  const int64_t most = group_tiles_most(p.M, p.g.n, kFewGroupRows), cols = tiles_of(p.N, 16 * kFewGroupTiles);
   // of a launch: the grid's second dimension, and fewer than 2^32 lanes
   const int64_t step = std::min<int64_t>(65535, std::max<int64_t>(1, ((int64_t)1 << 22) / cols));
   Groups g = p.g;
   for (int64_t m = 0; m < most; m += step) {
     g.first_tile = (int)m;
-    const dim3 grid((unsigned)cols, (unsigned)std::min(step, most - m));
-#define AWQ_FEW(AR, NT, ST, OCC)                                                                               \
-  mx_few_kernel<AF, AR, NT, ST, OCC, Groups><<<grid, kFewWaves * kWave, 0, stream>>>(p.A, p.as, p.M, p.W, p.ws, p.N, \
-                                                                                     p.K, p.Y, p.ld_y, y_dtype, g)
-    if (t.few_rows == 4) AWQ_FEW(4, 1, 4, 4);
-    else if (t.few_rows == 16 && t.few_tiles == 1) AWQ_FEW(16, 1, 2, 4);
-    else if (t.few_rows == 16) AWQ_FEW(16, 2, 2, 4);
-    else AWQ_FEW(32, 2, 2, 2);
-#undef AWQ_FEW
+    mx_few_kernel<AF, kFewGroupRows, kFewGroupTiles, 2, 4, Groups>
+        <<<dim3((unsigned)cols, (unsigned)std::min(step, most - m)), kFewWaves * kWave, 0, stream>>>(
+            p.A, p.as, p.M, p.W, p.ws, p.N, p.K, p.Y, p.ld_y, y_dtype, g);
   }
 }
 
@@ -67,7 +61,7 @@ template <int AF, int YT>
 static void grouped_launch(const GroupedArgs& p, uint8_t* work, hipStream_t stream) {
   const GroupTiling t = group_tiling(AF, p.M, p.N, p.K, p.g.n);
   if (t.tile == 0) {
-    grouped_few<AF>(p, t, YT, stream);
+    grouped_few<AF>(p, YT, stream);
   } else if (t.tile < kBigTile) {
     const int n_mt = (int)group_tiles_most(p.M, p.g.n, t.tile), n_nt = (int)tiles_of(p.N, t.tile);
     const int nk = (int)((p.K + kMxStage - 1) / kMxStage);
@@ -83,20 +77,17 @@ static void grouped_launch(const GroupedArgs& p, uint8_t* work, hipStream_t stre
     const int kb = (int)(p.K / kMxBlock);
     uint32_t* sc = (uint32_t*)work;
     const StagedGroups sg = {(const int4*)(work + w.tab), (const uint32_t*)(work + w.offsets)};
-    stage_groups_kernel<SB><<<dim3((unsigned)(w.rows / 256), (unsigned)((kb + 15) / 16)), 256, 0, stream>>>(
+    stage_groups_kernel<SB><<<dim3((unsigned)(w.rows / 256), (unsigned)((kb + 127) / 128)), 256, 0, stream>>>(
         p.g, p.as, (int)p.M, (uint32_t)(AF == kMxFp8 ? p.K : p.K / 2), p.ws, p.N, w.n_pad, kb, w.n_mt, w.rows, sc,
         (int4*)(work + w.tab), (uint32_t*)(work + w.offsets));
-    const int tiles = w.n_mt * w.n_nt;
     if constexpr (AF == kMxFp8) {
-      const unsigned blocks = (unsigned)std::min(tiles, 256);
-      if (p.g.rows != nullptr)
-        mx_big8_kernel<YT, Groups, true><<<blocks, 512, 0, stream>>>(p.A, p.M, p.W, p.N, p.K, sc, w.m_pad, w.rows, w.n_mt,
-                                                                     w.n_nt, 4, p.Y, p.ld_y, p.g, sg);
-      else
-        mx_big8_kernel<YT, Groups, false><<<blocks, 512, 0, stream>>>(p.A, p.M, p.W, p.N, p.K, sc, w.m_pad, w.rows, w.n_mt,
-                                                                      w.n_nt, 4, p.Y, p.ld_y, p.g, sg);
+#define AWQ_BIG8(GATHER)                                                                                             \
+  mx_big8_kernel<YT, Groups, GATHER><<<256, 512, 0, stream>>>(p.A, p.M, p.W, p.N, p.K, sc, w.m_pad, w.rows, w.n_mt, w.n_nt, \
+                                                              4, p.Y, p.ld_y, p.g, sg)
+      if (p.g.rows != nullptr) AWQ_BIG8(true); else AWQ_BIG8(false);
+#undef AWQ_BIG8
     } else {
-      mx_big_kernel<YT, Groups><<<(unsigned)tiles, 512, 0, stream>>>(p.A, p.M, p.W, p.N, p.K, sc, w.m_pad, w.rows, w.n_mt,
+      mx_big_kernel<YT, Groups><<<(unsigned)(w.n_mt * w.n_nt + 2 * kMxXcds), 512, 0, stream>>>(p.A, p.M, p.W, p.N, p.K, sc, w.m_pad, w.rows, w.n_mt,
                                                                      w.n_nt, 4, p.Y, p.ld_y, p.g, sg);
     }
   }

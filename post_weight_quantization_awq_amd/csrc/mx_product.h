@@ -773,25 +773,6 @@ struct StagedGroups {
   const uint32_t* a_at;
 };
 
-// 16 scale bytes of a row, from stage s0 on, as stage_scales_kernel lays them out
-template <int SB>
-__device__ __forceinline__ void stage_words(const uint8_t* p, bool live, int s0, int kb, uint32_t (&v)[4]) {
-  v[0] = v[1] = v[2] = v[3] = 0;
-  if (live) {
-    if ((s0 + 16 / SB) * SB <= kb) {
-      const uint4 u = ld_any<uint4>(p + s0 * SB);
-      v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int b0 = (s0 + i / SB) * SB;                          // the stage's first block
-        const int b = (b0 + SB <= kb ? b0 : kb - SB) + i % SB;      // the byte's
-        if (b0 < kb && b >= b0) v[i / 4] |= (uint32_t)p[b] << (8 * (i % 4));
-      }
-    }
-  }
-}
-
 // out[w][row] (rows: the A rows, then the W rows, each padded to whole tiles): word w of the row's scale bytes,
 // SB / 4 words a stage.  A last stage that K does not fill holds the row's last SB blocks, 0 in the place of
 // those of earlier stages; padded rows hold 0.
@@ -805,59 +786,135 @@ __global__ __launch_bounds__(256) void stage_scales_kernel(const uint8_t* __rest
   const bool live = r < (is_a ? M : N);
   const uint8_t* p = (is_a ? as : ws) + (live ? r : 0) * kb;
   const int s0 = (int)blockIdx.y * (16 / SB), n_stage = (kb + SB - 1) / SB;  // 16 blocks a thread
-  uint32_t v[4];
-  stage_words<SB>(p, live, s0, kb, v);
+  uint32_t v[4] = {0, 0, 0, 0};
+  if (live) {
+    if ((s0 + 16 / SB) * SB <= kb) {
+      const uint4 u = ld_any<uint4>(p + s0 * SB);
+      v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int b0 = (s0 + i / SB) * SB;                          // the stage's first block
+        const int b = (b0 + SB <= kb ? b0 : kb - SB) + i % SB;      // the byte's
+        if (b0 < kb && b >= b0) v[i / 4] |= (uint32_t)p[b] << (8 * (i % 4));
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (s0 + i * 4 / SB < n_stage) out[(int64_t)(s0 * (SB / 4) + i) * rows + row] = v[i];
 }
 
+// Tile t of all groups' 256-row tiles, its place among them with those of more than 128 rows first, and the numbers of
+// both kinds.  Every lane of a wave takes part.
+struct GroupPlace {
+  GroupTile tile;
+  int place, full, half;
+};
+__device__ __forceinline__ GroupPlace group_place(const Groups& g, int M, int t) {
+  GroupPlace p = {{-1, 0, 0}, 0, 0, 0};
+  int tiles = 0, half = 0;  // of the groups before
+  bool is_half = false;
+  for (int e0 = 0; e0 < g.n; e0 += kWave) {
+    const GroupSpan s = group_span(g, M, kBigTile, e0);
+    const int last = (s.end - s.first) % kBigTile;
+    const uint64_t halves = __ballot(last > 0 && last <= kHalfTile);  // groups whose last tile is half a one
+    const int total = span_total(s);
+    if (t >= tiles && t < tiles + total) {
+      p.tile = span_tile(s, e0, kBigTile, t - tiles);
+      const int l = p.tile.group - e0, before = half + __popcll(halves & ((1ull << l) - 1));
+      is_half = p.tile.end - p.tile.first <= kHalfTile;
+      p.place = is_half ? before : t - before;
+    }
+    tiles += total;
+    half += __popcll(halves);
+  }
+  p.full = tiles - half;
+  p.half = half;
+  if (is_half) p.place += p.full;
+  return p;
+}
+
 // The same for groups, with the rows of each group's tiles one after another (n_mt tiles at least) and the padded rows
-// of every group's weight behind them; rows of no tile and of groups without rows are not written.  tab[t]: tile t's
-// group, first row and end; tab[n_mt].x: the number of tiles.  a_at[row]: offset of the row's codes in A.
+// of every group's weight behind them; rows of no tile and of groups without rows are not written.  tab[place]: a
+// tile's group, first row, end and scale rows; tab[n_mt]: the numbers of full and of half tiles.  a_at[row]: offset of
+// the row's codes in A.
 template <int SB>
 __global__ __launch_bounds__(256) void stage_groups_kernel(const Groups g, const uint8_t* __restrict__ as, int M,
                                                            uint32_t a_row, const uint8_t* __restrict__ ws, int64_t N,
                                                            int64_t n_pad, int kb, int n_mt, int64_t rows,
                                                            uint32_t* __restrict__ out, int4* __restrict__ tab,
                                                            uint32_t* __restrict__ a_at) {
-  const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;  // whole tiles
+  // a block takes 128 bytes of 256 rows through LDS, so that both sides are read and written in whole lines (32 x 4096
+  // x 128 bytes of weight scales: 25 us by threads that each take 16 bytes of a row, 12 us so)
+  constexpr int CB = 128, LS = CB + 4;
+  __shared__ __attribute__((aligned(16))) uint8_t bytes[256 * LS];
+  __shared__ int64_t from[256];
+  const int tid = (int)threadIdx.x;
+  const int64_t row = (int64_t)blockIdx.x * 256 + tid;  // whole tiles
   const uint8_t* p;
-  bool live;
   if ((int)blockIdx.x < n_mt) {
-    const GroupTile t = group_tile(g, M, kBigTile, (int)blockIdx.x);
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
-      const GroupTile all = group_pick(g, M, kBigTile, [&](int total) {
-        if (threadIdx.x == 0) tab[n_mt].x = total;
-        return -1;
-      });
-      (void)all;
-    }
+    const GroupPlace at = group_place(g, M, (int)blockIdx.x);
+    const GroupTile& t = at.tile;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) tab[n_mt] = make_int4(at.full, at.half, 0, 0);
     if (t.group < 0) return;
-    const int m = t.first + (int)threadIdx.x;
+    const int m = t.first + tid;
     const int64_t of = m < t.end ? group_row(g, m) : -1;
-    live = of >= 0;
-    p = as + (live ? of : 0) * kb;
+    from[tid] = of;
+    p = as;
     if (blockIdx.y == 0) {
-      if (threadIdx.x == 0) tab[blockIdx.x] = make_int4(t.group, t.first, t.end, 0);
+      if (tid == 0) tab[at.place] = make_int4(t.group, t.first, t.end, (int)blockIdx.x * kBigTile);
       // the rows of each 32 in the order in which 8 lanes take every 8th of them
-      const int i = (int)threadIdx.x, place = (i & ~31) | (i & 7) << 2 | (i >> 3 & 3);
-      if (g.rows != nullptr) a_at[row - (int)threadIdx.x + place] = live ? (uint32_t)of * a_row : kMxOut;
+      const int place = (tid & ~31) | (tid & 7) << 2 | (tid >> 3 & 3);
+      if (g.rows != nullptr) a_at[row - tid + place] = of >= 0 ? (uint32_t)of * a_row : kMxOut;
     }
   } else {
     const int64_t r = row - (int64_t)n_mt * kBigTile;
     const int e = (int)(r / n_pad);  // the same for the block
     const int first = clamp_int(g.offsets[e], 0, M);
     if (g.offsets[e + 1] <= first || first == M) return;
-    live = r - e * n_pad < N;
-    p = ws + (live ? e * N + (r - e * n_pad) : 0) * kb;
+    from[tid] = r - e * n_pad < N ? e * N + (r - e * n_pad) : -1;
+    p = ws;
   }
-  const int s0 = (int)blockIdx.y * (16 / SB), n_stage = (kb + SB - 1) / SB;  // 16 blocks a thread
-  uint32_t v[4];
-  stage_words<SB>(p, live, s0, kb, v);
+  __syncthreads();
+  const int c0 = (int)blockIdx.y * CB;  // the first byte of each row
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (s0 + i * 4 / SB < n_stage) out[(int64_t)(s0 * (SB / 4) + i) * rows + row] = v[i];
+  for (int i = 0; i < 8; ++i) {
+    const int r = tid / 8 + 32 * i, c = 16 * (tid % 8);
+    uint32_t v[4] = {0, 0, 0, 0};
+    if (from[r] >= 0) {
+      const uint8_t* at = p + from[r] * kb + c0 + c;
+      if (c0 + c + 16 <= kb) {
+        const uint4 u = ld_any<uint4>(at);
+        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+      } else {
+#pragma unroll
+        for (int b = 0; b < 16; ++b)
+          if (c0 + c + b < kb) v[b / 4] |= (uint32_t)at[b] << (8 * (b % 4));
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < 4; ++d) *(uint32_t*)(bytes + r * LS + c + 4 * d) = v[d];
+  }
+  __syncthreads();
+  const uint8_t* mine = bytes + tid * LS;
+  const int words = (kb + SB - 1) / SB * (SB / 4);
+#pragma unroll 4
+  for (int d = 0; d < CB / 4; ++d) {
+    const int w = c0 / 4 + d, b0 = w * 4 / SB * SB;  // the word, its stage's first block
+    if (w >= words) break;
+    uint32_t v = 0;
+    if (b0 + SB <= kb) {
+      v = *(const uint32_t*)(mine + 4 * d);
+    } else {  // the row's last SB blocks, 0 in the place of those of earlier stages
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = kb - SB + (4 * w - b0) + i;
+        if (b >= b0) v |= (uint32_t)mine[b - c0] << (8 * i);
+      }
+    }
+    out[(int64_t)w * rows + row] = v;
+  }
 }
 
 template <int YT, class X = NoExtra>
@@ -879,19 +936,21 @@ __global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restric
 
   int mt, nt;
   if constexpr (X::kGroups) {
-    const int tiles = sg.tab[n_mt].x * n_nt;
-    if ((int)blockIdx.x >= tiles) return;
-    block_tile((int)blockIdx.x, tiles, tiles / n_nt, n_nt, group_m, &mt, &nt);
+    const int4 n = sg.tab[n_mt];
+    const int xcd = (int)blockIdx.x % kMxXcds, pos = (int)blockIdx.x / kMxXcds;
+    if (pos >= group_tiles_of_xcd(xcd, n.x, n.y, n_nt)) return;
+    group_tile_at(xcd, pos, n.x, n.y, n_nt, group_m, &mt, &nt);
   } else {
     block_tile((int)blockIdx.x, (int)gridDim.x, n_mt, n_nt, group_m, &mt, &nt);
   }
   int64_t m0 = (int64_t)mt * T;
-  const int64_t n0 = (int64_t)nt * T, sc_m = m0;
-  int64_t sc_n = m_pad + n0;  // the tile's scale rows
+  const int64_t n0 = (int64_t)nt * T;
+  int64_t sc_m = m0, sc_n = m_pad + n0;  // the tile's scale rows
   if constexpr (X::kGroups) {
     const int4 g = sg.tab[mt];
     m0 = g.y;
     M = g.z;
+    sc_m = g.w;
     W += (int64_t)g.x * N * (K / 2);
     sc_n += g.x * ((int64_t)n_nt * T);
   }
@@ -1006,8 +1065,16 @@ __global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restric
   products(F, c0, S);                    \
   interleave<NR, 0>();                   \
   __builtin_amdgcn_sched_barrier(0);
+  // waves without rows only load
+  constexpr bool kParts = X::kGroups;
+  const bool active = !kParts || m0 + wm * MT * 32 < M;
 #define AWQ_MX_STAGE(C, X)                               \
-  {                                                      \
+  if (kParts && !active) {                               \
+    wait_loads<0>();                                     \
+    block_barrier();                                     \
+    load_stage(C, kt + 2);                               \
+    ++kt;                                                \
+  } else {                                               \
     own_bytes(c0, c1);                                   \
     AWQ_MX_STEP(f0, f1, C, 0)                            \
     AWQ_MX_STEP(f1, f0, C, 1)                            \
@@ -1028,7 +1095,9 @@ __global__ __launch_bounds__(512, 2) void mx_big_kernel(const uint8_t* __restric
     AWQ_MX_STAGE(s0, s1)
     AWQ_MX_STAGE(s1, s0)
   }
-  if (kt < nk) AWQ_MX_STAGE(s0, s1)
+  if (kt < nk) {
+    AWQ_MX_STAGE(s0, s1)
+  }
 #undef AWQ_MX_STAGE
 #undef AWQ_MX_STEP
   wait_loads<0>();  // none may land after the block has given its LDS back
@@ -1098,10 +1167,16 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int nk = (int)((K + kMxStage - 1) / kMxStage);
-  int tiles = n_mt * n_nt;
+  // the block's tiles: every `step`th of `tiles` from tile on; groups: of its XCD's
+  int tile = (int)blockIdx.x, step = (int)gridDim.x, tiles = n_mt * n_nt;
+  int n_full = 0, n_half = 0;
+  const int xcd = (int)blockIdx.x % kMxXcds;
   if constexpr (X::kGroups) {
-    tiles = sg.tab[n_mt].x * n_nt;
-    if ((int)blockIdx.x >= tiles) return;
+    const int4 n = sg.tab[n_mt];
+    n_full = n.x, n_half = n.y;
+    tiles = group_tiles_of_xcd(xcd, n_full, n_half, n_nt);
+    tile = (int)blockIdx.x / kMxXcds, step = (int)gridDim.x / kMxXcds;
+    if (tile >= tiles) return;
   }
   const uint32_t a_row = (uint32_t)K, w_row = (uint32_t)(K / 2);
 
@@ -1125,15 +1200,15 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
     if constexpr (X::kGroups) {
       int mt, nt;
       const bool some = id < tiles;
-      block_tile(some ? id : 0, tiles, tiles / n_nt, n_nt, group_m, &mt, &nt);
+      group_tile_at(xcd, some ? id : 0, n_full, n_half, n_nt, group_m, &mt, &nt);
       const int4 g = sg.tab[mt];
-      return Place{some ? g.y : g.z, some ? nt * T : (int)N, g.z, g.x, mt * T};
+      return Place{some ? g.y : g.z, some ? nt * T : (int)N, g.z, g.x, g.w};
     } else {
       const TileAt t = big_tile_at(id, n_mt, n_nt, group_m, (int)M, (int)N);
       return Place{t.m0, t.n0, (int)M, 0, t.m0};
     }
   };
-  Place now = tile_at((int)blockIdx.x), then = tile_at((int)(blockIdx.x + gridDim.x));  // computed, computed next
+  Place now = tile_at(tile), then = tile_at(tile + step);  // computed, computed next
   Place src = now;  // loaded
   int l_k = 0;     // and its stage that is loaded next
   // GATHER: the offsets of a tile's rows, 32 of each wave, come with the stage that is computed when they are needed,
@@ -1236,6 +1311,10 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
 
   auto offsets = [&](const uint8_t* slot) { return (const void*)(slot + oO + 256 * wave + 16 * (lane / 8)); };
   const void* first = GATHER ? (const void*)(sg.a_at + now.sc + 32 * wave + 4 * (lane / 8)) : nullptr;
+  // waves without rows only load
+  constexpr bool kParts = X::kGroups;
+  auto has_rows = [&]() { return !X::kGroups || now.m0 + wm * MT * 32 < now.end; };
+  bool active = has_rows();
   Frags f0, f1;
   Scales c0, c1;
   clear();
@@ -1244,7 +1323,12 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
   // Before the barrier every wave has read the rest of C (lgkmcnt 0), so that it may be filled again, and X has
   // landed: only the loads into F are younger.
 #define AWQ_MX_STAGE(C, X, F)            \
-  {                                      \
+  if (kParts && !active) {               \
+    load_stage(F, offsets(C));           \
+    wait_loads<ND>();                    \
+    block_barrier();                     \
+    ++kt;                                \
+  } else {                               \
     own_bytes(c0, c1);                   \
     read_frags(f1, C, 1);                \
     load_stage(F, offsets(C));           \
@@ -1273,11 +1357,12 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
     store_tile<YT, MT, NT, NW, SB, 1, true>(acc, C, C, C, wave, own, ym, yn, ye, N, Y, ld_y);              \
   else                                                                                                     \
     store_tile<YT, MT, NT, NW, SB, 1>(acc, C, C, C, wave, own, ym, yn, ye, N, Y, ld_y);                    \
-  tile += (int)gridDim.x;
+  tile += step;
 #define AWQ_MX_NEXT(X)                   \
   kt = 0;                                \
   now = then;                            \
-  then = tile_at(tile + (int)gridDim.x); \
+  then = tile_at(tile + step);           \
+  active = has_rows();                   \
   clear();                               \
   wait_lds();                            \
   block_barrier();                       \
@@ -1292,8 +1377,7 @@ __global__ __launch_bounds__(512, 2) void mx_big8_kernel(const uint8_t* __restri
   read_frags(f0, C, 0);
 
   // The block's last stage is to be the third of the loop, its only way out: the stages over are done ahead
-  int tile = (int)blockIdx.x;
-  const int over = (int)((int64_t)((tiles - 1 - tile) / (int)gridDim.x + 1) * nk % 3);
+  const int over = (int)((int64_t)((tiles - 1 - tile) / step + 1) * nk % 3);
   if (over == 0) {
     AWQ_MX_START(s0, s1)
   } else if (over == 1) {

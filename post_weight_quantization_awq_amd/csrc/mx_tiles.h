@@ -51,6 +51,30 @@ __host__ __device__ __forceinline__ StageSpan stage_span(int first, int rows, ui
   return StageSpan{(uint32_t)(left < kBigTile ? left : kBigTile) * row_bytes, left <= 0 ? 0 : off < last ? off : last};
 }
 
+// Tiles of 256 rows in groups: n_full with more than 128 rows, then n_half with fewer, which take half the time.  Each
+// XCD has an equal share of both, the full ones first, and of each a contiguous range, walked in groups of group_m
+// tiles of rows.
+constexpr int kHalfTile = kBigTile / 2;
+__host__ __device__ __forceinline__ int xcd_share(int n, int i) { return n / kMxXcds + (i < n % kMxXcds ? 1 : 0); }
+__host__ __device__ __forceinline__ int xcd_first(int n, int i) {
+  return i * (n / kMxXcds) + (i < n % kMxXcds ? i : n % kMxXcds);
+}
+__host__ __device__ __forceinline__ int group_tiles_of_xcd(int xcd, int n_full, int n_half, int n_nt) {
+  return xcd_share(n_full * n_nt, xcd) + xcd_share(n_half * n_nt, kMxXcds - 1 - xcd);
+}
+// The XCD's tile `pos`: its place among the tiles of rows, and among those of outputs
+__host__ __device__ __forceinline__ void group_tile_at(int xcd, int pos, int n_full, int n_half, int n_nt, int group_m,
+                                                       int* mt, int* nt) {
+  const int full = xcd_share(n_full * n_nt, xcd);
+  const bool half = pos >= full;
+  const int n_mt = half ? n_half : n_full;
+  const int id = half ? xcd_first(n_half * n_nt, kMxXcds - 1 - xcd) + pos - full : xcd_first(n_full * n_nt, xcd) + pos;
+  const int per_group = group_m * n_nt, first_m = id / per_group * group_m;
+  const int gsz = n_mt - first_m < group_m ? n_mt - first_m : group_m;
+  *mt = (half ? n_full : 0) + first_m + id % per_group % gsz;
+  *nt = id % per_group / gsz;
+}
+
 constexpr int kMaxRanges = 8;
 inline int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
 
@@ -154,30 +178,40 @@ inline int64_t group_tiles_most(int64_t M, int n_groups, int tile) {
   return (M + used * (tile - 1)) / tile;
 }
 
-// The kernel and its tile, for even shares of the rows: the ones with the least estimated time.
+// The tile, for shares of the rows that are about even: the one with the least estimated time.  Few rows: blocks of 16
+// rows x 32 outputs.  The estimates (us) are fitted to measurements of 8 to 128 groups, N and K of 1000 to 4096, at
+// 0.1 to 512 rows a group; the tile that they choose is 2% slower than the best one in the mean.  E.g. (8 bits; few
+// rows / tiles of 64 / 128 / 256) 64 groups of 4096 x 4096, 1 row each: 65 / 71 / - / -; 16: 169 / 152 / 140 / -; 96:
+// - / 321 / 195 / 190; 256: - / 578 / 372 / 311; 64 groups of 4096 x 2048, 1 row each: 41 / 32 / - / -; 10 groups of
+// 1000 x 2080, 4 rows each: 4.8 / 6.5 / - / -.
+constexpr int kFewGroupRows = 16, kFewGroupTiles = 2;
 struct GroupTiling {
-  int tile;                  // 64, 128 or 256; 0: few rows a group,
-  int few_rows, few_tiles;   // then the LDS rows and 16-output tiles of a block
+  int tile;  // 64, 128 or 256; 0: few rows a group
 };
 inline GroupTiling group_tiling(int a_fmt, int64_t M, int64_t N, int64_t K, int n_groups) {
-  const double used = (double)(M < n_groups ? M : n_groups), each = (double)M / used;
-  const int rows = each <= 3 ? 4 : each <= 20 ? 16 : 32;
-  const double w_mb = used * (double)N * (double)K * (17.0 / 32) * 1e-6;
-  const double a_mb = (double)M * (double)K * (a_fmt == kMxFp8 ? 1.0 : 0.5) * 1e-6;
-  const double few_mt = used * ceil(each / rows);
-  GroupTiling best = {0, rows, rows == 4 || (N + 15) / 16 * few_mt <= 256 ? 1 : 2};
-  if (rows == 32) best.few_tiles = 2;
-  if (K < 3 * kMxStage) return best;
-  const double a_cost = rows == 4 ? 0.0 : rows == 16 ? 0.02 : a_fmt == kMxFp8 ? 0.05 : 0.035;
-  double least = each <= 64 ? 2 + w_mb / 5 + (ceil(each / rows) - 1) * w_mb / 10 +
-                                  a_cost * (double)N / (16 * best.few_tiles) * a_mb
-                            : HUGE_VAL;
-  const int nk = (int)((K + kMxStage - 1) / kMxStage);
-  for (int tile = 64; tile <= 256; tile *= 2) {
+  if (K < 3 * kMxStage) return {0};  // as in mx_tiling
+  // groups that have rows, and their tiles of rows: half a one more than full ones hold, unless one holds most shares
+  const double used = n_groups * (1 - pow(1 - 1.0 / n_groups, (double)M)), each = (double)M / used;
+  auto row_tiles = [&](double rows) { return used * (each < 0.4 * rows ? 1 : each / rows + 0.6); };
+  const double nk = (double)((K + kMxStage - 1) / kMxStage), w_mb = used * (double)N * (double)K * (17.0 / 32) * 1e-6;
+  const bool fp8 = a_fmt == kMxFp8;
+  const double few_mt = row_tiles(kFewGroupRows), few_nt = (double)tiles_of(N, 16 * kFewGroupTiles);
+  GroupTiling best = {0};
+  double least = 2.4 + w_mb / 8 + (few_mt > used ? few_mt - used : 0) * few_nt * nk * (fp8 ? 2.1e-4 : 1.8e-4) +
+                 few_mt * few_nt * 3.5e-3;
+  // for each stage `one` while no compute unit has more than a few blocks, else `full` for a block of each of the 256
+  struct Cost {
+    double base, ends, one, full;
+  };
+  static const Cost cost[2][3] = {{{3.3, 0, 0.20, 0.244}, {3.4, 2.7, 0.337, 0.467}, {11.5, 0, 0.79, 1.37}},
+                                  {{3.3, -1.7, 0.185, 0.233}, {3.3, 2.3, 0.263, 0.426}, {9, -1.1, 0.69, 1.37}}};
+  for (int tile = 64; tile <= kBigTile; tile *= 2) {
     const double n_nt = (double)((N + tile - 1) / tile);
     if (tile == kBigTile && K <= 3 * kMxStage) continue;  // the persistent blocks look two stages ahead within a tile
     if ((double)group_tiles_most(M, n_groups, tile) * n_nt > (1 << 22)) continue;  // a launch holds fewer than 2^32 lanes
-    const double t = tile_time(a_fmt, tile, used * ceil(each / tile) * n_nt, nk);
+    const Cost& c = cost[fp8 ? 0 : 1][tile == 64 ? 0 : tile == 128 ? 1 : 2];
+    const double load = row_tiles(tile) * n_nt / 256;
+    const double t = c.base + (nk + c.ends) * (c.one > c.full * load ? c.one : c.full * load);
     if (t < least) least = t, best.tile = tile;
   }
   return best;

@@ -55,7 +55,32 @@ SOURCE = r"""
 using namespace awq;
 extern "C" void grouped(int fmt, int64_t M, int64_t N, int64_t K, int groups, int* out) {
   const GroupTiling t = group_tiling(fmt, M, N, K, groups);
-  out[0] = t.tile, out[1] = t.few_rows, out[2] = t.few_tiles;
+  out[0] = t.tile, out[1] = kFewGroupRows, out[2] = kFewGroupTiles;
+}
+// How often each tile of 256 rows x outputs is some XCD's; -1: a place out of range, a full tile behind a half one, or
+// shares of full or half tiles that differ by more than one
+extern "C" int walk(int n_full, int n_half, int n_nt, int* visits) {
+  const int n_mt = n_full + n_half;
+  int least[2] = {1 << 30, 1 << 30}, most[2] = {0, 0};
+  for (int i = 0; i < n_mt * n_nt; ++i) visits[i] = 0;
+  for (int x = 0; x < kMxXcds; ++x) {
+    const int n = group_tiles_of_xcd(x, n_full, n_half, n_nt);
+    int kind[2] = {0, 0};
+    for (int pos = 0; pos < n; ++pos) {
+      int mt, nt;
+      group_tile_at(x, pos, n_full, n_half, n_nt, 4, &mt, &nt);
+      if (mt < 0 || mt >= n_mt || nt < 0 || nt >= n_nt) return -1;
+      const int half = mt >= n_full;
+      if (!half && kind[1]) return -1;
+      ++kind[half];
+      ++visits[mt * n_nt + nt];
+    }
+    for (int k = 0; k < 2; ++k) {
+      least[k] = kind[k] < least[k] ? kind[k] : least[k];
+      most[k] = kind[k] > most[k] ? kind[k] : most[k];
+    }
+  }
+  return most[0] - least[0] > 1 || most[1] - least[1] > 1 ? -1 : 0;
 }
 extern "C" int64_t most(int64_t M, int groups, int tile) { return group_tiles_most(M, groups, tile); }
 """
@@ -88,8 +113,7 @@ def test_grouped_forms(tiles, M, E, N, K, fmt, form):
 
 def test_grouped_forms_are_all_reached():
     for fmt in ("fp8", "fp4"):
-        assert {f for *_, g, f in GROUPED if g == fmt} == {"few 4 x 1", "few 16 x 1", "few 16 x 2", "few 32 x 2", "64",
-                                                           "128", "256"}
+        assert {f for *_, g, f in GROUPED if g == fmt} == {"few 16 x 2", "64", "128", "256"}
 
 
 def test_grouped_tiles_are_enough(tiles):
@@ -105,6 +129,17 @@ def test_grouped_tiles_are_enough(tiles):
         most = tiles.most(ctypes.c_int64(M), E, tile)
         assert (-(-counts // tile)).sum() <= most
     assert tiles.most(ctypes.c_int64(100), 1, 64) == 2 and tiles.most(ctypes.c_int64(3), 8, 64) == 3
+
+
+def test_grouped_walk(tiles):
+    """Every tile of the largest kind is computed once, and the XCDs' shares of full and half tiles are equal."""
+    rng = np.random.default_rng(1)
+    cases = [(0, 1, 1), (1, 0, 1), (3, 5, 1), (0, 9, 7), (47, 34, 16), (1000, 3, 33)]
+    cases += [(int(rng.integers(0, 60)), int(rng.integers(1, 60)), int(rng.integers(1, 40))) for _ in range(200)]
+    for full, half, nt in cases:
+        visits = (ctypes.c_int * ((full + half) * nt))()
+        assert tiles.walk(full, half, nt, visits) == 0, (full, half, nt)
+        assert all(v == 1 for v in visits), (full, half, nt)
 
 
 # ---- the C ABI's refusals ---------------------------------------------------
