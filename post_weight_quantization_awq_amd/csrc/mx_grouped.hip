@@ -63,13 +63,15 @@ static void grouped_launch(const GroupedArgs& p, uint8_t* work, hipStream_t stre
   if (t.tile == 0) {
     grouped_few<AF>(p, YT, stream);
   } else if (t.tile < kBigTile) {
-    const int n_mt = (int)group_tiles_most(p.M, p.g.n, t.tile), n_nt = (int)tiles_of(p.N, t.tile);
+    const int n_mt = (int)group_tiles_most(p.M, p.g.n, t.tile), n_nt = (int)tiles_of(p.N, group_tile_outs(t.tile));
     const int nk = (int)((p.K + kMxStage - 1) / kMxStage);
-#define AWQ_TILE(BM, NS, OCC)                                                                              \
-  mx_tile_kernel<AF, YT, BM, BM, 2, 2, NS, OCC, Groups><<<(unsigned)(n_mt * n_nt), 4 * kWave, 0, stream>>>( \
+#define AWQ_TILE(BM, BN, WM, WN, NS, OCC)                                                                            \
+  mx_tile_kernel<AF, YT, BM, BN, WM, WN, NS, OCC, Groups><<<(unsigned)(n_mt * n_nt), WM * WN * kWave, 0, stream>>>( \
       p.A, p.as, p.M, p.W, p.ws, p.N, p.K, n_mt, n_nt, 4, nk, p.Y, p.ld_y, p.g)
-    if (t.tile == 64) AWQ_TILE(64, 3, 4);
-    else AWQ_TILE(128, 3, 2);
+    if (t.tile == 32 && t.slots == 6) AWQ_TILE(32, 128, 1, 2, 6, 1);
+    else if (t.tile == 32) AWQ_TILE(32, 128, 1, 2, 3, 2);
+    else if (t.tile == 64) AWQ_TILE(64, 64, 2, 2, 3, 4);
+    else AWQ_TILE(128, 128, 2, 2, 3, 2);
 #undef AWQ_TILE
   } else if constexpr (AF == kMxFp4 || YT != 2) {
     const GroupedWork w = grouped_work(AF, p.M, p.N, p.K, p.g.n);

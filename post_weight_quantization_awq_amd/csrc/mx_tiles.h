@@ -179,40 +179,46 @@ inline int64_t group_tiles_most(int64_t M, int n_groups, int tile) {
 }
 
 // The tile, for shares of the rows that are about even: the one with the least estimated time.  Few rows: blocks of 16
-// rows x 32 outputs.  The estimates (us) are fitted to measurements of 8 to 128 groups, N and K of 1000 to 4096, at
-// 0.1 to 512 rows a group; the tile that they choose is 2% slower than the best one in the mean.  E.g. (8 bits; few
-// rows / tiles of 64 / 128 / 256) 64 groups of 4096 x 4096, 1 row each: 65 / 71 / - / -; 16: 169 / 152 / 140 / -; 96:
-// - / 321 / 195 / 190; 256: - / 578 / 372 / 311; 64 groups of 4096 x 2048, 1 row each: 41 / 32 / - / -; 10 groups of
-// 1000 x 2080, 4 rows each: 4.8 / 6.5 / - / -.
+// rows x 32 outputs; tiles of 32 rows have 128 outputs, the others as many as rows.  The estimates (us) are fitted to
+// measurements of 8 to 128 groups, N and K of 1000 to 4096, at 0.1 to 512 rows a group, with other weights from run
+// to run; the tile that they choose is 2% slower than the best one in the mean.  E.g. (8 bits; few rows / 32 / 64 / 128 /
+// 256) 64 groups of 4096 x 4096, 1 row each: 76 / 82 / 86 / 92 / -; 8: 129 / 118 / 139 / 132 / -; 32: 251 / 166 / 179 / 153
+// / -; 256: - / - / 578 / 372 / 311; 64 groups of 4096 x 2048, 8 rows each: 81 / 62 / 71 / 71 / -; 10 groups of 1000 x
+// 2080, 4 rows each: 5.8 / 8.3 / 7.7 / 10.2 / -.
 constexpr int kFewGroupRows = 16, kFewGroupTiles = 2;
 struct GroupTiling {
-  int tile;  // 64, 128 or 256; 0: few rows a group
+  int tile;   // 32, 64, 128 or 256; 0: few rows a group
+  int slots;  // of LDS, for tiles of 32 rows: six where there are stages to load ahead
 };
+inline int group_tile_outs(int tile) { return tile == 32 ? 128 : tile; }
 inline GroupTiling group_tiling(int a_fmt, int64_t M, int64_t N, int64_t K, int n_groups) {
-  if (K < 3 * kMxStage) return {0};  // as in mx_tiling
+  const int nk = (int)((K + kMxStage - 1) / kMxStage), slots = nk >= 24 ? 6 : 3;
+  if (K < 3 * kMxStage) return {0, 0};  // as in mx_tiling
   // groups that have rows, and their tiles of rows: half a one more than full ones hold, unless one holds most shares
   const double used = n_groups * (1 - pow(1 - 1.0 / n_groups, (double)M)), each = (double)M / used;
   auto row_tiles = [&](double rows) { return used * (each < 0.4 * rows ? 1 : each / rows + 0.6); };
-  const double nk = (double)((K + kMxStage - 1) / kMxStage), w_mb = used * (double)N * (double)K * (17.0 / 32) * 1e-6;
+  const double w_mb = used * (double)N * (double)K * (17.0 / 32) * 1e-6;
   const bool fp8 = a_fmt == kMxFp8;
   const double few_mt = row_tiles(kFewGroupRows), few_nt = (double)tiles_of(N, 16 * kFewGroupTiles);
-  GroupTiling best = {0};
-  double least = 2.4 + w_mb / 8 + (few_mt > used ? few_mt - used : 0) * few_nt * nk * (fp8 ? 2.1e-4 : 1.8e-4) +
-                 few_mt * few_nt * 3.5e-3;
+  GroupTiling best = {0, 0};
+  double least = 2.8 + w_mb / 7.2 + (few_mt > used ? few_mt - used : 0) * few_nt * nk * (fp8 ? 2.1e-4 : 1.8e-4) +
+                 few_mt * few_nt * 3.4e-3;
   // for each stage `one` while no compute unit has more than a few blocks, else `full` for a block of each of the 256
   struct Cost {
     double base, ends, one, full;
   };
-  static const Cost cost[2][3] = {{{3.3, 0, 0.20, 0.244}, {3.4, 2.7, 0.337, 0.467}, {11.5, 0, 0.79, 1.37}},
-                                  {{3.3, -1.7, 0.185, 0.233}, {3.3, 2.3, 0.263, 0.426}, {9, -1.1, 0.69, 1.37}}};
-  for (int tile = 64; tile <= kBigTile; tile *= 2) {
-    const double n_nt = (double)((N + tile - 1) / tile);
+  static const Cost cost[2][4] = {
+      {{3.3, 0.5, 0.259, 0.429}, {3.2, 0, 0.249, 0.254}, {3.4, 2.7, 0.349, 0.487}, {10.1, 0.5, 1.05, 1.46}},
+      {{3.1, 1, 0.239, 0.414}, {3.1, -1.1, 0.247, 0.245}, {2.8, 2.9, 0.303, 0.437}, {8.3, 0, 0.79, 1.36}}};
+  for (int i = 0; i < 4; ++i) {
+    const int tile = 32 << i;
+    const double n_nt = (double)tiles_of(N, group_tile_outs(tile));
     if (tile == kBigTile && K <= 3 * kMxStage) continue;  // the persistent blocks look two stages ahead within a tile
     if ((double)group_tiles_most(M, n_groups, tile) * n_nt > (1 << 22)) continue;  // a launch holds fewer than 2^32 lanes
-    const Cost& c = cost[fp8 ? 0 : 1][tile == 64 ? 0 : tile == 128 ? 1 : 2];
+    const Cost& c = cost[fp8 ? 0 : 1][i];
     const double load = row_tiles(tile) * n_nt / 256;
     const double t = c.base + (nk + c.ends) * (c.one > c.full * load ? c.one : c.full * load);
-    if (t < least) least = t, best.tile = tile;
+    if (t < least) least = t, best = {tile, slots};
   }
   return best;
 }

@@ -55,7 +55,7 @@ SOURCE = r"""
 using namespace awq;
 extern "C" void grouped(int fmt, int64_t M, int64_t N, int64_t K, int groups, int* out) {
   const GroupTiling t = group_tiling(fmt, M, N, K, groups);
-  out[0] = t.tile, out[1] = kFewGroupRows, out[2] = kFewGroupTiles;
+  out[0] = t.tile, out[1] = kFewGroupRows, out[2] = t.tile ? t.slots : kFewGroupTiles;
 }
 // How often each tile of 256 rows x outputs is some XCD's; -1: a place out of range, a full tile behind a half one, or
 // shares of full or half tiles that differ by more than one
@@ -103,7 +103,7 @@ def tiles(tmp_path_factory):
 def form_of(tiles, M, E, N, K, fmt):
     out = (ctypes.c_int * 3)()
     tiles.grouped(0 if fmt == "fp8" else 1, ctypes.c_int64(M), ctypes.c_int64(N), ctypes.c_int64(K), E, out)
-    return f"few {out[1]} x {out[2]}" if out[0] == 0 else str(out[0])
+    return f"few {out[1]} x {out[2]}" if out[0] == 0 else f"32, {out[2]} slots" if out[0] == 32 else str(out[0])
 
 
 @pytest.mark.parametrize("M,E,N,K,fmt,form", GROUPED)
@@ -113,7 +113,7 @@ def test_grouped_forms(tiles, M, E, N, K, fmt, form):
 
 def test_grouped_forms_are_all_reached():
     for fmt in ("fp8", "fp4"):
-        assert {f for *_, g, f in GROUPED if g == fmt} == {"few 16 x 2", "64", "128", "256"}
+        assert {f for *_, g, f in GROUPED if g == fmt} == {"few 16 x 2", "32, 3 slots", "32, 6 slots", "64", "128", "256"}
 
 
 def test_grouped_tiles_are_enough(tiles):
