@@ -193,98 +193,153 @@ __global__ __launch_bounds__(kRouteThreads) void route_select_kernel(const Route
   }
 }
 
-// More tokens: 4 lanes take a token, each a fourth of its logits, and keep the best K of them in order by insertion
-// (a maximum and a minimum for each place); two merges across the lanes join them.  A logit and its expert are one
-// positive double that orders as they do: 32 bits of key, then the experts from the last to the first.  62 operations
-// a token of 128 experts and 8 places, where a wave for each token takes 300.
+// More tokens: 4 lanes take a token, each a fourth of its logits.  A lane sorts K of them at a time and merges them into
+// its best K, in order; two merges across the lanes join those.  A logit and its expert are one word that orders as
+// they do, so that a comparison is a maximum and a minimum: for 16-bit logits 32 bits, the 19 of the key that such a
+// value can set over the experts from the last to the first; for 32-bit ones a positive double, 32 bits of key over 30.
+// A token of 128 experts and 8 places costs a lane 280 comparisons; a wave for each token takes 300 operations of 64
+// lanes.  A lane's logits are in flight at once, 32 of them.
 constexpr int kLaneThreads = 4 * kRouteChunk, kLaneExperts = 256;
-__device__ __forceinline__ double route_pack(uint32_t key, uint32_t e) {
-  return __builtin_bit_cast(double, (uint64_t)key << 30 | (0x3FFFFFFFu - e));
-}
-__device__ __forceinline__ uint32_t packed_key(double d) { return (uint32_t)(__builtin_bit_cast(uint64_t, d) >> 30); }
-__device__ __forceinline__ int packed_expert(double d) {
-  return (int)(0x3FFFFFFFu - ((uint32_t)__builtin_bit_cast(uint64_t, d) & 0x3FFFFFFFu));
-}
-template <int CTRL>
-__device__ __forceinline__ double dpp_d(double d) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, d);
-  return __builtin_bit_cast(double, (uint64_t)dpp_u<CTRL>((uint32_t)(u >> 32)) << 32 | dpp_u<CTRL>((uint32_t)u));
-}
-__device__ __forceinline__ void order(double& a, double& b) {  // a the larger
-  const double m = __builtin_fmax(a, b);
-  b = __builtin_fmin(a, b);
-  a = m;
-}
-// The best K of the lane's and another lane's lists, in order
-template <int K, int CTRL>
-__device__ __forceinline__ void merge_lists(double (&v)[K]) {
-  double o[K];
+constexpr uint32_t kNoKey = 0x007FFFFFu;  // -inf's: no larger one, no expert
+template <int DT>
+struct RouteWord {
+  using type = uint32_t;
+  static __device__ __forceinline__ type pack(uint32_t key, uint32_t e) { return (key & 0xFFFFE000u) | (0x1FFFu - e); }
+  static __device__ __forceinline__ float value(type w) {
+    return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, route_value(w)) & 0xFFFFE000u);
+  }
+  static __device__ __forceinline__ int expert(type w) { return (int)(0x1FFFu - (w & 0x1FFFu)); }
+  static __device__ __forceinline__ bool some(type w) { return w > kNoKey; }
+  static __device__ __forceinline__ void order(type& a, type& b) {  // a the larger
+    const type m = max(a, b);
+    b = min(a, b);
+    a = m;
+  }
+  static __device__ __forceinline__ type larger(type a, type b) { return max(a, b); }
+  template <int CTRL>
+  static __device__ __forceinline__ type moved(type w) { return dpp_u<CTRL>(w); }
+};
+template <>
+struct RouteWord<2> {
+  using type = double;
+  static __device__ __forceinline__ uint64_t bits(type w) { return __builtin_bit_cast(uint64_t, w); }
+  static __device__ __forceinline__ type pack(uint32_t key, uint32_t e) {
+    return __builtin_bit_cast(double, (uint64_t)key << 30 | (0x3FFFFFFFu - e));
+  }
+  static __device__ __forceinline__ uint32_t key(type w) { return (uint32_t)(bits(w) >> 30); }
+  static __device__ __forceinline__ int expert(type w) { return (int)(0x3FFFFFFFu - ((uint32_t)bits(w) & 0x3FFFFFFFu)); }
+  static __device__ __forceinline__ float value(type w) { return route_value(key(w)); }
+  static __device__ __forceinline__ bool some(type w) { return key(w) > kNoKey; }
+  // No word is a NaN; __builtin_fmax would make sure of it first, with an instruction for each operand
+  static __device__ __forceinline__ type larger(type a, type b) {
+    type m;
+    asm("v_max_f64 %0, %1, %2" : "=v"(m) : "v"(a), "v"(b));
+    return m;
+  }
+  static __device__ __forceinline__ void order(type& a, type& b) {
+    const type m = larger(a, b);
+    asm("v_min_f64 %0, %1, %2" : "=v"(b) : "v"(a), "v"(b));
+    a = m;
+  }
+  template <int CTRL>
+  static __device__ __forceinline__ type moved(type w) {
+    asm("s_nop 1" : "+v"(w));  // the two states from an instruction's result, here an asm's, to its use by another lane
+    return __builtin_bit_cast(double, (uint64_t)dpp_u<CTRL>((uint32_t)(bits(w) >> 32)) << 32 | dpp_u<CTRL>((uint32_t)bits(w)));
+  }
+};
+// K words into descending order: odd-even merge sort
+template <class W, int K>
+__device__ __forceinline__ void sort_words(typename W::type* x) {
 #pragma unroll
-  for (int i = 0; i < K; ++i) o[i] = dpp_d<CTRL>(v[K - 1 - i]);
+  for (int p = 1; p < K; p *= 2)
 #pragma unroll
-  for (int i = 0; i < K; ++i) v[i] = __builtin_fmax(v[i], o[i]);  // falls, then rises, or the other way round
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < K; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < K && (i + j) / (2 * p) == (i + j + k) / (2 * p)) W::order(x[i + j], x[i + j + k]);
+}
+// v: the K largest of v and o, both in descending order
+template <class W, int K>
+__device__ __forceinline__ void merge_words(typename W::type* v, const typename W::type* o) {
+#pragma unroll
+  for (int i = 0; i < K; ++i) v[i] = W::larger(v[i], o[K - 1 - i]);  // falls, then rises, or the other way round
 #pragma unroll
   for (int d = K / 2; d >= 1; d /= 2)
 #pragma unroll
     for (int i = 0; i < K; ++i)
-      if ((i & d) == 0) order(v[i], v[i + d]);
+      if ((i & d) == 0) W::order(v[i], v[i + d]);
+}
+template <class W, int K, int CTRL>
+__device__ __forceinline__ void merge_lanes(typename W::type* v) {
+  typename W::type o[K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) o[i] = W::template moved<CTRL>(v[i]);
+  merge_words<W, K>(v, o);
 }
 
-// The lane's 4 logits of 16 from e on; -inf for those that are not there
+// The lane's 8 logits of 32 from e on; -inf for those that are not there
 template <int DT>
-__device__ __forceinline__ void load_logits4(const RouteArgs& a, int64_t at, int e, float (&f)[4]) {
-  if (e + 4 <= a.n_experts) {
+__device__ __forceinline__ void load_logits8(const RouteArgs& a, int64_t at, int e, float (&f)[8]) {
+  if (e + 8 <= a.n_experts) {
     if constexpr (DT == 2) {
-      *(float4*)f = ld_any<float4>((const float*)a.logits + at + e);
+      *(float4*)&f[0] = ld_any<float4>((const float*)a.logits + at + e);
+      *(float4*)&f[4] = ld_any<float4>((const float*)a.logits + at + e + 4);
     } else {
-      const uint2 u = ld_any<uint2>((const uint16_t*)a.logits + at + e);
-      f[0] = x2f<DT>(u.x & 0xFFFFu), f[1] = x2f<DT>(u.x >> 16), f[2] = x2f<DT>(u.y & 0xFFFFu), f[3] = x2f<DT>(u.y >> 16);
+      unpack8<DT>(ld_any<uint4>((const uint16_t*)a.logits + at + e), f);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = e + i < a.n_experts ? route_logit(a.logits, DT, at + e + i) : -INFINITY;
+    for (int i = 0; i < 8; ++i) f[i] = e + i < a.n_experts ? route_logit(a.logits, DT, at + e + i) : -INFINITY;
   }
+}
+// Ascending with the value; NaN the largest, -0 as +0
+__device__ __forceinline__ uint32_t plain_key(float f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, f + 0.0f), k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return f != f ? 0xFFFFFFFFu : k;
 }
 
 template <int K, int DT>
 __global__ __launch_bounds__(kLaneThreads) void route_lanes_kernel(const RouteArgs a) {
+  using W = RouteWord<DT>;
   __shared__ unsigned long long mask[kLaneExperts];
   const int tid = threadIdx.x, q = tid % 4, tt = tid / 4;
   const int64_t t0 = (int64_t)blockIdx.x * a.per;
   uint32_t count = 0;  // of expert `tid`
   for (int c = 0; c < a.per && t0 + c < a.rows; c += kRouteChunk) {
     mask[tid] = 0;
-    __syncthreads();
     const int64_t t = t0 + c + tt;
     const bool live = t < a.rows;
     const int64_t at = (live ? t : a.rows - 1) * a.ld;
-    double v[K];
+    typename W::type v[K] = {};
+    float sum = 0.0f;
+    for (int e = 8 * q; e < a.n_experts; e += 128) {
+      float f[4][8];
 #pragma unroll
-    for (int i = 0; i < K; ++i) v[i] = 0.0;
-#pragma unroll 2
-    for (int e = 4 * q; e < a.n_experts; e += 16) {
-      float f[4];
-      load_logits4<DT>(a, at, e, f);
+      for (int g = 0; g < 4; ++g) load_logits8<DT>(a, at, e + 32 * g, f[g]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t key = route_key(f[i]);
-        double x = key != 0 ? route_pack(key, (uint32_t)(e + i)) : 0.0;
+      for (int g = 0; g < 4; ++g) {
+        typename W::type x[8];
 #pragma unroll
-        for (int s = 0; s < K; ++s) order(v[s], x);
+        for (int i = 0; i < 8; ++i) x[i] = W::pack(plain_key(f[g][i]), (uint32_t)(e + 32 * g + i));
+#pragma unroll
+        for (int i = 0; i < 8; i += K) {
+          sort_words<W, K>(x + i);
+          merge_words<W, K>(v, x + i);
+        }
       }
     }
-    merge_lists<K, 0xB1>(v);
-    merge_lists<K, 0x4E>(v);
-    const float most = route_value(packed_key(v[0]));
-    float sum = 0.0f;
-    if (!a.renorm && v[0] != 0.0) {
-#pragma unroll 2
-      for (int e = 4 * q; e < a.n_experts; e += 16) {
-        float f[4];
-        load_logits4<DT>(a, at, e, f);
+    merge_lanes<W, K, 0xB1>(v);
+    merge_lanes<W, K, 0x4E>(v);
+    const float most = W::value(v[0]);
+    if (!a.renorm && W::some(v[0])) {
+      for (int e = 8 * q; e < a.n_experts; e += 32) {
+        float f[8];
+        load_logits8<DT>(a, at, e, f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (route_key(f[i]) != 0) sum += expf(f[i] - most);
+        for (int i = 0; i < 8; ++i)
+          if (f[i] != -INFINITY) sum += expf(f[i] - most);
       }
     }
     // the lane's places: q, q + 4
@@ -293,17 +348,18 @@ __global__ __launch_bounds__(kLaneThreads) void route_lanes_kernel(const RouteAr
     float p[PL];
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      double d = 0.0;
+      typename W::type d = 0;
 #pragma unroll
       for (int s = 0; s < 4; ++s)
         if (4 * i + s < K) d = q == s ? v[4 * i + s] : d;
-      const bool some = d != 0.0 && 4 * i + q < a.top;
-      id[i] = some ? packed_expert(d) : -1;
-      p[i] = some ? expf(route_value(packed_key(d)) - most) : 0.0f;
+      const bool some = W::some(d) && 4 * i + q < a.top;
+      id[i] = some ? W::expert(d) : -1;
+      p[i] = some ? expf(W::value(d) - most) : 0.0f;
       if (a.renorm) sum += p[i];
     }
     sum += dpp_m<0xB1>(sum);
     sum += dpp_m<0x4E>(sum);
+    __syncthreads();  // the masks are clear
 #pragma unroll
     for (int i = 0; i < PL; ++i)
       if (live && 4 * i + q < a.top) {
@@ -324,61 +380,87 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(const RouteA
   __shared__ unsigned long long mask[1024];
   __shared__ uint32_t base[1024], total[1024], part[kRouteWaves];
   const int tid = threadIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * a.per;
+  const int slots = kRouteChunk * a.top;
+  int id[2];  // of the chunk's pairs tid and tid + 1024: at most 64 x 32
+  auto pairs_of = [&](int c) { return a.rows - t0 - c < kRouteChunk ? (int)(a.rows - t0 - c) * a.top : slots; };
+  auto load_ids = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int s = tid + kRouteThreads * i;
+      id[i] = s < pairs_of(c) ? a.experts[(t0 + c) * a.top + s] : -1;
+    }
+  };
+  load_ids(0);  // ahead of the counts' sums
   base[tid] = total[tid] = 0;
   mask[tid] = 0;
   __syncthreads();
-  const int lanes = a.ld_counts / 8, step = kRouteThreads / lanes;
-  const int col = tid % lanes, seg = tid / lanes;
-  if (seg < step) {
-    uint32_t all[8] = {}, before[8] = {};
-    for (int b = seg; b < a.blocks; b += step) {
-      const uint4 u = *(const uint4*)(a.counts + (int64_t)b * a.ld_counts + 8 * col);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  // lanes of a row of counts: a power of two, so that the rows of a wave are summed across its lanes first
+  const int cols = a.ld_counts / 8;
+  int lanes = 1;
+  while (lanes < cols) lanes *= 2;
+  const int step = kRouteThreads / lanes, col = tid & (lanes - 1), seg = tid / lanes;
+  uint32_t all[8] = {}, before[8] = {};
+  if (col < cols) {
+    for (int b0 = seg; b0 < a.blocks; b0 += 4 * step) {
+      uint4 u[4];  // in flight at once
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t n = i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
-        all[i] += n;
-        before[i] += b < (int)blockIdx.x ? n : 0;
+      for (int k = 0; k < 4; ++k)
+        u[k] = b0 + k * step < a.blocks ? *(const uint4*)(a.counts + (int64_t)(b0 + k * step) * a.ld_counts + 8 * col)
+                                        : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+        const bool under = b0 + k * step < (int)blockIdx.x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t n = i % 2 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+          all[i] += n;
+          before[i] += under ? n : 0;
+        }
       }
     }
+  }
+  for (int d = kWave / 2; d >= lanes; d /= 2)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (all[i]) atomicAdd(&total[8 * col + i], all[i]);
-      if (before[i]) atomicAdd(&base[8 * col + i], before[i]);
+      all[i] += __shfl_xor(all[i], d, kWave);
+      before[i] += __shfl_xor(before[i], d, kWave);
     }
-  }
+  if ((tid & (kWave - 1)) < lanes && col < cols)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // expert 8 col + i at col + i lanes: one bank each
+      if (all[i]) atomicAdd(&total[col + i * lanes], all[i]);
+      if (before[i]) atomicAdd(&base[col + i * lanes], before[i]);
+    }
   __syncthreads();
+  const int at = (tid / 8 & (lanes - 1)) + tid % 8 * lanes;  // of expert `tid`
+  const uint32_t mine = tid < a.ld_counts ? total[at] : 0, lower = tid < a.ld_counts ? base[at] : 0;
   uint32_t sum;
-  const uint32_t first = block_scan(total[tid], part, &sum);
-  base[tid] += first;
+  const uint32_t first = block_scan(mine, part, &sum);  // all have read base
+  base[tid] = lower + first;
   if (blockIdx.x == 0) {
     if (tid < a.n_experts) a.offsets[tid] = (int)first;
     if (tid == 0) a.offsets[a.n_experts] = (int)sum;
   }
-  const int64_t t0 = (int64_t)blockIdx.x * a.per;
-  const int slots = kRouteChunk * a.top;
   for (int c = 0; c < a.per && t0 + c < a.rows; c += kRouteChunk) {
-    const int64_t left = a.rows - t0 - c;
-    const int n = left < kRouteChunk ? (int)left * a.top : slots;
-    const int64_t at = (t0 + c) * a.top;
-    int id[2] = {-1, -1};  // of the chunk's pairs tid and tid + 1024: at most 64 x 32
+    if (c > 0) load_ids(c);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int s = tid + kRouteThreads * i;
-      if (s < n) id[i] = a.experts[at + s];
       if (id[i] >= 0) atomicOr(&mask[id[i]], 1ull << (s / a.top));
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int s = tid + kRouteThreads * i;
-      if (s < n) {
+      if (s < pairs_of(c)) {
         int place = -1;
         if (id[i] >= 0) {
           place = (int)(base[id[i]] + __popcll(mask[id[i]] & ((1ull << (s / a.top)) - 1)));
           a.rows_out[place] = (int)(t0 + c) + s / a.top;
         }
-        a.places[at + s] = place;
+        a.places[(t0 + c) * a.top + s] = place;
       }
     }
     __syncthreads();
