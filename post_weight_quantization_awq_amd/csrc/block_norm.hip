@@ -16,14 +16,14 @@ namespace awq {
 
 // A row of X, or the weighted sum of its rows that a token's places name; places outside X name none.  Rows are
 // loaded four at a time, ahead of their sums (one at a time from 16385 columns on, for want of registers).
-template <int DT, int CH, bool FULL>
+template <int DT, int CH, bool FULL, bool SUM>
 __device__ __forceinline__ void load_sum(const BlockNormArgs& a, int64_t row, int lane, int lanes, int cpr,
                                          float (&y)[CH][8]) {
 #pragma unroll
   for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[c][j] = 0.0f;
-  if (a.places == nullptr) {
+  if constexpr (!SUM) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
       if (FULL || lane + c * lanes < cpr) unpack8<DT>(ld_stream(a.X + row * a.ld_x + 8 * (lane + c * lanes)), y[c]);
@@ -96,7 +96,7 @@ __device__ __forceinline__ float squares(const float (&h)[CH][8], int lane, int 
 }
 
 // FULL: every lane has CH chunks
-template <int DT, int FMT, int GL, int CH, bool FULL>
+template <int DT, int FMT, int GL, int CH, bool FULL, bool SUM>
 __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const BlockNormArgs a) {
   const int lanes = GL ? GL : (int)blockDim.x;
   const int lane = GL ? (int)threadIdx.x % (GL ? GL : 1) : (int)threadIdx.x;
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const Bl
   for (int c = 0; c < CH; ++c)
     if (kEarly && (FULL || lane + c * lanes < cpr)) res[c] = ld_stream(a.R + row * a.ld_r + 8 * (lane + c * lanes));
   float h[CH][8];
-  load_sum<DT, CH, FULL>(a, row, lane, lanes, cpr, h);
+  load_sum<DT, CH, FULL, SUM>(a, row, lane, lanes, cpr, h);
   Ahead8 post[CH], gate[CH], norm[CH];
   auto each = [&](auto f) {
 #pragma unroll
@@ -173,13 +173,13 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const Bl
   }
 }
 
-template <int DT, int FMT>
+template <int DT, int FMT, bool SUM>
 static void block_norm_launch(const BlockNormArgs& a, hipStream_t stream) {
   const int64_t cpr = a.cols / 8;
 #define AWQ_NORM_W(GL, CH) \
-  block_norm_mx_kernel<DT, FMT, GL, CH, false><<<(unsigned)((a.rows + 256 / GL - 1) / (256 / GL)), 256, 0, stream>>>(a)
+  block_norm_mx_kernel<DT, FMT, GL, CH, false, SUM><<<(unsigned)((a.rows + 256 / GL - 1) / (256 / GL)), 256, 0, stream>>>(a)
 #define AWQ_NORM_B(CH, FULL)                                                                                         \
-  block_norm_mx_kernel<DT, FMT, 0, CH, FULL><<<(unsigned)a.rows, (unsigned)(((cpr + CH - 1) / CH + 63) / 64 * 64), 0, \
+  block_norm_mx_kernel<DT, FMT, 0, CH, FULL, SUM><<<(unsigned)a.rows, (unsigned)(((cpr + CH - 1) / CH + 63) / 64 * 64), 0, \
                                                stream>>>(a)
   if (cpr <= 4) AWQ_NORM_W(4, 1);
   else if (cpr <= 8) AWQ_NORM_W(8, 1);
@@ -199,11 +199,17 @@ static void block_norm_launch(const BlockNormArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_block_norm_mx(const BlockNormArgs& a, int dt, int fmt, hipStream_t stream) {
+#define AWQ_NORM(DT, FMT) \
+  do { \
+    if (a.places != nullptr) block_norm_launch<DT, FMT, true>(a, stream); \
+    else block_norm_launch<DT, FMT, false>(a, stream); \
+  } while (0)
   if (dt == 0) {
-    if (fmt == kMxFp8) block_norm_launch<0, kMxFp8>(a, stream); else block_norm_launch<0, kMxFp4>(a, stream);
+    if (fmt == kMxFp8) AWQ_NORM(0, kMxFp8); else AWQ_NORM(0, kMxFp4);
   } else {
-    if (fmt == kMxFp8) block_norm_launch<1, kMxFp8>(a, stream); else block_norm_launch<1, kMxFp4>(a, stream);
+    if (fmt == kMxFp8) AWQ_NORM(1, kMxFp8); else AWQ_NORM(1, kMxFp4);
   }
+#undef AWQ_NORM
   return hipGetLastError();
 }
 
