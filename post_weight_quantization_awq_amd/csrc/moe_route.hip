@@ -199,7 +199,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_select_kernel(const Route
 // value can set over the experts from the last to the first; for 32-bit ones a positive double, 32 bits of key over 30.
 // A token of 128 experts and 8 places costs a lane 280 comparisons; a wave for each token takes 300 operations of 64
 // lanes.  A lane's logits are in flight at once, 32 of them.
-constexpr int kLaneThreads = 4 * kRouteChunk, kLaneExperts = 256;
+constexpr int kLaneExperts = 256;
 constexpr uint32_t kNoKey = 0x007FFFFFu;  // -inf's: no larger one, no expert
 template <int DT>
 struct RouteWord {
@@ -300,78 +300,111 @@ __device__ __forceinline__ uint32_t plain_key(float f) {
   return f != f ? 0xFFFFFFFFu : k;
 }
 
-template <int K, int DT>
-__global__ __launch_bounds__(kLaneThreads) void route_lanes_kernel(const RouteArgs a) {
+// L lanes a token.  ONE: the only block, which also places the pairs
+template <int K, int DT, int L, bool ONE>
+__global__ __launch_bounds__(L * kRouteChunk) void route_lanes_kernel(const RouteArgs a) {
   using W = RouteWord<DT>;
+  static_assert(!ONE || L * kRouteChunk == kRouteThreads, "the scan is of 16 waves");
   __shared__ unsigned long long mask[kLaneExperts];
-  const int tid = threadIdx.x, q = tid % 4, tt = tid / 4;
+  __shared__ uint32_t base[ONE ? kLaneExperts : 1], part[kRouteWaves];
+  constexpr int kGroups = 16 / L;  // of 8 logits a lane, for 128 experts
+  constexpr int PL = (K + L - 1) / L;  // the lane's places: q, q + L
+  const int tid = threadIdx.x, q = tid % L, tt = tid / L;
   const int64_t t0 = (int64_t)blockIdx.x * a.per;
   uint32_t count = 0;  // of expert `tid`
+  int id[PL];
   for (int c = 0; c < a.per && t0 + c < a.rows; c += kRouteChunk) {
-    mask[tid] = 0;
+    if (tid < kLaneExperts) mask[tid] = 0;
     const int64_t t = t0 + c + tt;
     const bool live = t < a.rows;
-    const int64_t at = (live ? t : a.rows - 1) * a.ld;
-    typename W::type v[K] = {};
-    float sum = 0.0f;
-    for (int e = 8 * q; e < a.n_experts; e += 128) {
-      float f[4][8];
+    float share[PL];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) load_logits8<DT>(a, at, e + 32 * g, f[g]);
+    for (int i = 0; i < PL; ++i) id[i] = -1, share[i] = 0.0f;
+    if (t0 + c + __builtin_amdgcn_readfirstlane(tt) < a.rows) {  // a token for some lanes of the wave
+      const int64_t at = (live ? t : a.rows - 1) * a.ld;
+      typename W::type v[K] = {};
+      float sum = 0.0f;
+      for (int e = 8 * q; e < a.n_experts; e += 128) {
+        float f[kGroups][8];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        typename W::type x[8];
+        for (int g = 0; g < kGroups; ++g) load_logits8<DT>(a, at, e + 8 * L * g, f[g]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = W::pack(plain_key(f[g][i]), (uint32_t)(e + 32 * g + i));
+        for (int g = 0; g < kGroups; ++g) {
+          typename W::type x[8];
 #pragma unroll
-        for (int i = 0; i < 8; i += K) {
-          sort_words<W, K>(x + i);
-          merge_words<W, K>(v, x + i);
+          for (int i = 0; i < 8; ++i) x[i] = W::pack(plain_key(f[g][i]), (uint32_t)(e + 8 * L * g + i));
+#pragma unroll
+          for (int i = 0; i < 8; i += K) {
+            sort_words<W, K>(x + i);
+            merge_words<W, K>(v, x + i);
+          }
         }
       }
-    }
-    merge_lanes<W, K, 0xB1>(v);
-    merge_lanes<W, K, 0x4E>(v);
-    const float most = W::value(v[0]);
-    if (!a.renorm && W::some(v[0])) {
-      for (int e = 8 * q; e < a.n_experts; e += 32) {
-        float f[8];
-        load_logits8<DT>(a, at, e, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (f[i] != -INFINITY) sum += expf(f[i] - most);
+      merge_lanes<W, K, 0xB1>(v);
+      merge_lanes<W, K, 0x4E>(v);
+      if constexpr (L == 16) {
+        merge_lanes<W, K, 0x141>(v);
+        merge_lanes<W, K, 0x140>(v);
       }
-    }
-    // the lane's places: q, q + 4
-    constexpr int PL = (K + 3) / 4;
-    int id[PL];
-    float p[PL];
+      const float most = W::value(v[0]);
+      if (!a.renorm && W::some(v[0])) {
+        for (int e = 8 * q; e < a.n_experts; e += 8 * L) {
+          float f[8];
+          load_logits8<DT>(a, at, e, f);
 #pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      typename W::type d = 0;
+          for (int i = 0; i < 8; ++i)
+            if (f[i] != -INFINITY) sum += expf(f[i] - most);
+        }
+      }
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        if (4 * i + s < K) d = q == s ? v[4 * i + s] : d;
-      const bool some = W::some(d) && 4 * i + q < a.top;
-      id[i] = some ? W::expert(d) : -1;
-      p[i] = some ? expf(W::value(d) - most) : 0.0f;
-      if (a.renorm) sum += p[i];
+      for (int i = 0; i < PL; ++i) {
+        typename W::type d = 0;
+#pragma unroll
+        for (int s = 0; s < L; ++s)
+          if (L * i + s < K) d = q == s ? v[L * i + s] : d;
+        if (live && W::some(d) && L * i + q < a.top) id[i] = W::expert(d);
+        share[i] = id[i] >= 0 ? expf(W::value(d) - most) : 0.0f;
+        if (a.renorm) sum += share[i];
+      }
+      sum += dpp_m<0xB1>(sum);
+      sum += dpp_m<0x4E>(sum);
+      if constexpr (L == 16) {
+        sum += dpp_m<0x141>(sum);
+        sum += dpp_m<0x140>(sum);
+      }
+#pragma unroll
+      for (int i = 0; i < PL; ++i) share[i] = id[i] >= 0 ? share[i] / sum * a.scale : 0.0f;
     }
-    sum += dpp_m<0xB1>(sum);
-    sum += dpp_m<0x4E>(sum);
     __syncthreads();  // the masks are clear
 #pragma unroll
     for (int i = 0; i < PL; ++i)
-      if (live && 4 * i + q < a.top) {
-        a.experts[t * a.top + 4 * i + q] = id[i];
-        a.weights[t * a.top + 4 * i + q] = id[i] >= 0 ? p[i] / sum * a.scale : 0.0f;
+      if (live && L * i + q < a.top) {
+        a.experts[t * a.top + L * i + q] = id[i];
+        a.weights[t * a.top + L * i + q] = share[i];
         if (id[i] >= 0) atomicOr(&mask[id[i]], 1ull << tt);
       }
     __syncthreads();
-    count += __popcll(mask[tid]);
-    __syncthreads();  // the masks are cleared for the next chunk
+    if (tid < kLaneExperts) count += __popcll(mask[tid]);
+    if constexpr (!ONE) __syncthreads();  // the masks are cleared for the next chunk
   }
-  if (tid < a.ld_counts) a.counts[(int64_t)blockIdx.x * a.ld_counts + tid] = (uint16_t)count;
+  if constexpr (!ONE) {
+    if (tid < a.ld_counts) a.counts[(int64_t)blockIdx.x * a.ld_counts + tid] = (uint16_t)count;
+  } else {
+    uint32_t total;
+    const uint32_t first = block_scan(count, part, &total);
+    if (tid < a.n_experts) a.offsets[tid] = (int)first, base[tid] = first;
+    if (tid == 0) a.offsets[a.n_experts] = (int)total;
+    __syncthreads();
+    if (tt < a.rows && q < a.top) {
+      int place = -1;
+      if (id[0] >= 0) {
+        place = (int)(base[id[0]] + __popcll(mask[id[0]] & ((1ull << tt) - 1)));
+        a.rows_out[place] = tt;
+      }
+      a.places[tt * a.top + q] = place;
+    }
+    route_rest(a, total, tid, kRouteThreads);
+  }
 }
 
 // Places of a block's pairs: the experts' totals and what lies in the blocks before, from the counts of all blocks,
@@ -484,24 +517,22 @@ size_t moe_route_workspace(int64_t rows, int n_experts) {
   return rows <= kRouteChunk ? 0 : (size_t)route_blocks(rows) * ((n_experts + 7) / 8 * 8) * sizeof(uint16_t);
 }
 
+template <int K, int DT>
+static void route_lanes_launch(const RouteArgs& a, hipStream_t stream) {
+  if (a.blocks == 1) route_lanes_kernel<K, DT, 16, true><<<1, 16 * kRouteChunk, 0, stream>>>(a);
+  else route_lanes_kernel<K, DT, 4, false><<<(unsigned)a.blocks, 4 * kRouteChunk, 0, stream>>>(a);
+}
 template <int K>
 static void route_lanes_launch(const RouteArgs& a, hipStream_t stream) {
-  if (a.dtype == 0) route_lanes_kernel<K, 0><<<(unsigned)a.blocks, kLaneThreads, 0, stream>>>(a);
-  else if (a.dtype == 1) route_lanes_kernel<K, 1><<<(unsigned)a.blocks, kLaneThreads, 0, stream>>>(a);
-  else route_lanes_kernel<K, 2><<<(unsigned)a.blocks, kLaneThreads, 0, stream>>>(a);
+  if (a.dtype == 0) route_lanes_launch<K, 0>(a, stream);
+  else if (a.dtype == 1) route_lanes_launch<K, 1>(a, stream);
+  else route_lanes_launch<K, 2>(a, stream);
 }
 
 template <int EL>
-static void route_launch(const RouteArgs& a, hipStream_t stream) {
-  if (a.blocks == 1) {
-    route_select_kernel<EL, true><<<1, kRouteThreads, 0, stream>>>(a);
-    return;
-  }
-  if (a.n_experts > kLaneExperts || a.top > 8) route_select_kernel<EL, false><<<(unsigned)a.blocks, kRouteThreads, 0, stream>>>(a);
-  else if (a.top > 4) route_lanes_launch<8>(a, stream);
-  else if (a.top > 2) route_lanes_launch<4>(a, stream);
-  else route_lanes_launch<2>(a, stream);
-  route_place_kernel<<<(unsigned)a.blocks, kRouteThreads, 0, stream>>>(a);
+static void route_select_launch(const RouteArgs& a, hipStream_t stream) {
+  if (a.blocks == 1) route_select_kernel<EL, true><<<1, kRouteThreads, 0, stream>>>(a);
+  else route_select_kernel<EL, false><<<(unsigned)a.blocks, kRouteThreads, 0, stream>>>(a);
 }
 
 hipError_t launch_moe_route(const void* logits, int dtype, int64_t rows, int n_experts, int64_t ld, int top,
@@ -509,11 +540,22 @@ hipError_t launch_moe_route(const void* logits, int dtype, int64_t rows, int n_e
                             int32_t* places, int32_t* offsets, void* ws, hipStream_t stream) {
   const RouteArgs a = {logits, dtype, ld, rows, n_experts, top, renorm, scale, experts, weights, rows_out, places,
                        offsets, (uint16_t*)ws, (n_experts + 7) / 8 * 8, route_per(rows), (int)route_blocks(rows)};
-  if (n_experts <= 64) route_launch<1>(a, stream);
-  else if (n_experts <= 128) route_launch<2>(a, stream);
-  else if (n_experts <= 256) route_launch<4>(a, stream);
-  else if (n_experts <= 512) route_launch<8>(a, stream);
-  else route_launch<16>(a, stream);
+  if (n_experts <= kLaneExperts && top <= 8) {
+    if (top > 4) route_lanes_launch<8>(a, stream);
+    else if (top > 2) route_lanes_launch<4>(a, stream);
+    else route_lanes_launch<2>(a, stream);
+  } else if (n_experts <= 64) {
+    route_select_launch<1>(a, stream);
+  } else if (n_experts <= 128) {
+    route_select_launch<2>(a, stream);
+  } else if (n_experts <= 256) {
+    route_select_launch<4>(a, stream);
+  } else if (n_experts <= 512) {
+    route_select_launch<8>(a, stream);
+  } else {
+    route_select_launch<16>(a, stream);
+  }
+  if (a.blocks > 1) route_place_kernel<<<(unsigned)a.blocks, kRouteThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

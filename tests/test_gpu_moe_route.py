@@ -49,7 +49,7 @@ def logits(seed, T, E, dtype, spread=2.0):
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("T,E,top", [
     (1, 1, 1), (1, 8, 2), (3, 5, 5), (17, 64, 8), (64, 65, 6), (65, 64, 1), (63, 128, 8), (24, 256, 32), (7, 1024, 32),
-    (129, 128, 8), (1000, 10, 3), (257, 600, 16), (70, 1000, 32), (333, 9, 9), (2049, 40, 4),
+    (40, 200, 8), (300, 256, 7), (500, 250, 2), (129, 128, 8), (1000, 10, 3), (257, 600, 16), (70, 1000, 32), (333, 9, 9), (2049, 40, 4),
 ])
 def test_route(A, T, E, top, dtype):
     say(f"moe_route T {T} E {E} top {top} {dtype}")
