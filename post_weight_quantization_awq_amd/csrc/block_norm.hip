@@ -7,7 +7,12 @@
 //   v = h / sqrt(mean h^2 + eps) * norm                -> codes, scales
 // A row stays in registers from its loads to its codes, so that each input is
 // read once: bound by memory, in one launch.  Lanes of a row as in rms_norm_mx:
-// a wave or a part of it up to 512 columns, else a block.
+// a wave or a part of it up to 512 columns, else a block.  6001 x 4096 with a norm
+// and a gate 35.3 us (4.9 TB/s; a large copy 5.1), 4096 x 4096 with a sum of 4 rows
+// 39.5 us (5.5 TB/s), one row with a sum of 8 4.4 us.  What the rows in flight leave
+// of registers decides: the kernel without the sum has 58, and 88 (38.9 us for the
+// first) with the sum's loads in it, so each has a kernel of its own; the weights'
+// loads ahead of X cost more registers than they gain.
 #include "awq_launch.h"
 #include "mx_device.h"
 #include "mx_norm.h"
@@ -15,7 +20,8 @@
 namespace awq {
 
 // A row of X, or the weighted sum of its rows that a token's places name; places outside X name none.  Rows are
-// loaded four at a time, ahead of their sums (one at a time from 16385 columns on, for want of registers).
+// loaded eight at a time, ahead of their sums (four where a lane has two chunks, and one from 16385 columns on, for want
+// of registers).
 template <int DT, int CH, bool FULL, bool SUM>
 __device__ __forceinline__ void load_sum(const BlockNormArgs& a, int64_t row, int lane, int lanes, int cpr,
                                          float (&y)[CH][8]) {
@@ -29,7 +35,7 @@ __device__ __forceinline__ void load_sum(const BlockNormArgs& a, int64_t row, in
       if (FULL || lane + c * lanes < cpr) unpack8<DT>(ld_stream(a.X + row * a.ld_x + 8 * (lane + c * lanes)), y[c]);
     return;
   }
-  constexpr int NP = CH >= 4 ? 1 : 4;
+  constexpr int NP = CH >= 4 ? 1 : CH == 2 ? 4 : 8;
   for (int j0 = 0; j0 < a.top; j0 += NP) {
     uint32_t place[NP];
     float share[NP];
@@ -176,6 +182,10 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const Bl
 template <int DT, int FMT, bool SUM>
 static void block_norm_launch(const BlockNormArgs& a, hipStream_t stream) {
   const int64_t cpr = a.cols / 8;
+  // Rows of 4096: up to 128 of them, latency counts and a lane takes one chunk (the sum of 8 rows: 1 row 4.4 us, with
+  // two chunks 5.0; 64 rows 4.9 and 5.6); more have two, for more rows in flight (256 rows 7.5, with one chunk 8.3;
+  // 6001 without a sum 35.8 and 42).
+  const bool few = a.rows <= 128;
 #define AWQ_NORM_W(GL, CH) \
   block_norm_mx_kernel<DT, FMT, GL, CH, false, SUM><<<(unsigned)((a.rows + 256 / GL - 1) / (256 / GL)), 256, 0, stream>>>(a)
 #define AWQ_NORM_B(CH, FULL)                                                                                         \
@@ -186,8 +196,8 @@ static void block_norm_launch(const BlockNormArgs& a, hipStream_t stream) {
   else if (cpr <= 16) AWQ_NORM_W(16, 1);
   else if (cpr <= 32) AWQ_NORM_W(32, 1);
   else if (cpr <= 64) AWQ_NORM_W(32, 2);
-  else if (cpr <= 512 && cpr % 128 == 0) AWQ_NORM_B(2, true);
-  else if (cpr <= 512) AWQ_NORM_B(2, false);
+  else if (!few && cpr <= 512 && cpr % 128 == 0) AWQ_NORM_B(2, true);
+  else if (!few && cpr <= 512) AWQ_NORM_B(2, false);
   else if (cpr <= 1024 && cpr % 64 == 0) AWQ_NORM_B(1, true);
   else if (cpr <= 1024) AWQ_NORM_B(1, false);
   else if (cpr <= 2048 && cpr % 128 == 0) AWQ_NORM_B(2, true);

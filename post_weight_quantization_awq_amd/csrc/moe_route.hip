@@ -1,15 +1,19 @@
 // Routing of tokens to experts: each token's k largest logits, their shares, and
 // the (token, expert) pairs in expert order, as the grouped product takes them.
 //
-// A wave takes a token: its lanes hold the logits as unsigned keys that order as
-// the values do, and k rounds of a wave maximum pick the experts.  A token has an
-// expert at most once, so 64 tokens are a 64-bit mask for each expert in LDS: a
-// pair's rank among its expert's is the number of set bits below its token's, the
-// same in whatever order the bits were set.  Up to 64 tokens (a decoding step) one
-// block does it all; more take two launches, the second of which adds the counts
-// that the first left for each block.
+// Logits become unsigned keys that order as the values do.  Up to 256 experts, of
+// which a token takes up to 8, a few lanes sort a token's logits (route_lanes_kernel);
+// else a wave takes a token and k rounds of a wave maximum pick the experts
+// (route_select_kernel).  A token has an expert at most once, so 64 tokens are a
+// 64-bit mask for each expert in LDS: a pair's rank among its expert's is the number
+// of set bits below its token's, the same in whatever order the bits were set.  Up to
+// 64 tokens (a decoding step) one block does it all; more take two launches, the
+// second of which adds the counts that the first left for each block.
 //
-// Bound by latency, not by the logits' bytes.
+// Bound by latency, not by the logits' bytes: 24 tokens of 128 experts, 8 each, take
+// 3.9 us, of which a call that does next to nothing takes 3.2 (a wave for each token:
+// 6.8); 16001 tokens take 14 us in two launches (10 MB: 2 us at a copy's rate), of
+// which the second's sums of 251 blocks' counts are 2.
 #include "awq_launch.h"
 #include "mx_device.h"
 
@@ -193,12 +197,13 @@ __global__ __launch_bounds__(kRouteThreads) void route_select_kernel(const Route
   }
 }
 
-// More tokens: 4 lanes take a token, each a fourth of its logits.  A lane sorts K of them at a time and merges them into
-// its best K, in order; two merges across the lanes join those.  A logit and its expert are one word that orders as
+// L lanes take a token, each a part of its logits.  A lane sorts K of them at a time and merges them into its best K, in
+// order; merges across the lanes join those.  A logit and its expert are one word that orders as
 // they do, so that a comparison is a maximum and a minimum: for 16-bit logits 32 bits, the 19 of the key that such a
 // value can set over the experts from the last to the first; for 32-bit ones a positive double, 32 bits of key over 30.
-// A token of 128 experts and 8 places costs a lane 280 comparisons; a wave for each token takes 300 operations of 64
-// lanes.  A lane's logits are in flight at once, 32 of them.
+// Four lanes do that for 128 experts and 8 places with 300 comparisons each, all their logits in flight at once; a wave
+// for each token takes 300 operations of 64 lanes (16001 tokens: 14 us, 22 with waves).  Up to 64 tokens 16 lanes take
+// one, for latency (24 tokens: 3.9 us).
 constexpr int kLaneExperts = 256;
 constexpr uint32_t kNoKey = 0x007FFFFFu;  // -inf's: no larger one, no expert
 template <int DT>

@@ -3,6 +3,14 @@
 // matrix e of W.  The kernels are the product's (mx_product.h); a block finds its
 // tile of rows by itself, from the offsets on the device, so that the host waits
 // for nothing and a captured graph takes whatever offsets there are.
+//
+// Few rows a group are bound by reading the weights: the 8 groups of 4096 x 4096 of
+// one token 16.4 us (4.4 TB/s with the launch), 64 groups of 4096 x 2048 for 512 rows
+// 63 us (4.6).  Large groups are bound by the matrix cores and by tiles that no group fills:
+// 16384 rows of 32 uneven groups of 4096 x 4096 276 us (2.0 PFLOP/s; one group of all
+// 209, the plain product 195-203, and reading A through `rows` adds 13): a group's
+// last tile of fewer than 128 rows takes 0.95 of a full one, since its stages wait for
+// their loads either way.
 #include <algorithm>
 
 #include "awq_launch.h"
@@ -89,8 +97,8 @@ static void grouped_launch(const GroupedArgs& p, uint8_t* work, hipStream_t stre
       if (p.g.rows != nullptr) AWQ_BIG8(true); else AWQ_BIG8(false);
 #undef AWQ_BIG8
     } else {
-      mx_big_kernel<YT, Groups><<<(unsigned)(w.n_mt * w.n_nt + 2 * kMxXcds), 512, 0, stream>>>(p.A, p.M, p.W, p.N, p.K, sc, w.m_pad, w.rows, w.n_mt,
-                                                                     w.n_nt, 4, p.Y, p.ld_y, p.g, sg);
+      mx_big_kernel<YT, Groups><<<(unsigned)(w.n_mt * w.n_nt + 2 * kMxXcds), 512, 0, stream>>>(
+          p.A, p.M, p.W, p.N, p.K, sc, w.m_pad, w.rows, w.n_mt, w.n_nt, 4, p.Y, p.ld_y, p.g, sg);
     }
   }
 }

@@ -2,6 +2,14 @@
 // epilogue: Y = act(A W^T + bias) + residual, rounded once, or quantized to blocks.
 // The kernels and their choice are the product's (mx_product.h, mx_tiles.h); sums of
 // K ranges are joined by a second launch, which then has the epilogue.
+//
+// One token, 6144 x 4096: 5.0 us (13 MB of weights; the product's time).  8192 x 4096 x
+// 4096 in 4 bits with a residual: 100 us, the product alone 76 (the residual's 67 MB
+// arrive while the last stages are multiplied, what is stored is waited for); 4096 x
+// 12288 x 4096 in 8 bits with bias and GELU to 8 bits: 183-186 us (2.2 PFLOP/s), the
+// product alone 156-175 (activation and quantization are 26 and 12 operations a value,
+// for which the matrix cores wait).  A launch of its own for them would move 200 MB, 40
+// us, and 150 MB, 30 us.
 #include <algorithm>
 
 #include "awq_launch.h"

@@ -97,6 +97,9 @@ def check(out, n, fmt, dtype, scale=1.0):
     (2, 40032, "bf16", 0, None, None, "f32", "fp8", None, 0, 1.0),
     (131, 64, "bf16", 2, "f32", None, "f32", "fp4", 67, 1, 1.0),
     (35, 256, "f16", 0, None, ("f16", "cols"), "bf16", "fp8", None, 0, 1.0),
+    (140, 4096, "bf16", 8, "bf16", None, "bf16", "fp8", None, 0, 1.0),
+    (139, 2080, "f16", 5, None, ("f32", "rows"), "bf16", "fp4", 2083, 1, 0.5),
+    (129, 1056, "bf16", 0, "f16", None, "f32", "fp8", None, 0, 1.0),
     (17, 288, "bf16", 7, "f16", ("f32", "cols"), "f16", "fp8", 291, 1, 1.0),
 ])
 def test_block_norm(A, rows, cols, dtype, top, post, gate, wdtype, fmt, ld, offset, scale):
