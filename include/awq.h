@@ -582,8 +582,8 @@ awq_status awq_moe_route(const void* logits, int32_t dtype, int64_t T, int32_t n
  * captured graph takes what stands there in each replay.  M: rows that Y has room for;
  * rows of Y outside [offsets[0], offsets[n_groups]) are left as they were.  rows: int32 [M],
  * or NULL, when a_rows must be M.  Offsets outside [0, M] count as the nearest of them;
- * a row number outside [0, a_rows) stands for a row of zeros.  Where offsets descend, rows
- * that two groups name hold the result of either.
+ * a row number outside [0, a_rows) stands for a row of zeros.  Where offsets descend, a
+ * value in a row of groups is left as it was or is the result of one that names the row.
  * The weights of groups without rows are not read.  Y, its types, the sums and their
  * accuracy as awq_mx_matmul.  1 <= n_groups <= 1024, M <= 2^26, N <= 2^20, M N <= 2^37, K <=
  * 2^22, K % 32 == 0, a_rows <= 2^26, and with rows the codes of A below 2^31 bytes (AWQ_ESHAPE).

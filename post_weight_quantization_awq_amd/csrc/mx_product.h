@@ -520,7 +520,7 @@ __global__ __launch_bounds__(WM* WN* kWave, OCC) void mx_tile_kernel(
   int64_t m0;
   if constexpr (X::kGroups) {  // n_mt: at least the tiles of rows that there are
     const GroupTile g = group_pick(x, (int)M, BM, [&](int total) {
-      if ((int)blockIdx.x >= total * n_nt) return -1;
+      if (total > n_mt || (int)blockIdx.x >= total * n_nt) return -1;  // more than n_mt: offsets descend
       block_tile((int)blockIdx.x, total * n_nt, total, n_nt, group_m, &mt, &nt);
       return mt;
     });
@@ -856,8 +856,11 @@ __global__ __launch_bounds__(256) void stage_groups_kernel(const Groups g, const
   if ((int)blockIdx.x < n_mt) {
     const GroupPlace at = group_place(g, M, (int)blockIdx.x);
     const GroupTile& t = at.tile;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) tab[n_mt] = make_int4(at.full, at.half, 0, 0);
-    if (t.group < 0) return;
+    // offsets that descend can name rows more than once, and more tiles than the table has places for: then none
+    const bool over = at.full + at.half > n_mt;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0)
+      tab[n_mt] = over ? make_int4(0, 0, 0, 0) : make_int4(at.full, at.half, 0, 0);
+    if (over || t.group < 0) return;
     const int m = t.first + tid;
     const int64_t of = m < t.end ? group_row(g, m) : -1;
     from[tid] = of;

@@ -126,6 +126,42 @@ def test_rows_and_offsets_out_of_range(A, M, N, K, fmt):
     assert not got[bad].any()
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("M,E,N,K", [(500, 3, 333, 352), (61, 8, 4100, 2208), (900, 5, 1000, 416), (2000, 6, 2054, 800),
+                                     (3000, 3, 8209, 800), (4096, 7, 8196, 1184)])
+def test_offsets_that_descend(A, M, E, N, K, fmt):
+    """Values of rows that several groups name are left or are one group's, with more tiles than there are places for
+    and with as many; nothing behind the workspace is written."""
+    import torch
+    say(f"mx_matmul_grouped descending {M} {E} {N} {K} {fmt}")
+    rng = np.random.default_rng(K + E)
+    # activations of -1, 0 and 1, scales of 1: the sums are multiples of 1/2 below 2^14 and round nowhere
+    if fmt == "fp8":
+        ac = torch.from_numpy(rng.integers(-1, 2, (M, K)).astype(np.float32)).cuda().to(torch.float8_e4m3fn)
+    else:
+        nibble = np.array([0x0, 0x2, 0xA], np.uint8)[rng.integers(0, 3, (2, M, K // 2))]
+        ac = torch.from_numpy(nibble[0] | nibble[1] << 4).cuda()
+    a = ac, torch.full((M, K // 32), 127, dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu)
+    codes = torch.from_numpy(rng.integers(0, 256, (E, N, K // 2)).astype(np.uint8)).cuda()
+    scales = torch.full((E, N, K // 32), 127, dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu)
+    need = A.mx_matmul_grouped_workspace_bytes(fmt, M, N, K, E)
+    ws = torch.full((need + 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+    for cuts in ([0, M] * E, [0, 40, 20] + [20] * E, [M] + [0] * E, [0, M, 0] + [5] * E, [M // 2, M, 0, M // 2] + [M // 2] * E):
+        offsets = torch.tensor(cuts[:E + 1], dtype=torch.int32, device="cuda")
+        out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        plan = A.MxMatmulGroupedPlan(*a, codes, scales, offsets, out=out, ws=ws)
+        plan.run()
+        torch.cuda.synchronize()
+        assert plan.ws is ws and ws[need:].eq(0xA5).all()
+        left = out.eq(7)
+        for e in range(E):
+            lo, hi = max(0, cuts[e]), min(M, cuts[e + 1])
+            if lo < hi:
+                y = A.mx_matmul(a[0][lo:hi], a[1][lo:hi], codes[e], scales[e], out_dtype=torch.bfloat16)
+                left[lo:hi] |= out[lo:hi].eq(y)
+        assert left.all()
+
+
 def test_nothing_to_do(A):
     import torch
     say("mx_matmul_grouped empty")
