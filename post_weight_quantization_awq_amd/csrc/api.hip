@@ -1057,6 +1057,8 @@ awq_status awq_block_norm_mx(const void* X, int32_t x_dtype, int64_t x_rows, int
   if ((!X && x_rows > 0) || !residual || !norm || !residual_out || !codes || !scales)
     return fail(AWQ_EINVAL, "X / residual / norm / residual_out / codes / scales is NULL");
   if (places && residual_out == X) return fail(AWQ_EINVAL, "residual_out is X, whose rows other tokens read");
+  if (rows > 1 && ((residual_out == X && ld_ro != ld_x) || (residual_out == residual && ld_ro != ld_r)))
+    return fail(AWQ_EINVAL, "residual_out is X or residual, of another row stride");
   if (misaligned(X, x_dtype) || misaligned(residual, x_dtype) || misaligned(residual_out, x_dtype) ||
       misaligned(norm, norm_dtype) || (post && misaligned(post, post_dtype)) || (gate && misaligned(gate, gate_dtype)) ||
       misaligned(places, AWQ_F32) || misaligned(shares, AWQ_F32))

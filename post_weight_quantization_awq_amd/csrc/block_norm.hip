@@ -90,15 +90,15 @@ __device__ __forceinline__ void ahead_values(const Ahead8& r, int dt, float (&f)
   }
 }
 
-template <int CH, bool FULL>
-__device__ __forceinline__ float squares(const float (&h)[CH][8], int lane, int lanes, int cpr) {
-  float sum = 0.0f;
+template <int CH, bool FULL, int N>
+__device__ __forceinline__ void squares(const float (&h)[CH][8], int lane, int lanes, int cpr, float (&sums)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) sums[c] = 0.0f;
 #pragma unroll
   for (int c = 0; c < CH; ++c)
     if (FULL || lane + c * lanes < cpr)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(h[c][j], h[c][j], sum);
-  return sum;
+      for (int j = 0; j < 8; ++j) sums[N == 1 ? 0 : c] = __builtin_fmaf(h[c][j], h[c][j], sums[N == 1 ? 0 : c]);
 }
 
 // FULL: every lane has CH chunks
@@ -110,7 +110,10 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const Bl
                          : (int64_t)blockIdx.x;
   const bool live = FULL || row < a.rows;
   const int cpr = FULL ? CH * lanes : live ? (int)(a.cols / 8) : 0;  // chunks of the row that there are
-  __shared__ float part[2][GL ? 1 : 16];
+  // The sums of two chunks are kept apart: a row's total is then the same with one chunk a lane, which few rows have.
+  constexpr int NS = GL == 0 && CH == 2 ? 2 : 1;
+  __shared__ float part[2][GL ? 1 : 16 * NS];
+  float sums[NS];
   constexpr bool kEarly = CH < 4;  // what is added ahead of the sums, but for the longest rows, for want of registers
   uint4 res[CH];
 #pragma unroll
@@ -128,8 +131,8 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const Bl
   auto get_gate = [&]() { if (a.gate != nullptr) each([&](int c, int64_t col) { gate[c] = load_ahead(a.gate, a.gate_dtype, row * a.ld_g + col); }); };
   auto get_norm = [&]() { each([&](int c, int64_t col) { norm[c] = load_ahead(a.norm, a.norm_dtype, col); }); };
   if (a.post != nullptr) {
-    const float r = row_scale<GL, CH>(h, squares<CH, FULL>(h, lane, lanes, cpr), live, lane, lanes, cpr, a.cols, a.eps,
-                                      part[0]);
+    squares<CH, FULL>(h, lane, lanes, cpr, sums);
+    const float r = row_scale<GL, CH>(h, sums, live, lane, lanes, cpr, a.cols, a.eps, part[0]);
     get_post();
 #pragma unroll
     for (int c = 0; c < CH; ++c)
@@ -160,8 +163,8 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const Bl
       for (int j = 0; j < 8; ++j) h[c][j] = __builtin_fmaf(a.residual_scale, r[j], h[c][j]);
       st_any(a.RO + row * a.ld_ro + col, pack8<DT>(h[c]));
     }
-  const float r =
-      row_scale<GL, CH>(h, squares<CH, FULL>(h, lane, lanes, cpr), live, lane, lanes, cpr, a.cols, a.eps, part[1]);
+  squares<CH, FULL>(h, lane, lanes, cpr, sums);
+  const float r = row_scale<GL, CH>(h, sums, live, lane, lanes, cpr, a.cols, a.eps, part[1]);
   get_norm();
 #pragma unroll
   for (int c = 0; c < CH; ++c) {

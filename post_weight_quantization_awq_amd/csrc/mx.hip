@@ -336,7 +336,7 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void rms_norm_mx_kernel(const Norm
   const int cpr = (int)(a.cols / 8);
   const bool live = row < a.rows;
   float h[CH][8];
-  float sum = 0.0f;
+  float sum[1] = {0.0f};
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int k = lane + c * lanes;
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void rms_norm_mx_kernel(const Norm
         st_any(a.RO + row * a.ld_ro + 8 * k, pack8<DT>(h[c]));
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(h[c][j], h[c][j], sum);
+      for (int j = 0; j < 8; ++j) sum[0] = __builtin_fmaf(h[c][j], h[c][j], sum[0]);
     }
   }
   __shared__ float part[GL ? 1 : 16];

@@ -36,6 +36,28 @@ __device__ __forceinline__ float row_total(float v, float* part, F f) {
   }
 }
 
+// N values a lane, which count as N lanes: with GL = 0 the same result as of N times as many lanes with one each.
+template <int GL, int N, class F>
+__device__ __forceinline__ float row_total_of(const float (&v)[N], float* part, F f) {
+  if constexpr (N == 1) {
+    return row_total<GL>(v[0], part, f);
+  } else {
+    static_assert(GL == 0, "lanes of a wave have one value each");
+    const int wave = (int)threadIdx.x >> 6, nw = (int)blockDim.x >> 6;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      float x = v[c];
+#pragma unroll
+      for (int m = kWave / 2; m >= 1; m >>= 1) x = f(x, __shfl_xor(x, m, kWave));
+      if ((threadIdx.x & 63) == 0) part[c * nw + wave] = x;
+    }
+    __syncthreads();
+    float x = 0.0f;
+    for (int i = 0; i < N * nw; ++i) x = f(x, part[i]);
+    return x;
+  }
+}
+
 // Rows whose squares leave fp32's range: the mean is infinite, or so small that squares lost below the range count
 // (those are off by at most 2^-150 each, 2^-134 for the longest row, 2^-34 of the least sum or eps taken).  They are
 // brought to the middle of the range first, by the power of two of their largest value or, where that is less,
@@ -43,11 +65,13 @@ __device__ __forceinline__ float row_total(float v, float* part, F f) {
 constexpr float kNormLeast = 0x1p-100f;
 
 // 1 / sqrt(mean h^2 + eps) of a row whose lanes hold h and their sums of squares.  Where those leave fp32's range h
-// is scaled, and what is returned goes with the scaled h.  part: 16 floats of LDS with GL = 0.
-template <int GL, int CH>
-__device__ __forceinline__ float row_scale(float (&h)[CH][8], float sum, bool live, int lane, int lanes, int cpr,
+// is scaled, and what is returned goes with the scaled h.  N sums a lane: of all its chunks, or of each.  part: 16 N
+// floats of LDS with GL = 0.
+template <int GL, int CH, int N>
+__device__ __forceinline__ float row_scale(float (&h)[CH][8], float (&sums)[N], bool live, int lane, int lanes, int cpr,
                                            int64_t cols, float eps, float* part) {
-  sum = row_total<GL>(sum, part, [](float x, float y) { return x + y; });
+  static_assert(N == 1 || N == CH, "a sum for all of the lane's chunks or for each");
+  float sum = row_total_of<GL>(sums, part, [](float x, float y) { return x + y; });
   float mean = sum / (float)cols + eps;
   // the same for the whole row
   if (__builtin_expect(!(mean < HUGE_VALF) || (sum < kNormLeast && eps < kNormLeast), false)) {
@@ -64,7 +88,8 @@ __device__ __forceinline__ float row_scale(float (&h)[CH][8], float sum, bool li
     if (top < 0x7F800000u) {
       int k2 = (int)(top >> 23) - 127;
       if (eps > 0.0f) k2 = max(k2, ((int)(__builtin_bit_cast(uint32_t, eps) >> 23) - 127) / 2);
-      sum = 0.0f;
+#pragma unroll
+      for (int c = 0; c < N; ++c) sums[c] = 0.0f;
       if constexpr (GL == 0) __syncthreads();
 #pragma unroll
       for (int c = 0; c < CH; ++c)
@@ -72,9 +97,9 @@ __device__ __forceinline__ float row_scale(float (&h)[CH][8], float sum, bool li
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             h[c][j] = __builtin_ldexpf(h[c][j], -k2);
-            sum = __builtin_fmaf(h[c][j], h[c][j], sum);
+            sums[N == 1 ? 0 : c] = __builtin_fmaf(h[c][j], h[c][j], sums[N == 1 ? 0 : c]);
           }
-      sum = row_total<GL>(sum, part, [](float x, float y) { return x + y; });
+      sum = row_total_of<GL>(sums, part, [](float x, float y) { return x + y; });
       mean = sum / (float)cols + __builtin_ldexpf(eps, -2 * k2);
     }
   }

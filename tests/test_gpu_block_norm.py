@@ -164,6 +164,21 @@ def test_in_place_and_batch_independent(A, cols):
         A.block_norm_mx(**t, residual_out=t["X"][:37])
 
 
+@pytest.mark.parametrize("cols,top", [(4096, 0), (4096, 5), (2080, 0), (1056, 3), (8192, 0)])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 70])
+def test_many_rows_as_one(A, cols, top, size):
+    """More rows than take one chunk a lane: each as by itself, bit for bit, squares beyond fp32's range or not."""
+    import torch
+    say(f"block_norm_mx many rows {cols} top {top} size {size}")
+    t, n = case(np.random.default_rng(8), 150, cols, "bf16", top, "f32", ("f16", "rows"))
+    t["X"].mul_(size)
+    ref = A.block_norm_mx(**t)
+    for i in (0, 77, 149):
+        one = {k: v[i:i + 1] if v.dim() == 2 and not (k == "X" and top) else v for k, v in t.items()}
+        for a, b in zip(A.block_norm_mx(**one), ref):
+            assert torch.equal(a.view(torch.uint8), b[i:i + 1].contiguous().view(torch.uint8))
+
+
 @pytest.mark.parametrize("cols", [64, 1056])
 def test_bad_rows_stay_alone(A, cols):
     """A row with a NaN is NaN, one with an infinity in its block's result too; the others are as without them."""

@@ -248,6 +248,8 @@ def test_block_norm_validation(A):
     for k in ("X", "r", "w", "ro", "codes", "scales"):
         assert n(**{k: None}) == A.AWQ_EINVAL
     assert n(pl=FAKE, sh=FAKE, top=2) == A.AWQ_EINVAL and "other tokens" in err(A)
+    for other in ("ld", "ld_r", "ld_ro"):  # residual_out is X and residual here
+        assert n(**{other: 72}) == A.AWQ_EINVAL and "row stride" in err(A)
     assert n(X=ODD) == A.AWQ_EALIGN and n(w=FAKE + 2, wdt=A.AWQ_F32) == A.AWQ_EALIGN and n(codes=FAKE + 4) == A.AWQ_EALIGN
     assert n(r=ODD) == A.AWQ_EALIGN and n(post=ODD) == A.AWQ_EALIGN and n(gate=FAKE + 2, gdt=A.AWQ_F32) == A.AWQ_EALIGN
     assert n(pl=FAKE + 2, sh=FAKE, top=2, ro=FAKE + 64) == A.AWQ_EALIGN
