@@ -9,7 +9,7 @@
 // read once: bound by memory, in one launch.  Lanes of a row as in rms_norm_mx:
 // a wave or a part of it up to 512 columns, else a block.  6001 x 4096 with a norm
 // and a gate 35.3 us (4.9 TB/s; a large copy 5.1), 4096 x 4096 with a sum of 4 rows
-// 39.5 us (5.5 TB/s), one row with a sum of 8 4.4 us.  What the rows in flight leave
+// 39.5 us (5.5 TB/s), one row with a sum of 8 4.6 us.  What the rows in flight leave
 // of registers decides: the kernel without the sum has 58, and 88 (38.9 us for the
 // first) with the sum's loads in it, so each has a kernel of its own; the weights'
 // loads ahead of X cost more registers than they gain.
@@ -101,8 +101,8 @@ __device__ __forceinline__ void squares(const float (&h)[CH][8], int lane, int l
       for (int j = 0; j < 8; ++j) sums[N == 1 ? 0 : c] = __builtin_fmaf(h[c][j], h[c][j], sums[N == 1 ? 0 : c]);
 }
 
-// FULL: every lane has CH chunks
-template <int DT, int FMT, int GL, int CH, bool FULL, bool SUM>
+// FULL: every lane has CH chunks.  HALVES: twice the lanes of CH = 2 have a chunk each, for the same results
+template <int DT, int FMT, int GL, int CH, bool FULL, bool SUM, bool HALVES>
 __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const BlockNormArgs a) {
   const int lanes = GL ? GL : (int)blockDim.x;
   const int lane = GL ? (int)threadIdx.x % (GL ? GL : 1) : (int)threadIdx.x;
@@ -110,9 +110,9 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const Bl
                          : (int64_t)blockIdx.x;
   const bool live = FULL || row < a.rows;
   const int cpr = FULL ? CH * lanes : live ? (int)(a.cols / 8) : 0;  // chunks of the row that there are
-  // The sums of two chunks are kept apart: a row's total is then the same with one chunk a lane, which few rows have.
+  // The sums of two chunks are kept apart and joined first, so that a row's total is the same with HALVES.
   constexpr int NS = GL == 0 && CH == 2 ? 2 : 1;
-  __shared__ float part[2][GL ? 1 : 16 * NS];
+  __shared__ float part[2][GL ? 1 : HALVES ? 16 + 256 : 16];
   float sums[NS];
   constexpr bool kEarly = CH < 4;  // what is added ahead of the sums, but for the longest rows, for want of registers
   uint4 res[CH];
@@ -132,7 +132,7 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const Bl
   auto get_norm = [&]() { each([&](int c, int64_t col) { norm[c] = load_ahead(a.norm, a.norm_dtype, col); }); };
   if (a.post != nullptr) {
     squares<CH, FULL>(h, lane, lanes, cpr, sums);
-    const float r = row_scale<GL, CH>(h, sums, live, lane, lanes, cpr, a.cols, a.eps, part[0]);
+    const float r = row_scale<GL, CH, HALVES>(h, sums, live, lane, lanes, cpr, a.cols, a.eps, part[0]);
     get_post();
 #pragma unroll
     for (int c = 0; c < CH; ++c)
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const Bl
       st_any(a.RO + row * a.ld_ro + col, pack8<DT>(h[c]));
     }
   squares<CH, FULL>(h, lane, lanes, cpr, sums);
-  const float r = row_scale<GL, CH>(h, sums, live, lane, lanes, cpr, a.cols, a.eps, part[1]);
+  const float r = row_scale<GL, CH, HALVES>(h, sums, live, lane, lanes, cpr, a.cols, a.eps, part[1]);
   get_norm();
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -185,22 +185,29 @@ __global__ __launch_bounds__(GL ? 256 : 1024) void block_norm_mx_kernel(const Bl
 template <int DT, int FMT, bool SUM>
 static void block_norm_launch(const BlockNormArgs& a, hipStream_t stream) {
   const int64_t cpr = a.cols / 8;
-  // Rows of 4096: up to 128 of them, latency counts and a lane takes one chunk (the sum of 8 rows: 1 row 4.4 us, with
-  // two chunks 5.0; 64 rows 4.9 and 5.6); more have two, for more rows in flight (256 rows 7.5, with one chunk 8.3;
-  // 6001 without a sum 35.8 and 42).
-  const bool few = a.rows <= 128;
 #define AWQ_NORM_W(GL, CH) \
-  block_norm_mx_kernel<DT, FMT, GL, CH, false, SUM><<<(unsigned)((a.rows + 256 / GL - 1) / (256 / GL)), 256, 0, stream>>>(a)
+  block_norm_mx_kernel<DT, FMT, GL, CH, false, SUM, false><<<(unsigned)((a.rows + 256 / GL - 1) / (256 / GL)), 256, 0, stream>>>(a)
+#define AWQ_NORM_2(FULL)                                                                                             \
+  block_norm_mx_kernel<DT, FMT, 0, 1, FULL, SUM, true><<<(unsigned)a.rows, (unsigned)(((cpr + 1) / 2 + 63) / 64 * 128), 0, \
+                                                         stream>>>(a)
 #define AWQ_NORM_B(CH, FULL)                                                                                         \
-  block_norm_mx_kernel<DT, FMT, 0, CH, FULL, SUM><<<(unsigned)a.rows, (unsigned)(((cpr + CH - 1) / CH + 63) / 64 * 64), 0, \
+  block_norm_mx_kernel<DT, FMT, 0, CH, FULL, SUM, false><<<(unsigned)a.rows, (unsigned)(((cpr + CH - 1) / CH + 63) / 64 * 64), 0, \
                                                stream>>>(a)
+  if constexpr (SUM) {
+    // Few rows: twice the lanes have twice the sum's loads in flight (4096 columns, the sum of 8 rows: 1 row 4.6 us, with
+    // two chunks a lane 5.3; 64 rows 6.3 both; without a sum nothing is gained).
+    if (a.rows <= 32 && cpr > 64 && cpr <= 512) {
+      if (cpr % 128 == 0) AWQ_NORM_2(true); else AWQ_NORM_2(false);
+      return;
+    }
+  }
   if (cpr <= 4) AWQ_NORM_W(4, 1);
   else if (cpr <= 8) AWQ_NORM_W(8, 1);
   else if (cpr <= 16) AWQ_NORM_W(16, 1);
   else if (cpr <= 32) AWQ_NORM_W(32, 1);
   else if (cpr <= 64) AWQ_NORM_W(32, 2);
-  else if (!few && cpr <= 512 && cpr % 128 == 0) AWQ_NORM_B(2, true);
-  else if (!few && cpr <= 512) AWQ_NORM_B(2, false);
+  else if (cpr <= 512 && cpr % 128 == 0) AWQ_NORM_B(2, true);
+  else if (cpr <= 512) AWQ_NORM_B(2, false);
   else if (cpr <= 1024 && cpr % 64 == 0) AWQ_NORM_B(1, true);
   else if (cpr <= 1024) AWQ_NORM_B(1, false);
   else if (cpr <= 2048 && cpr % 128 == 0) AWQ_NORM_B(2, true);
@@ -209,6 +216,7 @@ static void block_norm_launch(const BlockNormArgs& a, hipStream_t stream) {
   else AWQ_NORM_B(8, false);
 #undef AWQ_NORM_W
 #undef AWQ_NORM_B
+#undef AWQ_NORM_2
 }
 
 hipError_t launch_block_norm_mx(const BlockNormArgs& a, int dt, int fmt, hipStream_t stream) {

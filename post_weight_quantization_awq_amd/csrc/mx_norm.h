@@ -36,26 +36,23 @@ __device__ __forceinline__ float row_total(float v, float* part, F f) {
   }
 }
 
-// N values a lane, which count as N lanes: with GL = 0 the same result as of N times as many lanes with one each.
-template <int GL, int N, class F>
-__device__ __forceinline__ float row_total_of(const float (&v)[N], float* part, F f) {
-  if constexpr (N == 1) {
-    return row_total<GL>(v[0], part, f);
-  } else {
-    static_assert(GL == 0, "lanes of a wave have one value each");
-    const int wave = (int)threadIdx.x >> 6, nw = (int)blockDim.x >> 6;
+// The same for a block whose upper half has the second chunks: the result of half as many lanes that have two chunks
+// each and join theirs first.  part: 16 floats, and one for each lane of the upper half.
+template <class F>
+__device__ __forceinline__ float row_total_halves(float v, float* part, F f) {
+  const int half = (int)blockDim.x / 2, lane = (int)threadIdx.x;
+  if (lane >= half) part[16 + lane - half] = v;
+  __syncthreads();
+  if (lane < half) {  // whole waves
+    v = f(v, part[16 + lane]);
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
-      float x = v[c];
-#pragma unroll
-      for (int m = kWave / 2; m >= 1; m >>= 1) x = f(x, __shfl_xor(x, m, kWave));
-      if ((threadIdx.x & 63) == 0) part[c * nw + wave] = x;
-    }
-    __syncthreads();
-    float x = 0.0f;
-    for (int i = 0; i < N * nw; ++i) x = f(x, part[i]);
-    return x;
+    for (int m = kWave / 2; m >= 1; m >>= 1) v = f(v, __shfl_xor(v, m, kWave));
+    if ((lane & 63) == 0) part[lane >> 6] = v;
   }
+  __syncthreads();
+  v = 0.0f;
+  for (int i = 0; i < half / kWave; ++i) v = f(v, part[i]);
+  return v;
 }
 
 // Rows whose squares leave fp32's range: the mean is infinite, or so small that squares lost below the range count
@@ -65,13 +62,24 @@ __device__ __forceinline__ float row_total_of(const float (&v)[N], float* part, 
 constexpr float kNormLeast = 0x1p-100f;
 
 // 1 / sqrt(mean h^2 + eps) of a row whose lanes hold h and their sums of squares.  Where those leave fp32's range h
-// is scaled, and what is returned goes with the scaled h.  N sums a lane: of all its chunks, or of each.  part: 16 N
-// floats of LDS with GL = 0.
-template <int GL, int CH, int N>
+// is scaled, and what is returned goes with the scaled h.  N sums a lane: of all its chunks, or of each.  part: 16
+// floats of LDS with GL = 0, and with HALVES as there.
+template <int GL, int CH, bool HALVES = false, int N>
 __device__ __forceinline__ float row_scale(float (&h)[CH][8], float (&sums)[N], bool live, int lane, int lanes, int cpr,
                                            int64_t cols, float eps, float* part) {
   static_assert(N == 1 || N == CH, "a sum for all of the lane's chunks or for each");
-  float sum = row_total_of<GL>(sums, part, [](float x, float y) { return x + y; });
+  auto total = [&](float v, auto f) {
+    if constexpr (HALVES) return row_total_halves(v, part, f);
+    else return row_total<GL>(v, part, f);
+  };
+  auto add = [](float x, float y) { return x + y; };
+  auto joined = [&]() {
+    float v = sums[0];
+#pragma unroll
+    for (int c = 1; c < N; ++c) v += sums[c];
+    return v;
+  };
+  float sum = total(joined(), add);
   float mean = sum / (float)cols + eps;
   // the same for the whole row
   if (__builtin_expect(!(mean < HUGE_VALF) || (sum < kNormLeast && eps < kNormLeast), false)) {
@@ -82,7 +90,7 @@ __device__ __forceinline__ float row_scale(float (&h)[CH][8], float (&sums)[N], 
       if (live && lane + c * lanes < cpr)
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = max(top, __builtin_bit_cast(uint32_t, h[c][j]) & 0x7FFFFFFFu);
-    top = __builtin_bit_cast(uint32_t, row_total<GL>(__builtin_bit_cast(float, top), part, [](float x, float y) {
+    top = __builtin_bit_cast(uint32_t, total(__builtin_bit_cast(float, top), [](float x, float y) {
       return __builtin_bit_cast(float, max(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)));
     }));
     if (top < 0x7F800000u) {
@@ -99,7 +107,7 @@ __device__ __forceinline__ float row_scale(float (&h)[CH][8], float (&sums)[N], 
             h[c][j] = __builtin_ldexpf(h[c][j], -k2);
             sums[N == 1 ? 0 : c] = __builtin_fmaf(h[c][j], h[c][j], sums[N == 1 ? 0 : c]);
           }
-      sum = row_total_of<GL>(sums, part, [](float x, float y) { return x + y; });
+      sum = total(joined(), add);
       mean = sum / (float)cols + __builtin_ldexpf(eps, -2 * k2);
     }
   }

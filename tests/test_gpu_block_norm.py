@@ -164,7 +164,7 @@ def test_in_place_and_batch_independent(A, cols):
         A.block_norm_mx(**t, residual_out=t["X"][:37])
 
 
-@pytest.mark.parametrize("cols,top", [(4096, 0), (4096, 5), (2080, 0), (1056, 3), (8192, 0)])
+@pytest.mark.parametrize("cols,top", [(4096, 0), (4096, 5), (2080, 0), (2080, 2), (1056, 3), (544, 6), (8192, 0)])
 @pytest.mark.parametrize("size", [1.0, 2.0 ** 70])
 def test_many_rows_as_one(A, cols, top, size):
     """More rows than take one chunk a lane: each as by itself, bit for bit, squares beyond fp32's range or not."""
