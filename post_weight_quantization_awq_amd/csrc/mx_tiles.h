@@ -51,7 +51,7 @@ __host__ __device__ __forceinline__ StageSpan stage_span(int first, int rows, ui
   return StageSpan{(uint32_t)(left < kBigTile ? left : kBigTile) * row_bytes, left <= 0 ? 0 : off < last ? off : last};
 }
 
-// Tiles of 256 rows in groups: n_full with more than 128 rows, then n_half with fewer, which take half the time.  Each
+// Tiles of 256 rows in groups: n_full with more than 128 rows, then n_half with fewer, which take a little less.  Each
 // XCD has an equal share of both, the full ones first, and of each a contiguous range, walked in groups of group_m
 // tiles of rows.
 constexpr int kHalfTile = kBigTile / 2;
