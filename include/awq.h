@@ -561,10 +561,10 @@ awq_status awq_mx_linear(const void* a_codes, const uint8_t* a_scales, int32_t a
  * token with a NaN or +inf logit are NaN.
  * logits: fp16, bf16 or fp32 [T, ld], ld >= n_experts, aligned to its elements.
  * experts, places: int32 [T, top]; weights: fp32 [T, top]; rows: int32 [T top]; offsets:
- * int32 [n_experts + 1].  1 <= top <= min(n_experts, 32), n_experts <= 1024, T <= 2^24,
- * T top < 2^31 (AWQ_ESHAPE).  T = 0 writes offsets alone (zeros).  ws:
- * awq_moe_route_workspace bytes (0 up to 64 tokens; ws may then be NULL), 256-byte
- * aligned, for this call alone while it runs.  Deterministic.
+ * int32 [n_experts + 1].  1 <= top <= min(n_experts, 32), n_experts <= 1024, T <= 2^24
+ * (AWQ_ESHAPE).  T = 0 writes offsets alone (zeros).  ws: awq_moe_route_workspace
+ * bytes (0 up to 64 tokens; ws may then be NULL), 256-byte aligned, for this call
+ * alone while it runs.  Deterministic.
  * ------------------------------------------------------------------------- */
 awq_status awq_moe_route_workspace(int64_t T, int32_t n_experts, size_t* bytes /* [host] */);
 awq_status awq_moe_route(const void* logits, int32_t dtype, int64_t T, int32_t n_experts, int64_t ld, int32_t top,

@@ -971,7 +971,6 @@ awq_status awq_moe_route(const void* logits, int32_t dtype, int64_t T, int32_t n
   if (awq_status st = route_shape(T, n_experts)) return st;
   if (top < 1 || top > n_experts || top > kMostTop)
     return fail(AWQ_ESHAPE, "top %d not in [1, min(%d, %d)]", top, n_experts, kMostTop);
-  if (T * top >= (int64_t)1 << 31) return fail(AWQ_ESHAPE, "T top = %lld >= 2^31", (long long)(T * top));
   if (ld < n_experts) return fail(AWQ_ESHAPE, "ld %lld < n_experts %d", (long long)ld, n_experts);
   if (!offsets || (T > 0 && (!logits || !experts || !weights || !rows || !places)))
     return fail(AWQ_EINVAL, "logits / experts / weights / rows / places / offsets is NULL");
