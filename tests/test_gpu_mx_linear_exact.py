@@ -12,7 +12,7 @@ from tests._util import say
 from tests.linear_shapes import QUANTIZED
 from tests.mx_shapes import PRODUCTS
 from tests.test_gpu_mx import A, tdt  # noqa: F401
-from tests.test_gpu_mx_exact import exact_product
+from tests.test_gpu_mx_exact import exact_product, operand
 
 pytestmark = pytest.mark.gpu
 KINDS = ["f16", "bf16", "f32"]
@@ -163,3 +163,58 @@ def test_rows_past_the_first_launch(A, fmt):
         codes, scales = A.mx_linear(*a, *w, bias=bias, residual=R, fmt=out_fmt)
         want = quantize(finish(y, bias, None, r), out_fmt)
         assert torch.equal(codes.view(torch.uint8), want[0]) and torch.equal(scales.view(torch.uint8), want[1])
+
+
+@pytest.mark.parametrize("M,N,K,fmt", [(1024, 16032, 768, "fp8"), (1500, 8224, 1184, "fp4"), (200, 2080, 12288, "fp8")])
+def test_workspaces_in_graphs_and_on_two_streams(A, M, N, K, fmt):
+    """Forms that use their workspace (laid out scales, K ranges): two plans captured and replayed at once on new
+    inputs, with eager calls between the replays, then two streams at once."""
+    import torch
+    say(f"mx_linear exact graphs {M}x{N}x{K} {fmt}")
+    g = torch.Generator(device="cuda").manual_seed(K)
+    assert A.mx_linear_workspace_bytes(fmt, M, N, K) > 0
+    bias = [eighths(g, "f32", N) for _ in range(2)]
+    R = [eighths(g, "f16", M, N) for _ in range(2)]
+    ops = [exact_product(M, N, K, fmt, "f16", i) for i in (1, 2)]
+    a = [tuple(t.clone() for t in o[0]) for o in ops]
+    w = [o[1] for o in ops]
+    plans = [A.MxLinearPlan(*a[0], *w[0], bias=bias[0], activation="relu", residual=R[0]),
+             A.MxLinearPlan(*a[1], *w[1], bias=bias[1], residual=R[1], fmt="fp8")]
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in plans]
+    for p, graph in zip(plans, graphs):
+        with torch.cuda.graph(graph):
+            p.run()
+    streams = [torch.cuda.Stream() for _ in graphs]
+
+    def check():
+        y = [x[2] @ v for x, v in zip(now, exact)]
+        assert torch.equal(plans[0].out, finish(y[0], bias[0], "relu", R[0]).half())
+        want = quantize(finish(y[1], bias[1], None, R[1]), "fp8")
+        assert all(torch.equal(p.view(torch.uint8), q) for p, q in zip(plans[1].out, want))
+
+    exact = [A.mx_dequant(*v).double().t().contiguous() for v in w]
+    for i in range(3):
+        now = []
+        for j in range(2):
+            codes, scales, _ = new = operand(g, M, K, fmt, 15, min(1.0, 60 / K))
+            now.append(new)
+            a[j][0].view(torch.uint8).copy_(codes.view(torch.uint8))
+            a[j][1].view(torch.uint8).copy_(scales.view(torch.uint8))
+            R[j].copy_(eighths(g, "f16", M, N))
+        for t in (plans[0].out, *plans[1].out):
+            t.view(torch.uint8).fill_(0xA5)
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        check()
+        A.mx_linear(*a[0], *w[0], bias=bias[0])
+    apart = [A.MxLinearPlan(*a[j], *w[j], bias=bias[j], residual=R[j], stream=s) for j, s in enumerate(streams)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = [p.run() for p in apart]
+    torch.cuda.synchronize()
+    for j in range(2):
+        assert torch.equal(got[j], finish(now[j][2] @ exact[j], bias[j], None, R[j]).half())
