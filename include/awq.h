@@ -526,7 +526,8 @@ awq_status awq_mx_matmul(const void* a_codes, const uint8_t* a_scales, int32_t a
  * act: AWQ_ACT_NONE; AWQ_ACT_RELU, max(x, 0); AWQ_ACT_SILU, x / (1 + exp(-x));
  * AWQ_ACT_GELU, x (1 + erf(x / sqrt 2)) / 2; AWQ_ACT_GELU_TANH, x (1 + tanh(sqrt(2 / pi)
  * (x + 0.044715 x^3))) / 2.  Each is within 2^-17 of its value (GELU 2^-16, GELU_TANH 2^-15)
- * down to fp32's smallest normal number, for any argument; NaN stays NaN.
+ * down to fp32's smallest normal number, for any finite argument and +inf; NaN stays NaN.
+ * SiLU and both GELUs of -inf are NaN, as their formulas' -inf / inf and -inf * 0 are.
  * bias: [N] of bias_dtype (fp16, bf16 or fp32), or NULL.  residual: [M, ld_r] of
  * r_dtype (fp16, bf16 or fp32), ld_r >= N, or NULL; it may be Y itself (same dtype and
  * row stride), else the buffers do not overlap.  Operands, sizes, alignment,

@@ -8,9 +8,9 @@
 // one token 16.4 us (4.4 TB/s with the launch), 64 groups of 4096 x 2048 for 512 rows
 // 63 us (4.6).  Large groups are bound by the matrix cores and by tiles that no group fills:
 // 16384 rows of 32 uneven groups of 4096 x 4096 276 us (2.0 PFLOP/s; one group of all
-// 209, the plain product 195-203, and reading A through `rows` adds 13): a group's
-// last tile of fewer than 128 rows takes 0.95 of a full one, since its stages wait for
-// their loads either way.
+// 209, the plain product 195-203, and reading A through `rows` adds 13), in 4 bits
+// 204-220 us (2.6 PFLOP/s): a group's last tile of fewer than 128 rows takes 0.95 of a full
+// one, since its stages wait for their loads either way.
 #include <algorithm>
 
 #include "awq_launch.h"
