@@ -136,3 +136,32 @@ def test_tiles_past_the_first_launch(A, M, E, N, K, fmt, dtype):
     say(f"mx_matmul_grouped exact launches {M} rows {E} groups {N}x{K} {fmt}")
     for gather in (True, False):
         check(A, M, E, N, K, fmt, dtype, gather, 5, 37, N, "even" if gather else "skewed")
+
+
+@pytest.mark.parametrize("how", ["even", "skewed"])
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("M,E,N,K", [(5000, 70, 1030, 544), (9000, 1024, 1030, 544), (20000, 130, 520, 544),
+                                     (30000, 70, 1030, 512), (60000, 200, 1030, 544)])
+def test_more_groups_than_lanes(A, M, E, N, K, fmt, how):
+    """More groups than a wave's lanes hold at once, on the tiles of 32 to 256 rows."""
+    say(f"mx_matmul_grouped exact {how} {M} rows {E} groups {N}x{K} {fmt}")
+    for gather in (True, False):
+        check(A, M, E, N, K, fmt, "f16", gather, 11, 300, N + 1, how)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("M,E,N,K", [(5000, 70, 130, 544), (60000, 200, 1030, 544)])
+def test_empty_groups_between_full_ones(A, M, E, N, K, fmt):
+    """All rows in the last groups of each 64, and in the last group of all."""
+    import torch
+    say(f"mx_matmul_grouped exact sparse {M} rows {E} groups {N}x{K} {fmt}")
+    a, w = operands(M, E, N, K, fmt, "f16", M)
+    for full in ([63], [E - 1], [63, 64, E - 1], [0, E - 1]):
+        counts = np.zeros(E, np.int64)
+        counts[full] = M // len(full)
+        counts[full[-1]] += M - counts.sum()
+        cuts = np.concatenate([[0], np.cumsum(counts)])
+        Y = A.mx_matmul_grouped(*a[:2], *w[:2], torch.from_numpy(cuts.astype(np.int32)).cuda(), out_dtype=torch.float16)
+        for e in full:
+            s = slice(int(cuts[e]), int(cuts[e + 1]))
+            assert torch.equal(Y[s], (a[2][s] @ w[2][e].t().contiguous()).half()), (full, e)

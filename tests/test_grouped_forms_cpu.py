@@ -17,6 +17,14 @@ def test_shape_takes_the_form_it_is_there_for(tiles, M, E, N, K, fmt, form):  # 
     assert form_of(tiles, M, E, N, K, fmt) == form
 
 
+def test_many_groups_take_every_tile(tiles):  # noqa: F811
+    """The shapes of more groups than a wave has lanes."""
+    got = {form_of(tiles, M, E, N, K, fmt).split(",")[0] for fmt in ("fp8", "fp4") for M, E, N, K in
+           ((5000, 70, 1030, 544), (9000, 1024, 1030, 544), (20000, 130, 520, 544), (30000, 70, 1030, 512),
+            (60000, 200, 1030, 544))}
+    assert got == {"32", "64", "128", "256"}
+
+
 def test_offsets_that_descend_fit(tiles):  # noqa: F811
     """The offsets that descend in the exact test have no more tiles than a launch has places for, whatever the tile."""
     for M, E in ((500, 3), (61, 8), (900, 5), (2000, 6), (3000, 3), (4096, 7)):
