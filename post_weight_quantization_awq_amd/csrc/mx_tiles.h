@@ -182,7 +182,7 @@ inline int64_t group_tiles_most(int64_t M, int n_groups, int tile) {
 // rows x 32 outputs; tiles of 32 rows have 128 outputs, the others as many as rows.  The estimates (us) are fitted to
 // measurements of 8 to 128 groups, N and K of 1000 to 4096, at 0.1 to 512 rows a group, with other weights from run
 // to run.  Of 222 points the tile that they choose is 1.7% slower than the best one in the mean, more than 8% at 14:
-// most at about 16 rows a group of 2048 x 4096 and more, where uneven groups have more tiles of 32 rows than are counted
+// the worst at about 16 rows a group, where uneven groups have more tiles of 32 rows than are counted
 // (8 groups of 4096 x 4096, 16 rows each: 21.3 us, 15.9 on tiles of 64; 64 of 2048 x 4096, 16 rows, 4 bits: 77.9, 64.2
 // on tiles of 128).  E.g. (8 bits; few rows / 32 / 64 / 128 /
 // 256) 64 groups of 4096 x 4096, 1 row each: 76 / 82 / 86 / 92 / -; 8: 129 / 118 / 139 / 132 / -; 32: 251 / 166 / 179 / 153
